@@ -8,6 +8,11 @@ the names of the C entry points declared in ``include/ep.h``.
 There is no fallback: if ``libep.so`` is missing or cannot be loaded, every
 call raises ``EpLibraryMissing``.  Build it with
 ``python -m bulk_async_tensor_amd.build``.
+
+The expert side (``include/ep_expert.h``: the 8-bit dispatch, the experts'
+8-bit products, the gradients of combine and dispatch) follows the same
+pattern; its calls take tensors of one device, which need not be the current
+one.
 """
 
 import ctypes
@@ -27,12 +32,13 @@ EP_STATUS_DUPLICATE_EXPERT = 2
 EP_MAX_TOPK = 32
 EP_MAX_EXPERTS = 1024
 EP_MAX_ENTRIES = (1 << 31) - 1 - (1 << 22)
+EP_FP8_BLOCK = 128
 
 VARIANTS = ("auto", "vgpr", "vgpr2", "lds1", "lds2", "vgpr_cached", "phase", "lds3", "pc", "vgpr_wg")
 
 _c_int, _c_i64, _c_sz, _p = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
 
-# name -> (restype, argtypes), mirroring include/ep.h
+# name -> (restype, argtypes), mirroring include/ep.h and include/ep_expert.h
 _SIGNATURES = {
     "ep_set_num_cus": (_c_int, [_c_int]),
     "ep_get_num_cus": (_c_int, []),
@@ -58,6 +64,11 @@ _SIGNATURES = {
     "ep_mfma_probe": (_c_int, [_c_int, _c_int, _p, _p]),
     "ep_stream_create_cu_masked": (_c_int, [ctypes.POINTER(ctypes.c_uint32), _c_int, ctypes.POINTER(_p)]),
     "ep_stream_destroy": (_c_int, [_p]),
+    "ep_dispatch_fp8": (_c_int, [_p, _c_int, _c_int, _p, _c_int, _p, _p, _c_i64, _p]),
+    "ep_grouped_gemm_fp8": (_c_int, [_p, _p, _c_i64, _c_int, _p, _c_int, _p, _p, _c_int, _p, _p]),
+    "ep_grouped_swiglu_fp8": (_c_int, [_p, _p, _c_i64, _c_int, _p, _c_int, _p, _p, _c_int, _p, _p, _p]),
+    "ep_combine_backward": (_c_int, [_p, _p, _c_i64, _c_int, _p, _p, _c_int, _c_int, _p, _p, _p]),
+    "ep_dispatch_backward": (_c_int, [_p, _c_i64, _c_int, _p, _c_int, _c_int, _p, _p]),
 }
 
 
@@ -370,6 +381,174 @@ def ep_combine_reduce(y, src_token, dest_row, topk_w, out, workspace=None, strea
                                    _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                    _stream(stream, out)), "ep_combine_reduce")
     return out
+
+
+# ------------------------------------------------------------------ expert side
+def _blocks(n):
+    return (n + EP_FP8_BLOCK - 1) // EP_FP8_BLOCK
+
+
+def _one_device(what, first, *others):
+    """The device index that every tensor given (None: not given) is on."""
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{what}: the tensors are on different devices")
+    return dev
+
+
+def _call_on(dev, stream, name, args):
+    """Calls entry point `name` with the current device set to `dev`, on the
+    given stream or on the current stream of that device."""
+    import torch
+
+    fn = getattr(_lib or lib(), name)
+    if stream is not None:
+        if stream.device.index is not None and stream.device.index != dev:
+            raise ValueError(f"{name}: the stream belongs to another device than the tensors")
+        handle = stream.cuda_stream
+    else:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    if torch.cuda.current_device() == dev:
+        return _check(fn(*args, handle), name)
+    with torch.cuda.device(dev):
+        return _check(fn(*args, handle), name)
+
+
+def ep_dispatch_fp8(x, dest_row, recv_q, recv_scale, stream=None):
+    """recv_q[dest_row[t, j]], recv_scale[dest_row[t, j]] = x[t] in e4m3 with one
+    float32 scale for each 128 values: x [T, H] bf16, dest_row [T, k] int32,
+    recv_q [R, H] float8_e4m3fn, recv_scale [R, ceil(H / 128)] float32.
+    Returns (recv_q, recv_scale)."""
+    import torch
+
+    _device_tensor(x, "x", torch.bfloat16)
+    _device_tensor(dest_row, "dest_row", torch.int32)
+    _device_tensor(recv_q, "recv_q", torch.float8_e4m3fn)
+    _device_tensor(recv_scale, "recv_scale", torch.float32)
+    if x.dim() != 2 or dest_row.dim() != 2 or dest_row.shape[0] != x.shape[0]:
+        raise ValueError("x must be [T, H] and dest_row [T, k]")
+    T, H = x.shape
+    if recv_q.dim() != 2 or recv_q.shape[1] != H or tuple(recv_scale.shape) != (recv_q.shape[0], _blocks(H)):
+        raise ValueError("recv_q must be [R, H] and recv_scale [R, ceil(H / 128)]")
+    dev = _one_device("ep_dispatch_fp8", x, dest_row, recv_q, recv_scale)
+    _call_on(dev, stream, "ep_dispatch_fp8", (x.data_ptr(), T, H, dest_row.data_ptr(), dest_row.shape[1],
+                                              recv_q.data_ptr(), recv_scale.data_ptr(), recv_q.shape[0]))
+    return recv_q, recv_scale
+
+
+def _grouped(what, a, a_scale, offsets, b, b_scale):
+    """Checks the operands of an expert product; (rows, K, E, weight rows)."""
+    import torch
+
+    _device_tensor(a, "a", torch.float8_e4m3fn)
+    _device_tensor(a_scale, "a_scale", torch.float32)
+    _device_tensor(offsets, "offsets", torch.int32)
+    _device_tensor(b, "b", torch.float8_e4m3fn)
+    _device_tensor(b_scale, "b_scale", torch.float32)
+    if a.dim() != 2 or b.dim() != 3 or b.shape[2] != a.shape[1]:
+        raise ValueError(f"{what}: a must be [rows, K] and b [E, N, K]")
+    rows, K = a.shape
+    E, N, _ = b.shape
+    if tuple(a_scale.shape) != (rows, _blocks(K)):
+        raise ValueError(f"{what}: a_scale must be [rows, ceil(K / 128)] = [{rows}, {_blocks(K)}]")
+    if tuple(b_scale.shape) != (E, _blocks(N), _blocks(K)):
+        raise ValueError(f"{what}: b_scale must be [E, ceil(N / 128), ceil(K / 128)] = [{E}, {_blocks(N)}, {_blocks(K)}]")
+    if offsets.dim() != 1 or offsets.shape[0] != E + 1:
+        raise ValueError(f"{what}: offsets must be [E + 1] = [{E + 1}]")
+    return rows, K, E, N
+
+
+def ep_grouped_gemm_fp8(a, a_scale, offsets, b, b_scale, y, stream=None):
+    """y[r] = bf16(a[r] @ b[e]^T) for the rows offsets[e] <= r < offsets[e + 1] of
+    each expert e: a [rows, K] and b [E, N, K] float8_e4m3fn, their float32
+    scales [rows, ceil(K / 128)] and [E, ceil(N / 128), ceil(K / 128)], offsets
+    [E + 1] int32 from ep_layout, y [rows, N] bf16.  Returns y."""
+    import torch
+
+    rows, K, E, N = _grouped("ep_grouped_gemm_fp8", a, a_scale, offsets, b, b_scale)
+    _device_tensor(y, "y", torch.bfloat16)
+    if tuple(y.shape) != (rows, N):
+        raise ValueError(f"y must be [rows, N] = [{rows}, {N}]")
+    dev = _one_device("ep_grouped_gemm_fp8", a, a_scale, offsets, b, b_scale, y)
+    _call_on(dev, stream, "ep_grouped_gemm_fp8", (a.data_ptr(), a_scale.data_ptr(), rows, K, offsets.data_ptr(), E,
+                                                  b.data_ptr(), b_scale.data_ptr(), N, y.data_ptr()))
+    return y
+
+
+def ep_grouped_swiglu_fp8(a, a_scale, offsets, b, b_scale, out_q, out_scale, stream=None):
+    """SiLU(gate) * up of each expert's gate and up product, in e4m3 with block
+    scales: operands as for ep_grouped_gemm_fp8 with b [E, 2 I, K] (I gate rows,
+    then I up rows), out_q [rows, I] float8_e4m3fn, out_scale
+    [rows, ceil(I / 128)] float32.  Returns (out_q, out_scale)."""
+    import torch
+
+    rows, K, E, N = _grouped("ep_grouped_swiglu_fp8", a, a_scale, offsets, b, b_scale)
+    if N % 2:
+        raise ValueError("ep_grouped_swiglu_fp8: b must hold as many gate as up rows")
+    I = N // 2
+    _device_tensor(out_q, "out_q", torch.float8_e4m3fn)
+    _device_tensor(out_scale, "out_scale", torch.float32)
+    if tuple(out_q.shape) != (rows, I) or tuple(out_scale.shape) != (rows, _blocks(I)):
+        raise ValueError(f"out_q must be [rows, I] = [{rows}, {I}] and out_scale [rows, ceil(I / 128)]")
+    dev = _one_device("ep_grouped_swiglu_fp8", a, a_scale, offsets, b, b_scale, out_q, out_scale)
+    _call_on(dev, stream, "ep_grouped_swiglu_fp8",
+             (a.data_ptr(), a_scale.data_ptr(), rows, K, offsets.data_ptr(), E, b.data_ptr(), b_scale.data_ptr(), I,
+              out_q.data_ptr(), out_scale.data_ptr()))
+    return out_q, out_scale
+
+
+def ep_combine_backward(dout, y, dest_row, topk_w, dy, dw, stream=None):
+    """The gradient of ep_combine: dy[dest_row[t, j]] = bf16(topk_w[t, j] * dout[t])
+    and dw[t, j] = <dout[t], y[dest_row[t, j]]>, for dout [T, H] and y, dy
+    [R, H] bf16, dest_row [T, k] int32, topk_w and dw [T, k] float32.  dy or dw
+    may be None (not wanted); y may be None without dw, topk_w without dy.
+    Returns (dy, dw)."""
+    import torch
+
+    _device_tensor(dout, "dout", torch.bfloat16)
+    _device_tensor(dest_row, "dest_row", torch.int32)
+    if dout.dim() != 2 or dest_row.dim() != 2 or dest_row.shape[0] != dout.shape[0]:
+        raise ValueError("dout must be [T, H] and dest_row [T, k]")
+    T, H = dout.shape
+    k = dest_row.shape[1]
+    rows = None
+    for t, name in ((y, "y"), (dy, "dy")):
+        if t is not None:
+            _device_tensor(t, name, torch.bfloat16)
+            if t.dim() != 2 or t.shape[1] != H or (rows is not None and t.shape[0] != rows):
+                raise ValueError(f"{name} must be [R, H]")
+            rows = t.shape[0]
+    for t, name in ((topk_w, "topk_w"), (dw, "dw")):
+        if t is not None:
+            _device_tensor(t, name, torch.float32)
+            if tuple(t.shape) != (T, k):
+                raise ValueError(f"{name} must be [T, k]")
+    if rows is None:
+        raise ValueError("ep_combine_backward needs y or dy")
+    dev = _one_device("ep_combine_backward", dout, y, dest_row, topk_w, dy, dw)
+    _call_on(dev, stream, "ep_combine_backward", (dout.data_ptr(), _ptr(y), rows, H, dest_row.data_ptr(), _ptr(topk_w),
+                                                  T, k, _ptr(dy), _ptr(dw)))
+    return dy, dw
+
+
+def ep_dispatch_backward(drecv, dest_row, dx, stream=None):
+    """The gradient of ep_dispatch: dx[t] = bf16(sum_j drecv[dest_row[t, j]]) for
+    drecv [R, H] and dx [T, H] bf16, dest_row [T, k] int32.  Returns dx."""
+    import torch
+
+    _device_tensor(drecv, "drecv", torch.bfloat16)
+    _device_tensor(dest_row, "dest_row", torch.int32)
+    _device_tensor(dx, "dx", torch.bfloat16)
+    if dx.dim() != 2 or dest_row.dim() != 2 or dest_row.shape[0] != dx.shape[0]:
+        raise ValueError("dx must be [T, H] and dest_row [T, k]")
+    T, H = dx.shape
+    if drecv.dim() != 2 or drecv.shape[1] != H:
+        raise ValueError("drecv must be [R, H]")
+    dev = _one_device("ep_dispatch_backward", drecv, dest_row, dx)
+    _call_on(dev, stream, "ep_dispatch_backward", (drecv.data_ptr(), drecv.shape[0], H, dest_row.data_ptr(), T,
+                                                   dest_row.shape[1], dx.data_ptr()))
+    return dx
 
 
 # ------------------------------------------------------------------ probes

@@ -13,6 +13,7 @@
 #include <utility>
 
 #include "ep.h"
+#include "ep_host.hpp"
 #include "ep_internal.hpp"
 
 static_assert(EP_MAX_TOPK == ep::kMaxK, "the kernels' largest k is the ABI's");
@@ -23,6 +24,10 @@ thread_local char g_err[512] = "";
 std::atomic<int> g_num_cus{-1};  // -1: not read from the environment yet
 std::atomic<int> g_variant{static_cast<int>(ep::Variant::Auto)};
 std::atomic<int> g_slab{0};
+
+}  // namespace
+
+namespace ep {
 
 int fail(int code, const char* fmt, ...) {
   va_list ap;
@@ -36,7 +41,16 @@ int hip_fail(hipError_t e, const char* what) {
   return fail(EP_ERR_HIP, "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+}  // namespace ep
+
+using ep::aligned;
+using ep::check_common;
+using ep::check_rows;
+using ep::current_device;
+using ep::fail;
+using ep::hip_fail;
+
+namespace {
 
 int num_cus_setting() {
   int v = g_num_cus.load();
@@ -83,6 +97,10 @@ void apply_stream_mask(hipStream_t stream, ep::Budget* b) {
   if (n > 0 && n < b->device_cus) b->device_cus = n;
 }
 
+}  // namespace
+
+namespace ep {
+
 // Device of the calling thread, checked once: gfx950 and its CU count; then
 // the CU count that `stream` may use.
 int current_device(ep::Budget* b, void* stream) {
@@ -121,7 +139,7 @@ int check_common(int T, int k, int H_or_E, const char* what) {
 // Rows of H elements (T token rows or recv_rows receive rows): their count
 // in 512-element slabs, the finest slab a kernel runs, must stay within
 // EP_MAX_ENTRIES (unit counters are 32-bit).
-int check_slabs(int64_t rows, int H, const char* name, const char* what) {
+static int check_slabs(int64_t rows, int H, const char* name, const char* what) {
   const int64_t slabs = rows * ((H + 511) / 512);
   if (slabs > EP_MAX_ENTRIES)
     return fail(EP_ERR_INVALID_ARG, "%s: %s * ceil(H / 512) = %lld exceeds EP_MAX_ENTRIES", what, name,
@@ -137,6 +155,10 @@ int check_rows(int H, int64_t recv_rows, int T, const char* what) {
   if (rc) return rc;
   return T > 0 ? check_slabs(T, H, "T", what) : EP_OK;
 }
+
+}  // namespace ep
+
+namespace {
 
 // Scratch of ep_layout_noalloc: the (chunk, expert) count table and the
 // per-chunk status words of the two- and three-launch layout paths, in a

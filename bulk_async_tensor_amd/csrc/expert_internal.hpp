@@ -1,0 +1,40 @@
+// Host-side interfaces between the expert side's C ABI (expert_api.hip) and
+// its kernel files.
+#pragma once
+
+#include "ep_internal.hpp"
+
+namespace ep {
+
+constexpr int kScaleBlock = 128;  // values that share a scale (the ABI's EP_FP8_BLOCK)
+inline __host__ __device__ int scale_blocks(int n) { return (n + kScaleBlock - 1) / kScaleBlock; }
+
+// ---- dispatch_fp8.hip
+hipError_t launch_dispatch_fp8(const Budget& b, const void* x, int T, int H, const int32_t* dest_row, int k,
+                               void* recv_q, float* recv_scale, int64_t recv_rows, hipStream_t stream);
+
+// ---- grouped_fp8.hip: swiglu = false: N weight rows, y is bf16 [rows, N];
+// swiglu = true: N = 2 I weight rows, y is e4m3 [rows, I] and y_scale its scales.
+struct GroupedArgs {
+  const void* a;
+  const float* a_scale;
+  int64_t rows;
+  int K;
+  const int32_t* offsets;
+  int E;
+  const void* b;
+  const float* b_scale;
+  int N;
+  void* y;
+  float* y_scale;
+};
+hipError_t launch_grouped_fp8(const Budget& b, const GroupedArgs& g, bool swiglu, hipStream_t stream);
+
+// ---- backward.hip
+hipError_t launch_combine_backward(const Budget& b, const void* dout, const void* y, int64_t recv_rows, int H,
+                                   const int32_t* dest_row, const float* w, int T, int k, void* dy, float* dw,
+                                   hipStream_t stream);
+hipError_t launch_dispatch_backward(const Budget& b, const void* drecv, int64_t recv_rows, int H,
+                                    const int32_t* dest_row, int T, int k, void* dx, hipStream_t stream);
+
+}  // namespace ep

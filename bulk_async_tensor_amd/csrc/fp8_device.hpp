@@ -1,0 +1,42 @@
+// 8-bit (e4m3, OCP encoding) values with a float32 scale for each block of
+// 128: conversion, the scale rule and the matrix-core product, shared by the
+// quantising dispatch and the experts' products.
+#pragma once
+
+#include "ep_device.hpp"
+
+namespace ep {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kE4m3Max = 448.0f;
+// Block maxima below this are taken as this, so that a scale and its inverse
+// stay normal numbers (448 / 2^-100 < 2^109) and no scale is zero.
+constexpr float kAmaxFloor = 0x1p-100f;
+
+// The block's scale and the factor that takes its values to [-448, 448]: two
+// correctly rounded float32 quotients.  x * inv exceeds 448 by at most one
+// rounding (448 (1 + 2^-23)), far below 464, where e4m3 would overflow.
+__device__ __forceinline__ float block_scale(float amax) { return amax / kE4m3Max; }
+__device__ __forceinline__ float block_inverse(float amax) { return kE4m3Max / amax; }
+
+// Four float32 -> four e4m3 in a dword, round to nearest even, NaN stays NaN:
+// the hardware conversion v_cvt_pk_fp8_f32 (OCP e4m3 on gfx950).
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+}
+
+// 16 x 16 product of 16 rows and 16 columns of 128 e4m3 values, float32 sums,
+// from +0 (v_mfma_f32_16x16x128_f8f6f4, no hardware scales).  Lane l holds 32
+// values of row (column) l % 16: those of its quarter l / 16, in an order that
+// only has to be the same on both sides.  Lane l's result i is row
+// 4 * (l / 16) + i, column l % 16.
+__device__ __forceinline__ f32x4 mfma_e4m3(i32x8 a, i32x8 b) {
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
+}
+
+}  // namespace ep

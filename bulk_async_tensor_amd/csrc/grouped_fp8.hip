@@ -1,0 +1,209 @@
+// The experts' 8-bit products with block scales (ep_grouped_gemm_fp8 and
+// ep_grouped_swiglu_fp8):
+//
+//   p[r, n] = sum_b sa[r, b] sb[e, n / 128, b] sum_{i in block b} a[r, i] w[e, n, i]
+//
+// for the rows r that the layout gives expert e.  The matrix-core instruction
+// takes 16 weight rows against 16 token rows over one whole block of 128, so
+// each result is one block's inner sum; it is then multiplied by the two
+// scales and added in float32.  Weights are the A operand and tokens the B
+// operand: a lane's results then belong to ONE token (its column) and four
+// adjacent weight rows, so the lane needs one token scale, and the block's
+// weight scale is the same for the whole tile.
+#include "expert_internal.hpp"
+#include "fp8_device.hpp"
+
+namespace ep {
+
+namespace {
+
+// A workgroup's rows: expert e, receive rows [r0, r1).
+struct RowTile {
+  int e;
+  int64_t r0, r1;
+};
+
+// Finds tile number `idx` of the experts' rows cut into tiles of BM (expert by
+// expert; an expert's last tile may be shorter).  False past the last one.
+// Every lane of the wave takes part.  Offsets are clamped to [0, rows].
+template <int BM>
+__device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, int E, int64_t rows, int64_t idx,
+                                          int lane, RowTile* out) {
+  int64_t before = 0;
+  for (int e0 = 0; e0 < E; e0 += kWave) {
+    const int e = e0 + lane;
+    int64_t lo = 0, hi = 0;
+    if (e < E) {
+      lo = offsets[e];
+      hi = offsets[e + 1];
+      lo = lo < 0 ? 0 : lo > rows ? rows : lo;
+      hi = hi < lo ? lo : hi > rows ? rows : hi;
+    }
+    const int n = (int)((hi - lo + BM - 1) / BM);
+    const int incl = wave_incl_scan(n, lane);
+    const uint64_t past = ballot(before + incl > idx);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      const int first = __builtin_amdgcn_readlane(incl - n, l);
+      out->e = e0 + l;
+      out->r0 = (int64_t)__builtin_amdgcn_readlane((int)lo, l) + (idx - before - first) * BM;
+      const int64_t end = __builtin_amdgcn_readlane((int)hi, l);
+      out->r1 = out->r0 + BM < end ? out->r0 + BM : end;
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(incl, kWave - 1);
+  }
+  return false;
+}
+
+constexpr int kNarrowWaves = 8;
+constexpr int kNarrowTiles = 4;               // token tiles of 16 per workgroup
+constexpr int kNarrowRows = 16 * kNarrowTiles;
+constexpr int kNarrowCols = 128;              // swiglu: output columns per workgroup (256 weight rows)
+
+// Few rows per expert: each wave streams two tiles of 16 weight rows from
+// memory straight into the matrix cores against up to 64 token rows.  swiglu:
+// the two tiles are the gate and the up rows of the same 16 outputs.
+template <bool SWIGLU>
+__global__ __launch_bounds__(kNarrowWaves * kWave) void grouped_narrow_kernel(GroupedArgs g, int units_n) {
+  __shared__ float s_max[kNarrowWaves][kNarrowRows];
+  const int lane = lane_id();
+  const int wave = wave_in_group();
+  const int col = lane & 15, quad = lane >> 4;
+  const int K = g.K, N = g.N, KB = scale_blocks(K);
+  const int outs = SWIGLU ? N / 2 : N;
+  const uint8_t* a = static_cast<const uint8_t*>(g.a);
+  const uint8_t* b = static_cast<const uint8_t*>(g.b);
+  for (int64_t u = blockIdx.x;; u += gridDim.x) {
+    RowTile tile;
+    if (!find_tile<kNarrowRows>(g.offsets, g.E, g.rows, u / units_n, lane, &tile)) break;
+    const int n0 = (int)(u % units_n) * (SWIGLU ? kNarrowCols : 2 * kNarrowCols) + wave * 16;
+    const int nt = (int)((tile.r1 - tile.r0 + 15) / 16);
+    int base[2];  // first weight row of each tile
+    base[0] = n0;
+    base[1] = SWIGLU ? outs + n0 : n0 + kNarrowCols;
+    f32x4 acc[2][kNarrowTiles] = {};
+    const uint8_t* wrow[2];
+    const float* wscale[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      int n = base[h] + col;
+      if (n >= N) n = N - 1;  // rows past the end: computed on the last row, never stored
+      wrow[h] = b + ((int64_t)tile.e * N + n) * K;
+      int nb = base[h] / kScaleBlock;
+      if (nb >= scale_blocks(N)) nb = scale_blocks(N) - 1;
+      wscale[h] = g.b_scale + ((int64_t)tile.e * scale_blocks(N) + nb) * KB;
+    }
+    const uint8_t* arow[kNarrowTiles];
+    const float* ascale[kNarrowTiles];
+#pragma unroll
+    for (int m = 0; m < kNarrowTiles; ++m) {
+      int64_t r = tile.r0 + m * 16 + col;
+      if (r >= tile.r1) r = tile.r1 - 1;
+      arow[m] = a + r * K;
+      ascale[m] = g.a_scale + r * KB;
+    }
+    for (int kb = 0; kb < KB; ++kb) {
+      i32x8 wv[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int c = kb * kScaleBlock + (quad + 4 * p) * 16;
+          u32x4 v = {0u, 0u, 0u, 0u};
+          if (c < K) v = *reinterpret_cast<const u32x4*>(wrow[h] + c);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) wv[h][4 * p + q] = (int)v[q];
+        }
+#pragma unroll
+      for (int m = 0; m < kNarrowTiles; ++m) {
+        if (m < nt) {
+          i32x8 av;
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const int c = kb * kScaleBlock + (quad + 4 * p) * 16;
+            u32x4 v = {0u, 0u, 0u, 0u};
+            if (c < K) v = *reinterpret_cast<const u32x4*>(arow[m] + c);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) av[4 * p + q] = (int)v[q];
+          }
+          const float sa = ascale[m][kb];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const f32x4 p = mfma_e4m3(wv[h], av);
+            const float s = sa * wscale[h][kb];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[h][m][i] = fmaf(p[i], s, acc[h][m][i]);
+          }
+        }
+      }
+    }
+    if constexpr (!SWIGLU) {
+      uint16_t* y = static_cast<uint16_t*>(g.y);
+#pragma unroll
+      for (int m = 0; m < kNarrowTiles; ++m) {
+        const int64_t r = tile.r0 + m * 16 + col;
+        if (r < tile.r1) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int n = base[h] + 4 * quad;
+            if (n < N) {
+              const u32x2 o = {pack_bf16x2(acc[h][m][0], acc[h][m][1]), pack_bf16x2(acc[h][m][2], acc[h][m][3])};
+              *reinterpret_cast<u32x2*>(y + r * N + n) = o;
+            }
+          }
+        }
+      }
+    } else {
+      uint8_t* y = static_cast<uint8_t*>(g.y);
+      const bool in = n0 + 4 * quad < outs;  // outs % 64 == 0: a tile is inside or outside as a whole
+#pragma unroll
+      for (int m = 0; m < kNarrowTiles; ++m) {
+        float top = kAmaxFloor;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float gate = acc[0][m][i];
+          const float v = gate / (1.0f + expf(-gate)) * acc[1][m][i];
+          acc[0][m][i] = v;
+          top = fmaxf(top, in ? fabsf(v) : 0.0f);
+        }
+        top = fmaxf(top, __shfl_xor(top, 16, kWave));
+        top = fmaxf(top, __shfl_xor(top, 32, kWave));
+        if (quad == 0) s_max[wave][m * 16 + col] = top;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int m = 0; m < kNarrowTiles; ++m) {
+        float top = s_max[0][m * 16 + col];
+#pragma unroll
+        for (int w = 1; w < kNarrowWaves; ++w) top = fmaxf(top, s_max[w][m * 16 + col]);
+        const int64_t r = tile.r0 + m * 16 + col;
+        if (r < tile.r1 && in) {
+          const float inv = block_inverse(top);
+          *reinterpret_cast<uint32_t*>(y + r * outs + n0 + 4 * quad) =
+              pack_e4m3x4(acc[0][m][0] * inv, acc[0][m][1] * inv, acc[0][m][2] * inv, acc[0][m][3] * inv);
+          if (wave == 0 && quad == 0) g.y_scale[r * scale_blocks(outs) + n0 / kScaleBlock] = block_scale(top);
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_grouped_fp8(const Budget& b, const GroupedArgs& g, bool swiglu, hipStream_t stream) {
+  (void)b;
+  const int units_n = swiglu ? (g.N / 2 + kNarrowCols - 1) / kNarrowCols : (g.N + 2 * kNarrowCols - 1) / (2 * kNarrowCols);
+  // one workgroup for each tile there can be: every expert may end inside one
+  const int64_t tiles = g.rows / kNarrowRows + (g.E < g.rows ? g.E : g.rows);
+  const int64_t want = tiles * units_n, most = 1 << 22;
+  const int grid = (int)(want < most ? want : most);
+  if (swiglu)
+    hipLaunchKernelGGL(grouped_narrow_kernel<true>, dim3(grid), dim3(kNarrowWaves * kWave), 0, stream, g, units_n);
+  else
+    hipLaunchKernelGGL(grouped_narrow_kernel<false>, dim3(grid), dim3(kNarrowWaves * kWave), 0, stream, g, units_n);
+  return hipGetLastError();
+}
+
+}  // namespace ep

@@ -1,0 +1,155 @@
+/*
+ * ep_expert.h -- the expert side of libep.so: the 8-bit dispatch, the experts'
+ * 8-bit matrix products on the dispatched rows, and the gradients of dispatch
+ * and combine.  Same library, same return codes and the same conventions as
+ * ep.h, which this header includes: device pointers into memory the caller
+ * owns, work only enqueued on `stream`, host-detectable errors before any HIP
+ * call, nothing allocated, no synchronisation.  Every call below may be
+ * captured into a HIP graph, and calls share no state: two of them on
+ * different streams do not touch each other's memory.
+ *
+ * A layer runs them in this order (R = T * k receive rows):
+ *
+ *   ep_layout             counts, offsets, dest_row of the router's choices
+ *   ep_dispatch_fp8       token rows to expert rows, 8 bits, block scales
+ *   ep_grouped_swiglu_fp8 gate and up products, SiLU(gate) * up, 8 bits again
+ *   ep_grouped_gemm_fp8   down product, bf16 expert outputs
+ *   ep_combine            the gate-weighted sum back in token order
+ *
+ * and, training on bf16 rows, the way back:
+ *
+ *   ep_combine_backward   dout -> gradient of the expert rows and the weights
+ *   (the experts' own backward)
+ *   ep_dispatch_backward  gradient of the receive rows -> of the token rows
+ *
+ * 8-bit values are e4m3 in the OCP encoding (1 sign, 4 exponent, 3 mantissa
+ * bits, largest finite value 448, no infinities).  A row of n values carries
+ * ceil(n / EP_FP8_BLOCK) float32 scales, one for each 128 consecutive values
+ * (the last block may be shorter); the value that is meant is
+ * float(q[i]) * scale[i / 128].
+ *
+ * Rows are 16-byte vectors, so an 8-bit row has a multiple of 16 values.
+ */
+#ifndef EP_EXPERT_H
+#define EP_EXPERT_H
+
+#include "ep.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* values that share a scale: along a row, and along both sides of a weight */
+#define EP_FP8_BLOCK 128
+
+/*
+ * ep_dispatch_fp8 -- ep_dispatch that quantises on the way: each token row is
+ * read and rounded to 8 bits once and written to its k receive rows.
+ *   per block b of 128 values of x[t, :]:
+ *     amax  = max(max |x|, 2^-100)
+ *     scale = amax / 448                            (float32, rounded once)
+ *     q     = e4m3_rne(float(x) * (448 / amax))     (quotient and product float32)
+ *   recv_q[dest_row[t*k+j], :] = q,  recv_scale[dest_row[t*k+j], b] = scale
+ * The floor keeps every scale a normal number, so an all-zero block is zeros
+ * with a small scale.  A NaN stays a NaN in its place (it does not enter the
+ * maximum); a block that holds an infinity becomes NaN as a whole, with an
+ * infinite scale.
+ *   x          bf16 [T, H], H % 16 == 0
+ *   dest_row   int32 [T, k], normally from ep_layout; an entry outside
+ *              [0, recv_rows) is skipped; rows nobody targets are untouched;
+ *              the entries in range are distinct, as ep_layout makes them (a
+ *              row that two entries list ends as a mix of the two)
+ *   recv_q     e4m3 [recv_rows, H], 16-byte aligned
+ *   recv_scale float32 [recv_rows, ceil(H / 128)]
+ * Limits as ep_dispatch.  Runs under the compute-unit budget
+ * (ep_set_num_cus) and on CU-masked streams; the variant and slab settings
+ * do not apply.
+ */
+int ep_dispatch_fp8(const void* x, int T, int H, const int32_t* dest_row, int k, void* recv_q, float* recv_scale,
+                    int64_t recv_rows, void* stream);
+
+/*
+ * ep_grouped_gemm_fp8 -- the rows of each expert times that expert's weight:
+ *   y[r, n] = bf16_rne( sum_b a_scale[r, b] * b_scale[e, n / 128, b]
+ *                             * sum_{i in block b} a[r, i] * b[e, n, i] )
+ * for every row r of expert e, offsets[e] <= r < offsets[e + 1].  The inner
+ * sums run on the matrix cores in float32; the outer one is float32 in
+ * ascending b (in few-row calls in up to 16 runs of consecutive blocks that
+ * are added at the end).  Which of its kernels runs follows from the sizes
+ * alone, so equal calls give equal bits.
+ *   a        e4m3 [rows, K], K % 16 == 0       a_scale  float32 [rows, ceil(K / 128)]
+ *   offsets  int32 [E + 1] from ep_layout, non-decreasing; they are clamped
+ *            to [0, rows], so no value reaches outside the buffers
+ *   b        e4m3 [E, N, K], N % 8 == 0        b_scale  float32 [E, ceil(N / 128), ceil(K / 128)]
+ *   y        bf16 [rows, N]; rows that no expert holds (past offsets[E]) are
+ *            neither read nor written
+ * a, b and y are 16-byte aligned.  Limits: 1 <= E <= EP_MAX_EXPERTS,
+ * 0 <= rows <= EP_MAX_ENTRIES, N * K < 2^31.  rows == 0 enqueues nothing.
+ * The gradient of a is the same product with the gradient rows and weights
+ * stored transposed ([E, K, N] with scales [E, ceil(K/128), ceil(N/128)]).
+ * The compute-unit budget does not apply (these are the computations that it
+ * keeps compute units free for); a CU-masked stream does.
+ */
+int ep_grouped_gemm_fp8(const void* a, const float* a_scale, int64_t rows, int K, const int32_t* offsets, int E,
+                        const void* b, const float* b_scale, int N, void* y, void* stream);
+
+/*
+ * ep_grouped_swiglu_fp8 -- gate and up product of each expert, the SwiGLU
+ * activation and the rounding to 8 bits for the product that follows:
+ *   gate[r, i] = the product above for weight row i,  up[r, i] for row I + i
+ *   h[r, i]    = gate / (1 + exp(-gate)) * up                     (float32)
+ *   out_scale[r, b], out_q[r, :] = h in blocks of 128, rounded as by
+ *                                  ep_dispatch_fp8
+ *   a, a_scale, offsets   as above
+ *   b        e4m3 [E, 2 I, K]: I gate rows, then I up rows; I % 64 == 0
+ *   b_scale  float32 [E, ceil(2 I / 128), ceil(K / 128)]
+ *   out_q    e4m3 [rows, I], 16-byte aligned
+ *   out_scale float32 [rows, ceil(I / 128)]
+ * Rows that no expert holds are neither read nor written.  Limits as above
+ * with N = 2 I.
+ */
+int ep_grouped_swiglu_fp8(const void* a, const float* a_scale, int64_t rows, int K, const int32_t* offsets, int E,
+                          const void* b, const float* b_scale, int I, void* out_q, float* out_scale, void* stream);
+
+/*
+ * ep_combine_backward -- the gradient of ep_combine.  For every entry (t, j)
+ * whose row r = dest_row[t*k+j] lies in [0, recv_rows):
+ *   dy[r, :]  = bf16_rne( topk_w[t, j] * float(dout[t, :]) )
+ *   dw[t, j]  = sum_h float(dout[t, h]) * float(y[r, h])          (float32)
+ * Entries out of range get dw = 0; rows of dy that no entry lists are
+ * untouched.  Entries in range are distinct, as ep_layout makes them (of a
+ * row that two entries list, either's gradient is kept, per 16-byte vector).
+ * The sums are taken in a fixed order: equal calls give equal bits.
+ *   dout      bf16 [T, H]
+ *   y         bf16 [recv_rows, H], the expert outputs that ep_combine read;
+ *             may be NULL when dw is NULL or recv_rows == 0
+ *   dest_row  int32 [T, k],  topk_w float32 [T, k] (may be NULL when dy is)
+ *   dy        bf16 [recv_rows, H], or NULL: not wanted
+ *   dw        float32 [T, k], or NULL: not wanted; not both NULL
+ * dy may not overlap y or dout.  Limits as ep_combine.  Runs under the
+ * compute-unit budget and on CU-masked streams.
+ */
+int ep_combine_backward(const void* dout, const void* y, int64_t recv_rows, int H, const int32_t* dest_row,
+                        const float* topk_w, int T, int k, void* dy, float* dw, void* stream);
+
+/*
+ * ep_dispatch_backward -- the gradient of ep_dispatch (and, taking the
+ * rounding to 8 bits as the identity, of ep_dispatch_fp8):
+ *   dx[t, :] = bf16_rne( sum_{j=0..k-1} float(drecv[dest_row[t*k+j], :]) )
+ * summed in float32 from +0.0, j ascending; an entry out of range adds
+ * nothing, and a token without one in range gets +0.0.  Bit-identical to
+ * ep_combine with unit weights, without reading any.
+ *   drecv     bf16 [recv_rows, H]; may be NULL when recv_rows == 0
+ *   dest_row  int32 [T, k]
+ *   dx        bf16 [T, H]
+ * Limits as ep_combine.  Runs under the compute-unit budget and on CU-masked
+ * streams.
+ */
+int ep_dispatch_backward(const void* drecv, int64_t recv_rows, int H, const int32_t* dest_row, int T, int k, void* dx,
+                         void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* EP_EXPERT_H */
