@@ -28,6 +28,11 @@ struct GroupedArgs {
   void* y;
   float* y_scale;
 };
+// The kernel for experts with many rows (grouped_wide.hip), bm = 128 or 256
+// token rows per workgroup; fits: whether it takes these sizes.
+bool grouped_wide_fits(const GroupedArgs& g, bool swiglu, int bm);
+hipError_t launch_grouped_wide(const GroupedArgs& g, bool swiglu, int bm, hipStream_t stream);
+
 hipError_t launch_grouped_fp8(const Budget& b, const GroupedArgs& g, bool swiglu, hipStream_t stream);
 
 // ---- backward.hip

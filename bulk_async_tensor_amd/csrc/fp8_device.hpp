@@ -39,4 +39,8 @@ __device__ __forceinline__ f32x4 mfma_e4m3(i32x8 a, i32x8 b) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
 }
 
+// SiLU(gate) * up in float32.  Far below zero exp(-gate) is infinite and the
+// quotient -0, as its limit is.
+__device__ __forceinline__ float silu_mul(float gate, float up) { return gate / (1.0f + expf(-gate)) * up; }
+
 }  // namespace ep

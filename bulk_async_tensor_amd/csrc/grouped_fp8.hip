@@ -162,8 +162,7 @@ __global__ __launch_bounds__(kNarrowWaves * kWave) void grouped_narrow_kernel(Gr
         float top = kAmaxFloor;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float gate = acc[0][m][i];
-          const float v = gate / (1.0f + expf(-gate)) * acc[1][m][i];
+          const float v = silu_mul(acc[0][m][i], acc[1][m][i]);
           acc[0][m][i] = v;
           top = fmaxf(top, in ? fabsf(v) : 0.0f);
         }
@@ -194,6 +193,9 @@ __global__ __launch_bounds__(kNarrowWaves * kWave) void grouped_narrow_kernel(Gr
 
 hipError_t launch_grouped_fp8(const Budget& b, const GroupedArgs& g, bool swiglu, hipStream_t stream) {
   (void)b;
+  const int64_t mean = g.rows / g.E;
+  const int bm = mean > 192 ? 256 : 128;
+  if (mean >= 32 && grouped_wide_fits(g, swiglu, bm)) return launch_grouped_wide(g, swiglu, bm, stream);
   const int units_n = swiglu ? (g.N / 2 + kNarrowCols - 1) / kNarrowCols : (g.N + 2 * kNarrowCols - 1) / (2 * kNarrowCols);
   // one workgroup for each tile there can be: every expert may end inside one
   const int64_t tiles = g.rows / kNarrowRows + (g.E < g.rows ? g.E : g.rows);
