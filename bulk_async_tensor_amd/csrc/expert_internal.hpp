@@ -29,9 +29,9 @@ struct GroupedArgs {
   float* y_scale;
 };
 // The kernel for experts with many rows (grouped_wide.hip), bm = 128 or 256
-// token rows per workgroup; fits: whether it takes these sizes.
-bool grouped_wide_fits(const GroupedArgs& g, bool swiglu, int bm);
-hipError_t launch_grouped_wide(const GroupedArgs& g, bool swiglu, int bm, hipStream_t stream);
+// token rows at a time; fits: whether it takes this K.
+bool grouped_wide_fits(const GroupedArgs& g);
+hipError_t launch_grouped_wide(const Budget& b, const GroupedArgs& g, bool swiglu, int bm, hipStream_t stream);
 
 hipError_t launch_grouped_fp8(const Budget& b, const GroupedArgs& g, bool swiglu, hipStream_t stream);
 

@@ -39,6 +39,18 @@ __device__ __forceinline__ f32x4 mfma_e4m3(i32x8 a, i32x8 b) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
 }
 
+// Exchanges between the 16-lane rows of a wave (v_permlane16_swap_b32 and
+// v_permlane32_swap_b32): {a0, b0, a2, b2} and {a1, b1, a3, b3} of the rows of
+// a and b; {a0, a1, b0, b1} and {a2, a3, b2, b3}.
+__device__ __forceinline__ u32x2 swap_rows16(uint32_t a, uint32_t b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  return u32x2{(uint32_t)r[0], (uint32_t)r[1]};
+}
+__device__ __forceinline__ u32x2 swap_rows32(uint32_t a, uint32_t b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  return u32x2{(uint32_t)r[0], (uint32_t)r[1]};
+}
+
 // SiLU(gate) * up in float32.  Far below zero exp(-gate) is infinite and the
 // quotient -0, as its limit is.
 __device__ __forceinline__ float silu_mul(float gate, float up) { return gate / (1.0f + expf(-gate)) * up; }

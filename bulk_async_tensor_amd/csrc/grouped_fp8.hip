@@ -192,10 +192,9 @@ __global__ __launch_bounds__(kNarrowWaves * kWave) void grouped_narrow_kernel(Gr
 }  // namespace
 
 hipError_t launch_grouped_fp8(const Budget& b, const GroupedArgs& g, bool swiglu, hipStream_t stream) {
-  (void)b;
   const int64_t mean = g.rows / g.E;
   const int bm = mean > 192 ? 256 : 128;
-  if (mean >= 32 && grouped_wide_fits(g, swiglu, bm)) return launch_grouped_wide(g, swiglu, bm, stream);
+  if (mean >= 32 && grouped_wide_fits(g)) return launch_grouped_wide(b, g, swiglu, bm, stream);
   const int units_n = swiglu ? (g.N / 2 + kNarrowCols - 1) / kNarrowCols : (g.N + 2 * kNarrowCols - 1) / (2 * kNarrowCols);
   // one workgroup for each tile there can be: every expert may end inside one
   const int64_t tiles = g.rows / kNarrowRows + (g.E < g.rows ? g.E : g.rows);

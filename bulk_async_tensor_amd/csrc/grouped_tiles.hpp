@@ -4,14 +4,14 @@
 // end to its start, so no offset reaches outside the buffers.
 #pragma once
 
+#include "ep.h"
 #include "ep_device.hpp"
 #include "expert_internal.hpp"
 
 namespace ep {
 
-constexpr int kXcds = 8;              // workgroup i of a grid runs on XCD i % 8
-constexpr int kWideMaxBlocks = 512;   // scale blocks along K that the wide kernel holds (K <= 65536)
-constexpr int64_t kWideMaxGrid = 1 << 22;  // workgroups of one launch (2^31 threads)
+constexpr int kXcds = 8;             // workgroup i of a grid runs on XCD i % 8
+constexpr int kWideMaxBlocks = 128;  // scale blocks along K that the wide kernel holds (K <= 16384)
 
 // Tiles there can be: every expert that holds a row may end inside one.
 inline int64_t wide_tiles_most(int64_t rows, int E, int bm) { return rows / bm + (E < rows ? E : rows); }
@@ -19,13 +19,30 @@ inline int64_t wide_tiles_most(int64_t rows, int E, int bm) { return rows / bm +
 struct Segment {
   int lo, hi;
 };
-__device__ __forceinline__ Segment segment_of(const int32_t* __restrict__ offsets, int E, int rows, int e) {
-  Segment s = {0, 0};
-  if (e < E) {
-    s.lo = min(max(offsets[e], 0), rows);
-    s.hi = min(max(offsets[e + 1], s.lo), rows);
-  }
+__device__ __forceinline__ Segment segment_of(const int32_t* __restrict__ offsets, int rows, int e) {
+  Segment s;
+  s.lo = min(max(offsets[e], 0), rows);
+  s.hi = min(max(offsets[e + 1], s.lo), rows);
   return s;
+}
+
+// first[e] = tiles before expert e, first[E] = all of them.  One wave.
+template <int BM>
+__device__ __forceinline__ void first_tiles(const int32_t* __restrict__ offsets, int E, int rows, int lane,
+                                            int32_t* first) {
+  int before = 0;
+  for (int e0 = 0; e0 < E; e0 += kWave) {
+    const int e = e0 + lane;
+    int n = 0;
+    if (e < E) {
+      const Segment s = segment_of(offsets, rows, e);
+      n = (int)(((int64_t)s.hi - s.lo + BM - 1) / BM);
+    }
+    const int incl = wave_incl_scan(n, lane);
+    if (e < E) first[e] = before + incl - n;
+    before += __builtin_amdgcn_readlane(incl, kWave - 1);
+  }
+  if (lane == 0) first[E] = before;
 }
 
 // A workgroup's rows: expert e, receive rows [r0, r1), and its tile along the
@@ -35,47 +52,28 @@ struct WideTile {
   int64_t r0, r1;
 };
 
-// The tiles, expert by expert and row tile fastest, are cut into 8 runs of
-// equal length, one for each XCD: the workgroups that run together on an XCD
-// then share an expert's weights and rows in its L2.  Every lane of the wave
-// takes part; false for a workgroup past the last tile.
+// Tile number id (below first[E] * units_n), expert by expert and row tile
+// fastest: neighbours share an expert's weights, and then its rows.  Two
+// rounds of 64 and 16 comparisons find the expert (E <= 1024).  Every lane of
+// the wave takes part.
 template <int BM>
-__device__ __forceinline__ bool find_wide_tile(const int32_t* __restrict__ offsets, int E, int64_t rows, int units_n,
-                                               int lane, WideTile* out) {
-  int mine = 0;
-  for (int e = lane; e < E; e += kWave) {
-    const Segment s = segment_of(offsets, E, (int)rows, e);
-    mine += (s.hi - s.lo + BM - 1) / BM;
-  }
-#pragma unroll
-  for (int d = kWave / 2; d > 0; d >>= 1) mine += __shfl_xor(mine, d, kWave);
-  const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(mine) * units_n;
-  const int64_t run = (total + kXcds - 1) / kXcds;
-  const int64_t slot = blockIdx.x / kXcds;
-  const int64_t id = (blockIdx.x % kXcds) * run + slot;
-  if (slot >= run || id >= total) return false;
-  const int want = (int)(id / units_n);  // row tiles before this one's expert are at most this many
-  int before = 0;
-  for (int e0 = 0; e0 < E; e0 += kWave) {
-    const Segment s = segment_of(offsets, E, (int)rows, e0 + lane);
-    const int n = (s.hi - s.lo + BM - 1) / BM;
-    const int incl = wave_incl_scan(n, lane);
-    const uint64_t past = ballot(before + incl > want);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      const int tiles = __builtin_amdgcn_readlane(n, l);
-      const int first = before + __builtin_amdgcn_readlane(incl, l) - tiles;
-      const int local = (int)(id - (int64_t)first * units_n);
-      out->e = e0 + l;
-      out->n = local / tiles;
-      const int lo = __builtin_amdgcn_readlane(s.lo, l), hi = __builtin_amdgcn_readlane(s.hi, l);
-      out->r0 = (int64_t)lo + (int64_t)(local - out->n * tiles) * BM;
-      out->r1 = out->r0 + BM < hi ? out->r0 + BM : hi;
-      return true;
-    }
-    before += __builtin_amdgcn_readlane(incl, kWave - 1);
-  }
-  return false;
+__device__ __forceinline__ void find_tile_of(const int32_t* __restrict__ offsets, const int32_t* first, int E,
+                                             int rows, int units_n, int64_t id, int lane, WideTile* out) {
+  static_assert(EP_MAX_EXPERTS <= kWave * 16, "the two rounds cover every expert");
+  const int q = (int)(id / units_n);
+  const int base = 16 * __builtin_popcountll(ballot(first[min((lane + 1) * 16, E)] <= q));
+  const int e = base + __builtin_popcountll(ballot(lane < 16 && first[min(base + lane + 1, E)] <= q));
+  const int before = __builtin_amdgcn_readfirstlane(first[e]);
+  const int tiles = __builtin_amdgcn_readfirstlane(first[e + 1]) - before;
+  const int local = (int)(id - (int64_t)before * units_n);
+  // (scalar loads: a vector load would wait for every load in flight)
+  typedef const __attribute__((address_space(4))) int32_t* scalar_i32;
+  const scalar_i32 at = (scalar_i32)(uintptr_t)(offsets + e);
+  const int lo = min(max(at[0], 0), rows), hi = min(max(at[1], lo), rows);
+  out->e = e;
+  out->n = local / tiles;
+  out->r0 = (int64_t)lo + (int64_t)(local - out->n * tiles) * BM;
+  out->r1 = out->r0 + BM < hi ? out->r0 + BM : hi;
 }
 
 }  // namespace ep

@@ -1,13 +1,22 @@
 // The experts' 8-bit products for experts with many rows: a workgroup of 8
-// waves computes 256 weight rows x BM token rows (swiglu: 128 gate and the 128
-// up rows of the same outputs) from tiles that both sides' loads bring
-// straight into LDS.
+// waves computes 256 weight rows x BM token rows at a time (swiglu: 128 gate
+// rows and the 128 up rows of the same outputs) from tiles that both sides'
+// loads bring straight into LDS.
 //
 // One step is one block of 128 values, so a step's matrix-core results are
 // whole inner sums: each is multiplied by its two scales and added to the
-// running sum in float32 on the vector units, which work beside the matrix
-// cores.  Two stages: the next step's tiles (64 KiB at BM = 256) load while
-// the current ones are multiplied.
+// running sum in float32 on the vector units, beside the matrix cores.
+//
+// The workgroups stay (one per CU; its LDS is full) and run through their
+// tiles as one stream of steps, so that the next tile's loads are under way
+// while a tile's last steps and its results are done.  The tiles of a step
+// have two copies in LDS, for even and odd steps.  A step has one barrier,
+// placed where every wave has its last rows of the step in registers and two
+// weight tiles' products still to issue: past it the copy is free and the
+// loads of the step after next start, and the next step's tiles, whose loads
+// started a step ago, are read while those products run.  (With the barrier at
+// the step's end the matrix cores wait for 80 KiB of LDS reads each step.)
+// The stream goes on loading past its end (the last tile again).
 //
 // LDS rows are 128 bytes, 8 chunks of 16; row r keeps chunk c at place
 // c ^ (r & 7), so the 16 rows that one instruction reads at one chunk fall on
@@ -21,112 +30,146 @@ namespace ep {
 
 namespace {
 
-typedef __attribute__((address_space(3))) uint8_t lds_byte_t;
-
 constexpr int kWideWaves = 8;
 constexpr int kWideCols = 256;   // weight rows per workgroup
+constexpr int kHalf = 128;       // the first and the second weight rows
 constexpr int kStepBytes = 128;  // one block of a row
+constexpr int kScaleSteps = 8;   // blocks whose token scales are loaded together
 
-template <int BM, bool SWIGLU>
+template <int BM>
 struct Wide {
-  static constexpr int WN = BM == 256 ? 2 : 4;   // waves along the weight rows
-  static constexpr int WM = kWideWaves / WN;     // waves along the token rows
-  static constexpr int NT = kWideCols / 16 / WN; // weight tiles of a wave
-  static constexpr int MT = BM / 16 / WM;        // token tiles of a wave
-  static constexpr int kB = kWideCols * kStepBytes;
-  static constexpr int kStage = kB + BM * kStepBytes;
-  static_assert(MT == 4, "a wave's token scales are one per lane");
-  // first LDS weight row of the wave's tile i
-  static __device__ __forceinline__ int row_of(int wn, int i) {
-    if (!SWIGLU) return (wn * NT + i) * 16;
-    return i < NT / 2 ? (wn * (NT / 2) + i) * 16 : 128 + (wn * (NT / 2) + i - NT / 2) * 16;
-  }
+  static constexpr int WN = BM == 256 ? 2 : 4;  // waves along the weight rows
+  static constexpr int WM = kWideWaves / WN;    // waves along the token rows
+  static constexpr int HT = kHalf / 16 / WN;    // weight tiles of a wave in each half
+  static constexpr int MT = BM / 16 / WM;       // token tiles of a wave
+  static constexpr int kT = BM * kStepBytes, kStage = kT + kWideCols * kStepBytes;  // token rows, then weight rows
+  static constexpr int LT = BM / kWideWaves / 8;     // load instructions of a wave: token rows,
+  static constexpr int LW = kHalf / kWideWaves / 8;  // and weight rows of one half
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+// A raw buffer of `bytes` at p: loads past its end bring zeros.
+__device__ __forceinline__ u32x4 buffer_of(const void* p, int64_t bytes) {
+  const uint64_t at = (uint64_t)(uintptr_t)p;
+  u32x4 r = {(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (uint32_t)bytes, 0x00020000u};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = (uint32_t)__builtin_amdgcn_readfirstlane((int)r[i]);
+  return r;
+}
+
+// Buffer loads straight to LDS: every lane's 16 (or 4) bytes from its own
+// offset land at lds + 16 (or 4) * lane.  They are written as instructions
+// because the compiler, which cannot tell the copies of an array apart, would
+// wait for all of them before any LDS read; the barriers below wait for the
+// ones that are due.  They have no result registers, and the next instruction
+// may change the address registers.  The s_nop covers M0 and buffer registers
+// that a vector instruction has just written (5 wait states).
+__device__ __forceinline__ void load16_to_lds(const u32x4& buf, uint32_t lds, uint32_t offset, int base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(offset),
+               "s"(buf), "s"(base)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void load4_to_lds(const u32x4& buf, uint32_t lds, uint32_t offset, int base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(offset),
+               "s"(buf), "s"(base)
+               : "memory", "m0");
+}
+
+// Every wave's loads have landed (LOADS), and its LDS accesses are done.
+template <bool LOADS>
+__device__ __forceinline__ void wide_barrier() {
+  constexpr int imm = (0x7 << 4) | (LOADS ? 0 : 0xF | (0x3 << 14));  // lgkmcnt(0), vmcnt(0) or none
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(imm);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 template <int BM, bool SWIGLU>
 __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) {
-  using W = Wide<BM, SWIGLU>;
-  constexpr int NT = W::NT, MT = W::MT;
-  __shared__ __attribute__((aligned(1024))) uint8_t s_stage0[W::kStage];
-  __shared__ __attribute__((aligned(1024))) uint8_t s_stage1[W::kStage];
-  __shared__ float s_sa0[kWideWaves][kWave], s_sa1[kWideWaves][kWave];
-  __shared__ float s_sb[3][kWideMaxBlocks];
+  using W = Wide<BM>;
+  constexpr int HT = W::HT, MT = W::MT, NT = 2 * HT;
+  static_assert(MT == 4, "a wave holds four token tiles");
+  __shared__ __attribute__((aligned(1024))) uint8_t s_rows[2 * W::kStage];
+  __shared__ float s_sa[2][BM * kScaleSteps];
+  __shared__ float s_sb[2][3][kWideMaxBlocks];
+  __shared__ int32_t s_first[EP_MAX_EXPERTS + 1];
   __shared__ float s_max[W::WN][BM];
   const int lane = lane_id();
   const int wave = wave_in_group();
   const int col = lane & 15, quad = lane >> 4;
   const int K = g.K, N = g.N, KB = scale_blocks(K), NB = scale_blocks(N);
   const int outs = SWIGLU ? N / 2 : N;
-
-  WideTile tile;
-  if (!find_wide_tile<BM>(g.offsets, g.E, g.rows, units_n, lane, &tile)) return;
-  const int n0 = tile.n * (SWIGLU ? kWideCols / 2 : kWideCols);
-  const int held = (int)(tile.r1 - tile.r0);
   const int wn = wave % W::WN, wm = wave / W::WN;
 
-  // ---- the loads: each wave brings 32 weight rows and BM / 8 token rows a step, 8 rows an instruction
-  const uint8_t* a = static_cast<const uint8_t*>(g.a) + tile.r0 * K;
-  const uint8_t* b = static_cast<const uint8_t*>(g.b) + (int64_t)tile.e * N * K;
-  const __amdgpu_buffer_rsrc_t ra = buffer_of(a, (int64_t)held * K);
-  const __amdgpu_buffer_rsrc_t rb = buffer_of(b, (int64_t)N * K);
-  const __amdgpu_buffer_rsrc_t rs = buffer_of(g.a_scale + tile.r0 * KB, (int64_t)held * KB * 4);
-  constexpr int LB = kWideCols / kWideWaves / 8, LA = BM / kWideWaves / 8;
-  const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
-  uint32_t vb[LB], va[LA], vs;
-#pragma unroll
-  for (int j = 0; j < LB; ++j) {
-    const int r = wave * (kWideCols / kWideWaves) + j * 8 + (lane >> 3);
-    int n = SWIGLU ? (r < 128 ? n0 + r : outs + n0 + r - 128) : n0 + r;
-    if (n >= N) n = N - 1;  // rows past the end: computed on the last row, never stored
-    vb[j] = (uint32_t)n * K + chunk;
-  }
-#pragma unroll
-  for (int j = 0; j < LA; ++j) {
-    int r = wave * (BM / kWideWaves) + j * 8 + (lane >> 3);
-    if (r >= held) r = held - 1;
-    va[j] = (uint32_t)r * K + chunk;
-  }
-  {
-    int r = wm * (MT * 16) + lane;
-    if (r >= held) r = held - 1;
-    vs = (uint32_t)r * KB * 4;
-  }
+  // ---- the tiles of this workgroup: a run of them for each XCD
+  if (wave == 0) first_tiles<BM>(g.offsets, g.E, (int)g.rows, lane, s_first);
+  __syncthreads();
+  const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(s_first[g.E]) * units_n;
+  const int64_t run = (total + kXcds - 1) / kXcds;
+  const int64_t begin = (blockIdx.x % kXcds) * run;
+  const int64_t end = begin + run < total ? begin + run : total;
+  const int stride = gridDim.x / kXcds;
+  int64_t id = begin + blockIdx.x / kXcds;
+  if (id >= end) return;
 
-  // ---- the weight scales of all steps: block rows n0 / 128 and the next; swiglu: one gate and two up rows
-  for (int i = threadIdx.x; i < 3 * KB; i += kWideWaves * kWave) {
-    const int which = i / KB, kb = i - which * KB;
-    int nb = SWIGLU ? (which == 0 ? n0 / kScaleBlock : (outs + n0) / kScaleBlock + which - 1) : n0 / kScaleBlock + which;
-    if (nb >= NB) nb = NB - 1;
-    s_sb[which][kb] = g.b_scale[((int64_t)tile.e * NB + nb) * KB + kb];
-  }
-  // the block row of the wave's tiles: plain, its half; swiglu, gate and up
-  const int sb0 = SWIGLU ? 0 : wn * NT * 16 / kScaleBlock;
-  const int sb1 = SWIGLU ? 1 + ((outs + n0 + wn * (NT / 2) * 16) / kScaleBlock - (outs + n0) / kScaleBlock) : sb0;
+  // ---- the loads of the stream
+  u32x4 ra, rb, rs, rw;
+  WideTile nxt;
+  int lk = 0, lgroup = 0, ltile = 0;  // the step, scale set and tile parity that loads next
+  // A lane's place in a load of 8 rows.  Rows past the segment's or the
+  // weight's end are past the buffer's: they bring zeros, and their results
+  // are never stored.
+  const uint32_t at_row = (uint32_t)(lane >> 3) * K + ((lane & 7) ^ (lane >> 3)) * 16;
+  auto first_col = [&](const WideTile& t) { return t.n * (SWIGLU ? kHalf : kWideCols); };
+  auto aim = [&]() {
+    find_tile_of<BM>(g.offsets, s_first, g.E, (int)g.rows, units_n, id, lane, &nxt);
+    const int n0 = first_col(nxt);
+    const int64_t held = nxt.r1 - nxt.r0;
+    ra = buffer_of(static_cast<const uint8_t*>(g.a) + nxt.r0 * K, held * K);
+    rb = buffer_of(static_cast<const uint8_t*>(g.b) + (int64_t)nxt.e * N * K, (int64_t)N * K);
+    rs = buffer_of(g.a_scale + nxt.r0 * KB, held * KB * 4);
+    rw = buffer_of(g.b_scale + (int64_t)nxt.e * NB * KB, (int64_t)NB * KB * 4);
+    // The weight scales of all steps, 64 an instruction: block row n0 / 128
+    // and the next; swiglu: one gate and two up rows.  (Blocks past the last
+    // one bring a neighbour's scale, or zero past the buffer; no step uses them.)
+    for (int i = wave; i < 3 * ((KB + 63) / 64); i += kWideWaves) {
+      const int which = i % 3, k0 = i / 3 * 64;
+      int nb = SWIGLU ? (which == 0 ? n0 / kScaleBlock : (outs + n0) / kScaleBlock + which - 1) : n0 / kScaleBlock + which;
+      if (nb >= NB) nb = NB - 1;
+      load4_to_lds(rw, lds_addr_of(&s_sb[ltile][which][k0]), (k0 + lane) * 4, nb * KB * 4);
+    }
+  };
+  const uint32_t rows0 = lds_addr_of(s_rows);
+  auto load = [&](int copy) {  // step lk
+    if (lk % kScaleSteps == 0) {
+      // token scales: a lane takes one block's scale of one token, 8 tokens x 8 blocks an instruction
+#pragma unroll
+      for (int j = 0; j < W::LT; ++j)
+        load4_to_lds(rs, lds_addr_of(&s_sa[lgroup][(wave * (BM / kWideWaves) + j * 8) * kScaleSteps]),
+                     (uint32_t)((wave * (BM / kWideWaves) + j * 8 + (lane >> 3)) * KB + (lane & 7)) * 4, lk * 4);
+      lgroup ^= 1;
+    }
+#pragma unroll
+    for (int j = 0; j < W::LT; ++j)
+      load16_to_lds(ra, rows0 + copy * W::kStage + (wave * (BM / kWideWaves) + j * 8) * kStepBytes,
+                    at_row + (uint32_t)(wave * (BM / kWideWaves) + j * 8) * K, lk * kStepBytes);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < W::LW; ++j)
+        load16_to_lds(rb,
+                      rows0 + copy * W::kStage + W::kT +
+                          (h * kHalf + wave * (kHalf / kWideWaves) + j * 8) * kStepBytes,
+                      at_row + (uint32_t)(first_col(nxt) + (h ? (SWIGLU ? outs : kHalf) : 0) +
+                                          wave * (kHalf / kWideWaves) + j * 8) * K,
+                      lk * kStepBytes);
+  };
 
+  // ---- the products
   f32x4 acc[NT][MT] = {};
   const int off0 = col * kStepBytes + ((quad ^ (col & 7)) * 16);
   const int off1 = col * kStepBytes + (((quad + 4) ^ (col & 7)) * 16);
-
-  auto load = [&](uint8_t* stage, float* sa, int kb) {
-#pragma unroll
-    for (int j = 0; j < LB; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rb, (lds_void_t*)(stage + (wave * (kWideCols / kWideWaves) + j * 8) * kStepBytes), 16, vb[j],
-          kb * kStepBytes, 0, 0);
-#pragma unroll
-    for (int j = 0; j < LA; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          ra, (lds_void_t*)(stage + W::kB + (wave * (BM / kWideWaves) + j * 8) * kStepBytes), 16, va[j],
-          kb * kStepBytes, 0, 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)sa, 4, vs, kb * 4, 0, 0);
-  };
-
-  // A fragment: 32 values of a row's block.
-  auto frag = [&](const uint8_t* rows) {
+  auto frag = [&](const uint8_t* rows) {  // 32 values of a row's block
     const u32x4 lo = *reinterpret_cast<const u32x4*>(rows + off0);
     const u32x4 hi = *reinterpret_cast<const u32x4*>(rows + off1);
     i32x8 f;
@@ -137,126 +180,207 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
     }
     return f;
   };
-
-  // One block: for each weight tile its four products, while the vector units
-  // scale and add those of the tile before and the next tile's rows are read.
-  // The scheduling barriers keep that order (left alone, the compiler reads
-  // all tiles first and spills).
-  auto step = [&](const uint8_t* stage, const float* sa, int kb) {
-    i32x8 t[MT], w[2];
-    float s0[MT], s1[MT];
-    f32x4 p[2][MT];
-    const uint8_t* wrows = stage + W::row_of(wn, 0) * kStepBytes;
-    const uint8_t* trows = stage + W::kB + wm * MT * 16 * kStepBytes;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) t[m] = frag(trows + m * 16 * kStepBytes);
-    w[0] = frag(wrows);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const float v = sa[m * 16 + col];
-      s0[m] = v * s_sb[sb0][kb];
-      s1[m] = SWIGLU ? v * s_sb[sb1][kb] : s0[m];
+  // A last block that is not full: its rows hold other bytes past their end
+  // (the next row's, or zeros past the buffer), which become zeros here.
+  const int full = K / kStepBytes;
+  auto clear_tail = [&](uint8_t* rows, int n) {
+    const int first = (K - full * kStepBytes) / 16;
+    for (int i = threadIdx.x; i < n * 8; i += kWideWaves * kWave) {
+      const int r = i >> 3, c = i & 7;
+      if (c >= first) *reinterpret_cast<u32x4*>(rows + r * kStepBytes + ((c ^ (r & 7)) * 16)) = u32x4{0u, 0u, 0u, 0u};
     }
+  };
+
+  WideTile cur;
+  int kb = 0, cgroup = 0, ctile = 0;
+  bool more = true;
+
+  i32x8 t[MT], w[4];
+  f32x4 p[4] = {};
+  float s0[MT] = {}, s1[MT] = {}, v[MT], v0, v1;
+  // Product number q of a step (weight tile q / 4, token tile q % 4) is scaled
+  // and added three products after it started, when the matrix core has
+  // finished it: the last three of a step in the next step.
+  constexpr int kLag = 3;
+  auto add = [&](int q) {
+    const int n = (q + NT * MT) % (NT * MT) / MT, m = (q + MT) % MT;
+    const float sc = n < HT ? s0[m] : s1[m];
 #pragma unroll
-    for (int n = 0; n <= NT; ++n) {
+    for (int i = 0; i < 4; ++i) acc[n][m][i] = fmaf(p[q & 3][i], sc, acc[n][m][i]);
+  };
+  auto weight_rows = [&](const uint8_t* stage, int n) {
+    return stage + W::kT + (wn * HT * 16 + (n < HT ? n * 16 : kHalf + (n - HT) * 16)) * kStepBytes;
+  };
+  auto token_rows = [&](const uint8_t* stage, int m) { return stage + (wm * MT + m) * 16 * kStepBytes; };
+  auto read_scales = [&](const WideTile& at, int tile, int group, int k) {
+    const int c0 = outs + first_col(at);
+    const int up = SWIGLU ? 1 + (c0 + wn * HT * 16) / kScaleBlock - c0 / kScaleBlock : 1;
+    v0 = s_sb[tile][0][k];
+    v1 = s_sb[tile][up][k];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) v[m] = s_sa[group][((wm * MT + m) * 16 + col) * kScaleSteps + k % kScaleSteps];
+  };
+  // The products of weight tiles [N0, N1) of the step in `stage`.  The rows of
+  // the weight tile two ahead are read meanwhile, those of the next step from
+  // its copy; and each token tile's of the next step once its last product has
+  // started.  The scheduling barriers keep this order (left alone, the
+  // compiler reads all tiles first and spills).
+  auto products = [&](const uint8_t* stage, const uint8_t* next, int N0, int N1) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (n < N0 || n >= N1) continue;
       __builtin_amdgcn_sched_barrier(0);
-      if (n + 1 < NT) w[(n + 1) & 1] = frag(wrows + (W::row_of(0, n + 1) - W::row_of(0, 0)) * kStepBytes);
+      w[(n + 2) & 3] = n + 2 < NT ? frag(weight_rows(stage, n + 2)) : frag(weight_rows(next, n + 2 - NT));
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        if (n < NT) p[n & 1][m] = mfma_e4m3(w[n & 1], t[m]);
-        if (n > 0) {
-          const float sc = n - 1 < NT / 2 ? s0[m] : s1[m];
+        const int q = n * MT + m;
+        if (q == kLag)  // the last products of the step before are added: its scales are done
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[n - 1][m][i] = fmaf(p[(n - 1) & 1][m][i], sc, acc[n - 1][m][i]);
-        }
+          for (int i = 0; i < MT; ++i) {
+            s0[i] = v[i] * v0;
+            s1[i] = v[i] * v1;
+          }
+        p[q & 3] = mfma_e4m3(w[n & 3], t[m]);
+        if (n == NT - 1) t[m] = frag(token_rows(next, m));
+        add(q - kLag);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  // A last block that is not full: its tiles hold other bytes past the row's
-  // end (the next row's, or zeros past the buffer), which become zeros here.
-  const int full = K / kStepBytes;
-  auto clear_tail = [&](uint8_t* stage) {
-    const int first = (K - full * kStepBytes) / 16;
-    for (int i = threadIdx.x; i < (kWideCols + BM) * 8; i += kWideWaves * kWave) {
-      const int r = i >> 3, c = i & 7;
-      if (c >= first) *reinterpret_cast<u32x4*>(stage + r * kStepBytes + ((c ^ (r & 7)) * 16)) = u32x4{0u, 0u, 0u, 0u};
+  auto finish = [&]() {  // the tile's results
+    const int n0 = first_col(cur), held = (int)(cur.r1 - cur.r0);
+    // lane (col, quad) holds rows 4 quad .. + 3 of each weight tile, token col of each token tile
+    if constexpr (!SWIGLU) {
+      uint16_t* y = static_cast<uint16_t*>(g.y);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int r = (wm * MT + m) * 16 + col;
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+          // two neighbouring tiles: lanes exchange so that each holds 8 adjacent outputs
+          const u32x2 d0 = swap_rows16(pack_bf16x2(acc[n][m][0], acc[n][m][1]),
+                                       pack_bf16x2(acc[n + 1][m][0], acc[n + 1][m][1]));
+          const u32x2 d1 = swap_rows16(pack_bf16x2(acc[n][m][2], acc[n][m][3]),
+                                       pack_bf16x2(acc[n + 1][m][2], acc[n + 1][m][3]));
+          const int tile = n + (quad & 1);
+          const int c = n0 + (n < HT ? 0 : kHalf - HT * 16) + (wn * HT + tile) * 16 + 8 * (quad >> 1);
+          if (r < held && c < N)
+            st16<true>(reinterpret_cast<u32x4*>(y + (cur.r0 + r) * N + c), u32x4{d0[0], d1[0], d0[1], d1[1]});
+        }
+      }
+    } else {
+      uint8_t* y = static_cast<uint8_t*>(g.y);
+      const int c0 = n0 + wn * HT * 16;  // the wave's first output; outs % 64 == 0: inside or outside as a whole
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        float top = kAmaxFloor;
+#pragma unroll
+        for (int n = 0; n < HT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float v = silu_mul(acc[n][m][i], acc[n + HT][m][i]);
+            acc[n][m][i] = v;
+            top = fmaxf(top, c0 < outs ? fabsf(v) : 0.0f);
+          }
+        top = fmaxf(top, __shfl_xor(top, 16, kWave));
+        top = fmaxf(top, __shfl_xor(top, 32, kWave));
+        if (quad == 0) s_max[wn][(wm * MT + m) * 16 + col] = top;
+      }
+      wide_barrier<false>();
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int r = (wm * MT + m) * 16 + col;
+        float top = s_max[0][r];
+#pragma unroll
+        for (int o = 1; o < W::WN; ++o) top = fmaxf(top, s_max[o][r]);
+        const float inv = block_inverse(top);
+        uint32_t d[HT];
+#pragma unroll
+        for (int n = 0; n < HT; ++n)
+          d[n] = pack_e4m3x4(acc[n][m][0] * inv, acc[n][m][1] * inv, acc[n][m][2] * inv, acc[n][m][3] * inv);
+        const bool in = r < held && c0 < outs;
+        uint8_t* out = y + (cur.r0 + r) * outs + c0;
+        if constexpr (HT == 4) {
+          // four tiles of 16 outputs: after two exchanges lane quad q holds tile q's 16
+          const u32x2 e0 = swap_rows32(d[0], d[2]), e1 = swap_rows32(d[1], d[3]);
+          const u32x2 f0 = swap_rows16(e0[0], e1[0]), f1 = swap_rows16(e0[1], e1[1]);
+          if (in) st16<true>(reinterpret_cast<u32x4*>(out + 16 * quad), u32x4{f0[0], f0[1], f1[0], f1[1]});
+        } else {
+          const u32x2 f = swap_rows16(d[0], d[1]);
+          if (in) __builtin_nontemporal_store(f, reinterpret_cast<u32x2*>(out + 16 * (quad & 1) + 8 * (quad >> 1)));
+        }
+        if (r < held && wn == 0 && quad == 0) g.y_scale[(cur.r0 + r) * scale_blocks(outs) + cur.n] = block_scale(top);
+      }
     }
-    __syncthreads();
   };
 
-  const bool live = wm * MT * 16 < held;  // waves past the last row only load
-  load(s_stage0, s_sa0[wave], 0);
-  for (int kb = 0; kb < KB; kb += 2) {
-    __syncthreads();
-    if (kb + 1 < KB) load(s_stage1, s_sa1[wave], kb + 1);
-    if (kb == full) clear_tail(s_stage0);
-    if (live) step(s_stage0, s_sa0[wave], kb);
-    if (kb + 1 < KB) {
-      __syncthreads();
-      if (kb + 2 < KB) load(s_stage0, s_sa0[wave], kb + 2);
-      if (kb + 1 == full) clear_tail(s_stage1);
-      if (live) step(s_stage1, s_sa1[wave], kb + 1);
+  aim();
+  cur = nxt;
+  load(0);
+  ++lk;
+  load(1);
+  ++lk;
+  wide_barrier<true>();
+  bool fresh = true;  // the current step is a tile's first
+  bool live = false;  // waves past the tile's last row only load
+  for (int copy = 0;; copy ^= 1) {  // step kb of the current tile
+    uint8_t* const stage = s_rows + copy * W::kStage;
+    uint8_t* const next = s_rows + (copy ^ 1) * W::kStage;
+    if (fresh) {
+      live = wm * MT * 16 < (int)(cur.r1 - cur.r0);
+      if (live) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) t[m] = frag(token_rows(stage, m));
+        w[0] = frag(weight_rows(stage, 0));
+        w[1] = frag(weight_rows(stage, 1));
+        read_scales(cur, ctile, cgroup, kb);
+      }
+    }
+    if (live) products(stage, next, 0, NT - 2);
+    wide_barrier<true>();
+    if (kb + 1 == full && full < KB) {
+      clear_tail(next, BM + kWideCols);
+      wide_barrier<false>();
+    }
+    if (lk == KB) {
+      lk = 0;
+      ltile ^= 1;
+      id += stride;
+      more = id < end;
+      if (!more) id -= stride;  // the stream loads its last tile again
+      aim();
+    }
+    load(copy);
+    ++lk;
+    ++kb;
+    const bool last = kb == KB;
+    if (last || kb % kScaleSteps == 0) cgroup ^= 1;
+    if (live) {
+      if (!last) read_scales(cur, ctile, cgroup, kb);  // the next step's
+      products(stage, next, NT - 2, NT);
+    }
+    fresh = last;
+    if (last) {
+#pragma unroll
+      for (int q = NT * MT - kLag; q < NT * MT; ++q) add(q);
+      finish();
+      if (!more) break;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[n][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // nothing is left to add in the next step
+        p[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        s1[i] = 0.0f;
+      }
+      cur = nxt;
+      kb = 0;
+      ctile ^= 1;
     }
   }
-
-  // ---- results: lane (col, quad) holds rows 4 quad .. + 3 of each weight tile, token col of each token tile
-  if constexpr (!SWIGLU) {
-    uint16_t* y = static_cast<uint16_t*>(g.y);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int r = (wm * MT + m) * 16 + col;
-      if (r < held) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int c = n0 + W::row_of(wn, n) + 4 * quad;
-          if (c < N) {
-            const u32x2 o = {pack_bf16x2(acc[n][m][0], acc[n][m][1]), pack_bf16x2(acc[n][m][2], acc[n][m][3])};
-            *reinterpret_cast<u32x2*>(y + (tile.r0 + r) * N + c) = o;
-          }
-        }
-      }
-    }
-  } else {
-    uint8_t* y = static_cast<uint8_t*>(g.y);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      float top = kAmaxFloor;
-#pragma unroll
-      for (int n = 0; n < NT / 2; ++n) {
-        const bool in = n0 + W::row_of(wn, n) < outs;  // outs % 64 == 0: a tile is inside or outside as a whole
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float v = silu_mul(acc[n][m][i], acc[n + NT / 2][m][i]);
-          acc[n][m][i] = v;
-          top = fmaxf(top, in ? fabsf(v) : 0.0f);
-        }
-      }
-      top = fmaxf(top, __shfl_xor(top, 16, kWave));
-      top = fmaxf(top, __shfl_xor(top, 32, kWave));
-      if (quad == 0) s_max[wn][(wm * MT + m) * 16 + col] = top;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int r = (wm * MT + m) * 16 + col;
-      float top = s_max[0][r];
-#pragma unroll
-      for (int w = 1; w < W::WN; ++w) top = fmaxf(top, s_max[w][r]);
-      if (r < held) {
-        const float inv = block_inverse(top);
-#pragma unroll
-        for (int n = 0; n < NT / 2; ++n) {
-          const int c = n0 + W::row_of(wn, n) + 4 * quad;
-          if (c < outs)
-            *reinterpret_cast<uint32_t*>(y + (tile.r0 + r) * outs + c) =
-                pack_e4m3x4(acc[n][m][0] * inv, acc[n][m][1] * inv, acc[n][m][2] * inv, acc[n][m][3] * inv);
-        }
-        if (wn == 0 && quad == 0) g.y_scale[(tile.r0 + r) * scale_blocks(outs) + tile.n] = block_scale(top);
-      }
-    }
-  }
+  wait_vmcnt<0>();  // no load may write this workgroup's LDS after its end
 }
 
 // One workgroup fills a CU's LDS: two waves per SIMD, 256 registers each.
@@ -267,12 +391,13 @@ __global__ __launch_bounds__(kWideWaves * kWave) __attribute__((amdgpu_waves_per
 }
 
 template <int BM, bool SWIGLU>
-hipError_t launch(const GroupedArgs& g, hipStream_t stream) {
-  const int outs = SWIGLU ? g.N / 2 : g.N, per = SWIGLU ? kWideCols / 2 : kWideCols;
+hipError_t launch(const Budget& b, const GroupedArgs& g, hipStream_t stream) {
+  const int outs = SWIGLU ? g.N / 2 : g.N, per = SWIGLU ? kHalf : kWideCols;
   const int units_n = (outs + per - 1) / per;
-  const int64_t want = wide_tiles_most(g.rows, g.E, BM) * units_n;
-  const int64_t grid = (want + kXcds - 1) / kXcds * kXcds;
-  if (grid > kWideMaxGrid) return hipErrorInvalidValue;
+  const int64_t most = wide_tiles_most(g.rows, g.E, BM) * units_n;
+  int64_t grid = b.device_cus / kXcds * kXcds;
+  if (grid > most) grid = (most + kXcds - 1) / kXcds * kXcds;
+  if (grid < kXcds) grid = kXcds;
   hipLaunchKernelGGL((grouped_wide_kernel<BM, SWIGLU>), dim3((unsigned)grid), dim3(kWideWaves * kWave), 0, stream, g,
                      units_n);
   return hipGetLastError();
@@ -280,15 +405,14 @@ hipError_t launch(const GroupedArgs& g, hipStream_t stream) {
 
 }  // namespace
 
-bool grouped_wide_fits(const GroupedArgs& g, bool swiglu, int bm) {
-  const int outs = swiglu ? g.N / 2 : g.N, per = swiglu ? kWideCols / 2 : kWideCols;
-  return scale_blocks(g.K) <= kWideMaxBlocks &&
-         wide_tiles_most(g.rows, g.E, bm) * ((outs + per - 1) / per) <= kWideMaxGrid - kXcds;
+bool grouped_wide_fits(const GroupedArgs& g) {
+  const int blocks = scale_blocks(g.K);
+  return blocks >= 2 && blocks <= kWideMaxBlocks;  // (a tile of one step would be two tiles ahead of its results)
 }
 
-hipError_t launch_grouped_wide(const GroupedArgs& g, bool swiglu, int bm, hipStream_t stream) {
-  if (bm == 256) return swiglu ? launch<256, true>(g, stream) : launch<256, false>(g, stream);
-  return swiglu ? launch<128, true>(g, stream) : launch<128, false>(g, stream);
+hipError_t launch_grouped_wide(const Budget& b, const GroupedArgs& g, bool swiglu, int bm, hipStream_t stream) {
+  if (bm == 256) return swiglu ? launch<256, true>(b, g, stream) : launch<256, false>(b, g, stream);
+  return swiglu ? launch<128, true>(b, g, stream) : launch<128, false>(b, g, stream);
 }
 
 }  // namespace ep
