@@ -9,14 +9,16 @@
 //
 // The workgroups stay (one per CU; its LDS is full) and run through their
 // tiles as one stream of steps, so that the next tile's loads are under way
-// while a tile's last steps and its results are done.  The tiles of a step
-// have two copies in LDS, for even and odd steps.  A step has one barrier,
+// while a tile's last steps and its results are done.  A step's tiles
+// lie in one of two or three copies in LDS.  A step has one barrier,
 // placed where every wave has its last rows of the step in registers and two
 // weight tiles' products still to issue: past it the copy is free and the
 // loads of the step after next start, and the next step's tiles, whose loads
 // started a step ago, are read while those products run.  (With the barrier at
 // the step's end the matrix cores wait for 80 KiB of LDS reads each step.)
-// The stream goes on loading past its end (the last tile again).
+// With BM = 128, where the weights' bytes bound the kernel, there are three
+// copies and two steps' loads on the way.  The stream goes on loading past its
+// end (the last tile again), so that the waits can count the loads.
 //
 // LDS rows are 128 bytes, 8 chunks of 16; row r keeps chunk c at place
 // c ^ (r & 7), so the 16 rows that one instruction reads at one chunk fall on
@@ -34,7 +36,6 @@ constexpr int kWideWaves = 8;
 constexpr int kWideCols = 256;   // weight rows per workgroup
 constexpr int kHalf = 128;       // the first and the second weight rows
 constexpr int kStepBytes = 128;  // one block of a row
-constexpr int kScaleSteps = 8;   // blocks whose token scales are loaded together
 
 template <int BM>
 struct Wide {
@@ -43,6 +44,9 @@ struct Wide {
   static constexpr int HT = kHalf / 16 / WN;    // weight tiles of a wave in each half
   static constexpr int MT = BM / 16 / WM;       // token tiles of a wave
   static constexpr int kT = BM * kStepBytes, kStage = kT + kWideCols * kStepBytes;  // token rows, then weight rows
+  static constexpr int S = BM == 256 ? 2 : 3;   // copies: steps whose tiles are in LDS or on the way
+  static constexpr int SS = BM == 256 ? 8 : 4;  // blocks whose token scales are loaded together
+  static constexpr int LS = BM / kWideWaves * SS / kWave;  // load instructions of a wave for them
   static constexpr int LT = BM / kWideWaves / 8;     // load instructions of a wave: token rows,
   static constexpr int LW = kHalf / kWideWaves / 8;  // and weight rows of one half
 };
@@ -74,10 +78,11 @@ __device__ __forceinline__ void load4_to_lds(const u32x4& buf, uint32_t lds, uin
                : "memory", "m0");
 }
 
-// Every wave's loads have landed (LOADS), and its LDS accesses are done.
-template <bool LOADS>
+// Every wave's loads but its newest N have landed (N = 63: any may be on the
+// way), and its LDS accesses are done.  vmcnt retires in issue order.
+template <int N>
 __device__ __forceinline__ void wide_barrier() {
-  constexpr int imm = (0x7 << 4) | (LOADS ? 0 : 0xF | (0x3 << 14));  // lgkmcnt(0), vmcnt(0) or none
+  constexpr int imm = (N & 0xF) | (0x7 << 4) | ((N >> 4) << 14);  // vmcnt(N), lgkmcnt(0)
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt(imm);
   __builtin_amdgcn_s_barrier();
@@ -89,8 +94,8 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
   using W = Wide<BM>;
   constexpr int HT = W::HT, MT = W::MT, NT = 2 * HT;
   static_assert(MT == 4, "a wave holds four token tiles");
-  __shared__ __attribute__((aligned(1024))) uint8_t s_rows[2 * W::kStage];
-  __shared__ float s_sa[2][BM * kScaleSteps];
+  __shared__ __attribute__((aligned(1024))) uint8_t s_rows[W::S * W::kStage];
+  __shared__ float s_sa[W::S][BM * W::SS];
   __shared__ float s_sb[2][3][kWideMaxBlocks];
   __shared__ int32_t s_first[EP_MAX_EXPERTS + 1];
   __shared__ float s_max[W::WN][BM];
@@ -140,29 +145,33 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
     }
   };
   const uint32_t rows0 = lds_addr_of(s_rows);
-  auto load = [&](int copy) {  // step lk
-    if (lk % kScaleSteps == 0) {
-      // token scales: a lane takes one block's scale of one token, 8 tokens x 8 blocks an instruction
+  auto load_scales = [&]() {  // of steps lk .. lk + SS - 1
+    // a lane takes one block's scale of one token: 32 or 16 contiguous bytes a
+    // token (one block of 64 tokens at a time would touch a line for each value)
 #pragma unroll
-      for (int j = 0; j < W::LT; ++j)
-        load4_to_lds(rs, lds_addr_of(&s_sa[lgroup][(wave * (BM / kWideWaves) + j * 8) * kScaleSteps]),
-                     (uint32_t)((wave * (BM / kWideWaves) + j * 8 + (lane >> 3)) * KB + (lane & 7)) * 4, lk * 4);
-      lgroup ^= 1;
+    for (int j = 0; j < W::LS; ++j) {
+      const int r = wave * (BM / kWideWaves) + j * (kWave / W::SS);
+      load4_to_lds(rs, lds_addr_of(&s_sa[lgroup][r * W::SS]),
+                   (uint32_t)((r + lane / W::SS) * KB + lane % W::SS) * 4, lk * 4);
     }
+    lgroup = lgroup + 1 == W::S ? 0 : lgroup + 1;
+  };
+  constexpr int kLoads = W::LT + 2 * W::LW;
+  auto load = [&](int copy, int i0, int i1) {  // loads [i0, i1) of step lk
 #pragma unroll
-    for (int j = 0; j < W::LT; ++j)
-      load16_to_lds(ra, rows0 + copy * W::kStage + (wave * (BM / kWideWaves) + j * 8) * kStepBytes,
-                    at_row + (uint32_t)(wave * (BM / kWideWaves) + j * 8) * K, lk * kStepBytes);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < W::LW; ++j)
-        load16_to_lds(rb,
-                      rows0 + copy * W::kStage + W::kT +
-                          (h * kHalf + wave * (kHalf / kWideWaves) + j * 8) * kStepBytes,
-                      at_row + (uint32_t)(first_col(nxt) + (h ? (SWIGLU ? outs : kHalf) : 0) +
-                                          wave * (kHalf / kWideWaves) + j * 8) * K,
+    for (int i = 0; i < kLoads; ++i) {
+      if (i < i0 || i >= i1) continue;
+      if (i < W::LT) {
+        const int r = wave * (BM / kWideWaves) + i * 8;
+        load16_to_lds(ra, rows0 + copy * W::kStage + r * kStepBytes, at_row + (uint32_t)r * K, lk * kStepBytes);
+      } else {
+        const int h = (i - W::LT) / W::LW, j = (i - W::LT) % W::LW;
+        const int r = wave * (kHalf / kWideWaves) + j * 8;
+        load16_to_lds(rb, rows0 + copy * W::kStage + W::kT + (h * kHalf + r) * kStepBytes,
+                      at_row + (uint32_t)(first_col(nxt) + (h ? (SWIGLU ? outs : kHalf) : 0) + r) * K,
                       lk * kStepBytes);
+      }
+    }
   };
 
   // ---- the products
@@ -218,18 +227,25 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
     v0 = s_sb[tile][0][k];
     v1 = s_sb[tile][up][k];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) v[m] = s_sa[group][((wm * MT + m) * 16 + col) * kScaleSteps + k % kScaleSteps];
+    for (int m = 0; m < MT; ++m) v[m] = s_sa[group][((wm * MT + m) * 16 + col) * W::SS + k % W::SS];
   };
+  // The loads of a step are issued two with each weight tile's products: all
+  // at once they would hold the waves up until the memory pipeline has taken
+  // 64 KiB, a third of a step, with the matrix cores idle.
+  constexpr int kPairs = (kLoads + 1) / 2, kEarly = 2 * 2;  // the first two pairs before the step's end
+  static_assert(kPairs <= NT, "the loads are out before the next barrier");
   // The products of weight tiles [N0, N1) of the step in `stage`.  The rows of
   // the weight tile two ahead are read meanwhile, those of the next step from
   // its copy; and each token tile's of the next step once its last product has
   // started.  The scheduling barriers keep this order (left alone, the
   // compiler reads all tiles first and spills).
-  auto products = [&](const uint8_t* stage, const uint8_t* next, int N0, int N1) {
+  auto products = [&](const uint8_t* stage, const uint8_t* next, int N0, int N1, int copy, bool loads) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       if (n < N0 || n >= N1) continue;
       __builtin_amdgcn_sched_barrier(0);
+      const int pair = n >= NT - 2 ? n - (NT - 2) : n + 2;
+      if (pair < kPairs && loads) load(copy, 2 * pair, 2 * pair + 2);
       w[(n + 2) & 3] = n + 2 < NT ? frag(weight_rows(stage, n + 2)) : frag(weight_rows(next, n + 2 - NT));
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -287,7 +303,7 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
         top = fmaxf(top, __shfl_xor(top, 32, kWave));
         if (quad == 0) s_max[wn][(wm * MT + m) * 16 + col] = top;
       }
-      wide_barrier<false>();
+      wide_barrier<63>();
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const int r = (wm * MT + m) * 16 + col;
@@ -317,16 +333,17 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
 
   aim();
   cur = nxt;
-  load(0);
-  ++lk;
-  load(1);
-  ++lk;
-  wide_barrier<true>();
+  for (; lk < W::S; ++lk) {
+    if (lk % W::SS == 0) load_scales();
+    load(lk, 0, kLoads);
+  }
+  wide_barrier<0>();
   bool fresh = true;  // the current step is a tile's first
   bool live = false;  // waves past the tile's last row only load
-  for (int copy = 0;; copy ^= 1) {  // step kb of the current tile
+  for (int copy = 0, prev = W::S - 1;; prev = copy, copy = copy + 1 == W::S ? 0 : copy + 1) {
+    // step kb of the current tile
     uint8_t* const stage = s_rows + copy * W::kStage;
-    uint8_t* const next = s_rows + (copy ^ 1) * W::kStage;
+    uint8_t* const next = s_rows + (copy + 1 == W::S ? 0 : copy + 1) * W::kStage;
     if (fresh) {
       live = wm * MT * 16 < (int)(cur.r1 - cur.r0);
       if (live) {
@@ -337,11 +354,14 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
         read_scales(cur, ctile, cgroup, kb);
       }
     }
-    if (live) products(stage, next, 0, NT - 2);
-    wide_barrier<true>();
+    // and the rest of the loads that the step before began, into its copy
+    if (live) products(stage, next, 0, NT - 2, prev, !fresh);
+    else if (!fresh) load(prev, kEarly, kLoads);
+    if (!fresh) ++lk;
+    wide_barrier<(W::S - 2) * kLoads>();  // the next step's tiles are here; those after may be on the way
     if (kb + 1 == full && full < KB) {
       clear_tail(next, BM + kWideCols);
-      wide_barrier<false>();
+      wide_barrier<63>();
     }
     if (lk == KB) {
       lk = 0;
@@ -351,17 +371,20 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
       if (!more) id -= stride;  // the stream loads its last tile again
       aim();
     }
-    load(copy);
-    ++lk;
+    if (lk % W::SS == 0) load_scales();
     ++kb;
     const bool last = kb == KB;
-    if (last || kb % kScaleSteps == 0) cgroup ^= 1;
+    if (last || kb % W::SS == 0) cgroup = cgroup + 1 == W::S ? 0 : cgroup + 1;
     if (live) {
       if (!last) read_scales(cur, ctile, cgroup, kb);  // the next step's
-      products(stage, next, NT - 2, NT);
+      products(stage, next, NT - 2, NT, copy, true);
+    } else {
+      load(copy, 0, kEarly);
     }
     fresh = last;
     if (last) {
+      load(copy, kEarly, kLoads);
+      ++lk;
 #pragma unroll
       for (int q = NT * MT - kLag; q < NT * MT; ++q) add(q);
       finish();
@@ -406,8 +429,9 @@ hipError_t launch(const Budget& b, const GroupedArgs& g, hipStream_t stream) {
 }  // namespace
 
 bool grouped_wide_fits(const GroupedArgs& g) {
+  // (a tile shorter than the copies would be two tiles ahead of its results)
   const int blocks = scale_blocks(g.K);
-  return blocks >= 2 && blocks <= kWideMaxBlocks;  // (a tile of one step would be two tiles ahead of its results)
+  return blocks >= Wide<128>::S && blocks <= kWideMaxBlocks;
 }
 
 hipError_t launch_grouped_wide(const Budget& b, const GroupedArgs& g, bool swiglu, int bm, hipStream_t stream) {
