@@ -191,10 +191,24 @@ __global__ __launch_bounds__(kNarrowWaves * kWave) void grouped_narrow_kernel(Gr
 
 }  // namespace
 
+// Token rows per workgroup of the wide kernel.  A tile of 256 takes 1.6 times
+// as long as one of 128 where the products bound it, so the choice goes by the
+// rounds of tiles that the compute units make (every expert's last tile is
+// taken as half full).  Measured, 128 against 256: 32 experts, K = N = 4096,
+// 128 rows each 148 / 163 us, 512 each 374 / 348, 2048 each 1365 / 1204; 16
+// experts, swiglu K 2048, I 1024, 128 each 27 / 40 us, 512 each 73 / 77.
+static int wide_rows(const Budget& b, const GroupedArgs& g, bool swiglu) {
+  const int64_t outs = swiglu ? g.N / 2 : g.N, per = swiglu ? 128 : 256;
+  const int64_t units_n = (outs + per - 1) / per, held = g.E < g.rows ? g.E : g.rows;
+  auto rounds = [&](int bm) {
+    const int64_t tiles = units_n * (2 * g.rows / bm + held) / 2;
+    return (tiles + b.device_cus - 1) / b.device_cus;
+  };
+  return 8 * rounds(256) <= 5 * rounds(128) ? 256 : 128;
+}
+
 hipError_t launch_grouped_fp8(const Budget& b, const GroupedArgs& g, bool swiglu, hipStream_t stream) {
-  const int64_t mean = g.rows / g.E;
-  const int bm = mean > 192 ? 256 : 128;
-  if (mean >= 32 && grouped_wide_fits(g)) return launch_grouped_wide(b, g, swiglu, bm, stream);
+  if (grouped_wide_fits(g)) return launch_grouped_wide(b, g, swiglu, wide_rows(b, g, swiglu), stream);
   const int units_n = swiglu ? (g.N / 2 + kNarrowCols - 1) / kNarrowCols : (g.N + 2 * kNarrowCols - 1) / (2 * kNarrowCols);
   // one workgroup for each tile there can be: every expert may end inside one
   const int64_t tiles = g.rows / kNarrowRows + (g.E < g.rows ? g.E : g.rows);
