@@ -1,9 +1,14 @@
 // ep_dispatch_fp8: recv_q[dest_row[t, j], :] = e4m3(x[t, :] * (448 / amax)), one
 // amax (and scale amax / 448) for each 128 values.
 //
-// A wave takes a token: a lane's 16-byte load holds 8 values, so a block is 16
-// lanes, its maximum four exchanges inside them.  The row is read and rounded
-// once and stored k times.
+// A unit is (token, slab): a wave reads VPL 16-byte vectors per lane of a row,
+// all in flight together, rounds them once and stores the slab k times.  A
+// lane's vector holds 8 values, so a block is 16 lanes and its maximum four
+// exchanges inside them.  The slab's scales are gathered through LDS into
+// neighbouring lanes, so that a copy's scales are one store.
+//
+// The kernel is bound by the bytes it moves, three quarters of them writes at
+// k = 6.
 #include "expert_internal.hpp"
 #include "fp8_device.hpp"
 
@@ -11,42 +16,93 @@ namespace ep {
 
 namespace {
 
-__global__ __launch_bounds__(256) void dispatch_fp8_kernel(const u32x4* __restrict__ x, u32x2* __restrict__ q,
-                                                           float* __restrict__ scale,
-                                                           const int32_t* __restrict__ dest_row, int64_t recv_rows,
-                                                           int row_vec, int blocks, int k, int T) {
+constexpr int kMaxVpl = 16;
+constexpr int kWaves = 4;                // waves per workgroup
+constexpr int64_t kMaxGrid = 1 << 22;  // workgroups of one launch
+
+template <int VPL>
+__global__ __launch_bounds__(kWaves * kWave) void dispatch_fp8_kernel(const u32x4* __restrict__ x,
+                                                                      u32x2* __restrict__ q,
+                                                                      float* __restrict__ scale,
+                                                                      const int32_t* __restrict__ dest_row,
+                                                                      int64_t recv_rows, int row_vec, int blocks,
+                                                                      int k, int nslab, int units) {
+  __shared__ float s_scale[kWaves][4 * VPL];
   const int lane = lane_id();
-  const int wpg = blockDim.x >> 6;
-  const int64_t stride = (int64_t)gridDim.x * wpg;
-  for (int64_t t = (int64_t)blockIdx.x * wpg + wave_in_group(); t < T; t += stride) {
-    const int32_t* dr = dest_row + t * k;
-    for (int c0 = 0; c0 < row_vec; c0 += kWave) {
-      const int c = c0 + lane;
-      const bool in = c < row_vec;
-      u32x4 v = {0u, 0u, 0u, 0u};
-      if (in) v = ld16<true>(x + t * row_vec + c);
-      float f[8], m = kAmaxFloor;
+  const int wave = wave_in_group();
+  const int stride = gridDim.x * kWaves;
+  for (int64_t u = (int64_t)blockIdx.x * kWaves + wave; u < units; u += stride) {
+    const int t = (int)u / nslab;
+    const int c0 = ((int)u - t * nslab) * (VPL * kWave);
+    const u32x4* src = x + (int64_t)t * row_vec;
+    u32x4 v[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int c = c0 + i * kWave + lane;
+      v[i] = ld16<true>(src + (c < row_vec ? c : row_vec - 1));
+    }
+    u32x2 o[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const bool in = c0 + i * kWave + lane < row_vec;
+      float f[8], m = 0.0f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        f[2 * e] = bf16_lo(v[e]);
-        f[2 * e + 1] = bf16_hi(v[e]);
+        f[2 * e] = bf16_lo(v[i][e]);
+        f[2 * e + 1] = bf16_hi(v[i][e]);
         m = fmaxf(m, fmaxf(fabsf(f[2 * e]), fabsf(f[2 * e + 1])));
       }
+      m = in ? fmaxf(m, kAmaxFloor) : kAmaxFloor;  // lanes past the row's end hold its last values again
 #pragma unroll
       for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, kWave));
       const float inv = block_inverse(m);
-      const u32x2 o = {pack_e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                       pack_e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv)};
-      const float s = block_scale(m);
-      for (int j = 0; j < k; ++j) {
-        const int64_t d = dr[j];
-        if ((uint64_t)d >= (uint64_t)recv_rows) continue;
-        if (in) {
-          q[d * row_vec + c] = o;
-          if ((lane & 15) == 0) scale[d * blocks + c / 16] = s;
-        }
-      }
+      o[i] = u32x2{pack_e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+                   pack_e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv)};
+      if ((lane & 15) == 0) s_scale[wave][4 * i + (lane >> 4)] = block_scale(m);
     }
+    // (the wave's own LDS accesses keep their order; this keeps the compiler's)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const int b0 = c0 / 16;
+    const bool holds = lane < 4 * VPL && b0 + lane < blocks;
+    const float s = lane < 4 * VPL ? s_scale[wave][lane] : 0.0f;
+    const int32_t* dr = dest_row + (int64_t)t * k;
+    for (int j = 0; j < k; ++j) {
+      const int64_t d = dr[j];
+      if ((uint64_t)d >= (uint64_t)recv_rows) continue;
+      u32x2* out = q + d * row_vec;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const int c = c0 + i * kWave + lane;
+        if (c < row_vec) __builtin_nontemporal_store(o[i], out + c);
+      }
+      if (holds) scale[d * blocks + b0 + lane] = s;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+using Fn = void (*)(const u32x4*, u32x2*, float*, const int32_t*, int64_t, int, int, int, int, int);
+
+Fn pick(int vpl) {
+  switch (vpl) {
+    case 1: return dispatch_fp8_kernel<1>;
+    case 2: return dispatch_fp8_kernel<2>;
+    case 3: return dispatch_fp8_kernel<3>;
+    case 4: return dispatch_fp8_kernel<4>;
+    case 5: return dispatch_fp8_kernel<5>;
+    case 6: return dispatch_fp8_kernel<6>;
+    case 7: return dispatch_fp8_kernel<7>;
+    case 8: return dispatch_fp8_kernel<8>;
+    case 9: return dispatch_fp8_kernel<9>;
+    case 10: return dispatch_fp8_kernel<10>;
+    case 11: return dispatch_fp8_kernel<11>;
+    case 12: return dispatch_fp8_kernel<12>;
+    case 13: return dispatch_fp8_kernel<13>;
+    case 14: return dispatch_fp8_kernel<14>;
+    case 15: return dispatch_fp8_kernel<15>;
+    default: return dispatch_fp8_kernel<16>;
   }
 }
 
@@ -54,18 +110,32 @@ __global__ __launch_bounds__(256) void dispatch_fp8_kernel(const u32x4* __restri
 
 hipError_t launch_dispatch_fp8(const Budget& b, const void* x, int T, int H, const int32_t* dest_row, int k,
                                void* recv_q, float* recv_scale, int64_t recv_rows, hipStream_t stream) {
-  int grid = (T + 3) / 4;
+  const int row_vec = H / 8, nv = (row_vec + kWave - 1) / kWave;
+  const bool budget = b.num_cus > 0;
+  const int cus = budget && b.num_cus < b.device_cus ? b.num_cus : b.device_cus;
+  // Whole rows up to 16 KiB; a small batch takes shorter slabs, down to 1 KiB,
+  // until every CU has 8 waves of them.
+  int64_t want = (int64_t)T * nv / (8 * cus);
+  if (want < 1) want = 1;
+  int nslab = (nv + kMaxVpl - 1) / kMaxVpl;
+  if (want < (nv + nslab - 1) / nslab) nslab = (nv + (int)want - 1) / (int)want;
+  const int vpl = (nv + nslab - 1) / nslab;
+  nslab = (nv + vpl - 1) / vpl;
+  const int units = T * nslab;  // at most EP_MAX_ENTRIES (checked by the ABI)
+  Fn fn = pick(vpl);
+  int64_t grid = ((int64_t)units + kWaves - 1) / kWaves;
   size_t lds = 0;
-  if (b.num_cus > 0) {
-    grid = b.num_cus < b.device_cus ? b.num_cus : b.device_cus;
+  if (budget) {
+    grid = cus;
     lds = kExclusiveLds;
-    hipError_t e = allow_dynamic_lds((const void*)dispatch_fp8_kernel, lds);
+    hipError_t e = allow_dynamic_lds((const void*)fn, lds);
     if (e != hipSuccess) return e;
-  } else if (grid > 8 * b.device_cus) {
-    grid = 8 * b.device_cus;
+  } else if (grid > kMaxGrid) {
+    grid = kMaxGrid;
   }
-  hipLaunchKernelGGL(dispatch_fp8_kernel, dim3(grid), dim3(256), lds, stream, static_cast<const u32x4*>(x),
-                     static_cast<u32x2*>(recv_q), recv_scale, dest_row, recv_rows, H / 8, scale_blocks(H), k, T);
+  hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(kWaves * kWave), lds, stream, static_cast<const u32x4*>(x),
+                     static_cast<u32x2*>(recv_q), recv_scale, dest_row, recv_rows, row_vec, scale_blocks(H), k, nslab,
+                     units);
   return hipGetLastError();
 }
 
