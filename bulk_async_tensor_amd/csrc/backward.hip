@@ -30,7 +30,7 @@ constexpr int kMaxVpl = 16;
 
 // VPL vectors per lane of both rows in flight together; rows of more than 16
 // KiB in nslab slabs.
-template <int VPL, bool DY, bool DW>
+template <int VPL, bool NT, bool DY, bool DW>
 __global__ __launch_bounds__(512) void combine_backward_kernel(const u32x4* __restrict__ dout,
                                                                const u32x4* __restrict__ y, u32x4* __restrict__ dy,
                                                                float* __restrict__ dw,
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(512) void combine_backward_kernel(const u32x4* __re
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
           const int c = c0 + i * kWave;
-          yv[i] = ld16<true>(yr + (c < row_vec ? c : row_vec - 1));
+          yv[i] = ld16<NT>(yr + (c < row_vec ? c : row_vec - 1));
         }
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
@@ -97,7 +97,7 @@ __global__ __launch_bounds__(512) void combine_backward_kernel(const u32x4* __re
 // A unit is one of nseg segments of STEPS * VS vectors per lane of a token's
 // row.  A step gathers VS vectors from KS rows at a time (8 loads in flight,
 // and the next step's where registers allow); ONE: k is at most KS.
-template <int KS, int VS, int STEPS, bool ONE>
+template <int KS, int VS, int STEPS, bool ONE, bool NT>
 __global__ __launch_bounds__(256) void dispatch_backward_kernel(const u32x4* __restrict__ drecv,
                                                                 u32x4* __restrict__ dx,
                                                                 const int32_t* __restrict__ dest_row,
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(256) void dispatch_backward_kernel(const u32x4* __r
 #pragma unroll
           for (int i = 0; i < VS; ++i) {
             const int c = c0 + (s * VS + i) * kWave;
-            v[j][i] = ld16<true>(src + (c < row_vec ? c : row_vec - 1));
+            v[j][i] = ld16<NT>(src + (c < row_vec ? c : row_vec - 1));
           }
         }
 #pragma unroll
@@ -181,53 +181,63 @@ using CombineFn = void (*)(const u32x4*, const u32x4*, u32x4*, float*, const int
                            int, int64_t);
 
 template <int VPL>
-CombineFn pick_outputs(bool dy, bool dw) {
-  return !dw ? combine_backward_kernel<VPL, true, false>
-             : !dy ? combine_backward_kernel<VPL, false, true> : combine_backward_kernel<VPL, true, true>;
+CombineFn pick_outputs(bool nt, bool dy, bool dw) {
+  if (!dw) return combine_backward_kernel<VPL, false, true, false>;  // reads no y
+  if (!dy) return nt ? combine_backward_kernel<VPL, true, false, true> : combine_backward_kernel<VPL, false, false, true>;
+  return nt ? combine_backward_kernel<VPL, true, true, true> : combine_backward_kernel<VPL, false, true, true>;
 }
 
-CombineFn pick_combine(int vpl, bool dy, bool dw) {
+CombineFn pick_combine(int vpl, bool nt, bool dy, bool dw) {
   switch (vpl) {
-    case 1: return pick_outputs<1>(dy, dw);
-    case 2: return pick_outputs<2>(dy, dw);
-    case 3: return pick_outputs<3>(dy, dw);
-    case 4: return pick_outputs<4>(dy, dw);
-    case 5: return pick_outputs<5>(dy, dw);
-    case 6: return pick_outputs<6>(dy, dw);
-    case 7: return pick_outputs<7>(dy, dw);
-    case 8: return pick_outputs<8>(dy, dw);
+    case 1: return pick_outputs<1>(nt, dy, dw);
+    case 2: return pick_outputs<2>(nt, dy, dw);
+    case 3: return pick_outputs<3>(nt, dy, dw);
+    case 4: return pick_outputs<4>(nt, dy, dw);
+    case 5: return pick_outputs<5>(nt, dy, dw);
+    case 6: return pick_outputs<6>(nt, dy, dw);
+    case 7: return pick_outputs<7>(nt, dy, dw);
+    case 8: return pick_outputs<8>(nt, dy, dw);
     case 9:
-    case 10: return pick_outputs<10>(dy, dw);
+    case 10: return pick_outputs<10>(nt, dy, dw);
     case 11:
-    case 12: return pick_outputs<12>(dy, dw);
+    case 12: return pick_outputs<12>(nt, dy, dw);
     case 13:
-    case 14: return pick_outputs<14>(dy, dw);
-    default: return pick_outputs<16>(dy, dw);
+    case 14: return pick_outputs<14>(nt, dy, dw);
+    default: return pick_outputs<16>(nt, dy, dw);
   }
 }
 
 using DispatchFn = void (*)(const u32x4*, u32x4*, const int32_t*, int64_t, int, int, int, int, int);
 
 // Segments of `steps` steps (a last step may be partly past the row's end).
-template <int KS, int VS, bool ONE>
+template <int KS, int VS, bool ONE, bool NT>
 DispatchFn pick_steps(int steps) {
   switch (steps) {
-    case 1: return dispatch_backward_kernel<KS, VS, 1, ONE>;
-    case 2: return dispatch_backward_kernel<KS, VS, 2, ONE>;
+    case 1: return dispatch_backward_kernel<KS, VS, 1, ONE, NT>;
+    case 2: return dispatch_backward_kernel<KS, VS, 2, ONE, NT>;
     case 3:
-      if constexpr (VS <= 2) return dispatch_backward_kernel<KS, VS, 3, ONE>;
+      if constexpr (VS <= 2) return dispatch_backward_kernel<KS, VS, 3, ONE, NT>;
     case 4:
-      if constexpr (VS <= 2) return dispatch_backward_kernel<KS, VS, 4, ONE>;
+      if constexpr (VS <= 2) return dispatch_backward_kernel<KS, VS, 4, ONE, NT>;
     case 5:
-      if constexpr (VS == 1) return dispatch_backward_kernel<KS, VS, 5, ONE>;
+      if constexpr (VS == 1) return dispatch_backward_kernel<KS, VS, 5, ONE, NT>;
     case 6:
-      if constexpr (VS == 1) return dispatch_backward_kernel<KS, VS, 6, ONE>;
+      if constexpr (VS == 1) return dispatch_backward_kernel<KS, VS, 6, ONE, NT>;
     case 7:
-      if constexpr (VS == 1) return dispatch_backward_kernel<KS, VS, 7, ONE>;
+      if constexpr (VS == 1) return dispatch_backward_kernel<KS, VS, 7, ONE, NT>;
     default:
-      if constexpr (VS == 1) return dispatch_backward_kernel<KS, VS, 8, ONE>;
+      if constexpr (VS == 1) return dispatch_backward_kernel<KS, VS, 8, ONE, NT>;
       else return nullptr;
   }
+}
+
+template <bool NT>
+DispatchFn pick_dispatch(int k, int steps) {
+  return k == 1   ? pick_steps<1, 4, true, NT>(steps)
+         : k == 2 ? pick_steps<2, 4, true, NT>(steps)
+         : k <= 4 ? pick_steps<4, 2, true, NT>(steps)
+         : k <= 8 ? pick_steps<8, 1, true, NT>(steps)
+                  : pick_steps<8, 1, false, NT>(steps);
 }
 
 }  // namespace
@@ -238,7 +248,7 @@ hipError_t launch_combine_backward(const Budget& b, const void* dout, const void
   const int row_vec = H / 8, nv = (row_vec + kWave - 1) / kWave;
   const int nslab = (nv + kMaxVpl - 1) / kMaxVpl;
   const int vpl = nslab == 1 ? nv : kMaxVpl;
-  const CombineFn fn = pick_combine(vpl, dy != nullptr, dw != nullptr);
+  const CombineFn fn = pick_combine(vpl, stream_rows((int64_t)T * k * H * 2), dy != nullptr, dw != nullptr);
   const int64_t entries = (int64_t)T * k;
   // a workgroup is one token, so that its row comes from HBM once (two at k = 2 and 3, four at 1)
   const int wpg = k <= 2 ? 4 : k == 3 ? 6 : k > 8 ? 8 : k;
@@ -266,11 +276,7 @@ hipError_t launch_dispatch_backward(const Budget& b, const void* drecv, int64_t 
   const int vs = k <= 2 ? 4 : k <= 4 ? 2 : 1;
   const int nsteps = (nv + vs - 1) / vs, nseg = (nsteps * vs + most - 1) / most;
   const int steps = (nsteps + nseg - 1) / nseg;
-  const DispatchFn fn = k == 1   ? pick_steps<1, 4, true>(steps)
-                        : k == 2 ? pick_steps<2, 4, true>(steps)
-                        : k <= 4 ? pick_steps<4, 2, true>(steps)
-                        : k <= 8 ? pick_steps<8, 1, true>(steps)
-                                 : pick_steps<8, 1, false>(steps);
+  const DispatchFn fn = stream_rows((int64_t)T * k * H * 2) ? pick_dispatch<true>(k, steps) : pick_dispatch<false>(k, steps);
   if (!fn) return hipErrorInvalidValue;
   const int units = T * nseg;  // at most EP_MAX_ENTRIES (checked by the ABI)
   constexpr int kWaves = 4;

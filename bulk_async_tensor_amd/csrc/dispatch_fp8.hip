@@ -20,7 +20,7 @@ constexpr int kMaxVpl = 16;
 constexpr int kWaves = 4;                // waves per workgroup
 constexpr int64_t kMaxGrid = 1 << 22;  // workgroups of one launch
 
-template <int VPL>
+template <int VPL, bool NT>
 __global__ __launch_bounds__(kWaves * kWave) void dispatch_fp8_kernel(const u32x4* __restrict__ x,
                                                                       u32x2* __restrict__ q,
                                                                       float* __restrict__ scale,
@@ -39,7 +39,7 @@ __global__ __launch_bounds__(kWaves * kWave) void dispatch_fp8_kernel(const u32x
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int c = c0 + i * kWave + lane;
-      v[i] = ld16<true>(src + (c < row_vec ? c : row_vec - 1));
+      v[i] = ld16<NT>(src + (c < row_vec ? c : row_vec - 1));
     }
     u32x2 o[VPL];
 #pragma unroll
@@ -85,24 +85,25 @@ __global__ __launch_bounds__(kWaves * kWave) void dispatch_fp8_kernel(const u32x
 
 using Fn = void (*)(const u32x4*, u32x2*, float*, const int32_t*, int64_t, int, int, int, int, int);
 
+template <bool NT>
 Fn pick(int vpl) {
   switch (vpl) {
-    case 1: return dispatch_fp8_kernel<1>;
-    case 2: return dispatch_fp8_kernel<2>;
-    case 3: return dispatch_fp8_kernel<3>;
-    case 4: return dispatch_fp8_kernel<4>;
-    case 5: return dispatch_fp8_kernel<5>;
-    case 6: return dispatch_fp8_kernel<6>;
-    case 7: return dispatch_fp8_kernel<7>;
-    case 8: return dispatch_fp8_kernel<8>;
-    case 9: return dispatch_fp8_kernel<9>;
-    case 10: return dispatch_fp8_kernel<10>;
-    case 11: return dispatch_fp8_kernel<11>;
-    case 12: return dispatch_fp8_kernel<12>;
-    case 13: return dispatch_fp8_kernel<13>;
-    case 14: return dispatch_fp8_kernel<14>;
-    case 15: return dispatch_fp8_kernel<15>;
-    default: return dispatch_fp8_kernel<16>;
+    case 1: return dispatch_fp8_kernel<1, NT>;
+    case 2: return dispatch_fp8_kernel<2, NT>;
+    case 3: return dispatch_fp8_kernel<3, NT>;
+    case 4: return dispatch_fp8_kernel<4, NT>;
+    case 5: return dispatch_fp8_kernel<5, NT>;
+    case 6: return dispatch_fp8_kernel<6, NT>;
+    case 7: return dispatch_fp8_kernel<7, NT>;
+    case 8: return dispatch_fp8_kernel<8, NT>;
+    case 9: return dispatch_fp8_kernel<9, NT>;
+    case 10: return dispatch_fp8_kernel<10, NT>;
+    case 11: return dispatch_fp8_kernel<11, NT>;
+    case 12: return dispatch_fp8_kernel<12, NT>;
+    case 13: return dispatch_fp8_kernel<13, NT>;
+    case 14: return dispatch_fp8_kernel<14, NT>;
+    case 15: return dispatch_fp8_kernel<15, NT>;
+    default: return dispatch_fp8_kernel<16, NT>;
   }
 }
 
@@ -122,7 +123,7 @@ hipError_t launch_dispatch_fp8(const Budget& b, const void* x, int T, int H, con
   const int vpl = (nv + nslab - 1) / nslab;
   nslab = (nv + vpl - 1) / vpl;
   const int units = T * nslab;  // at most EP_MAX_ENTRIES (checked by the ABI)
-  Fn fn = pick(vpl);
+  Fn fn = stream_rows((int64_t)T * H * 2) ? pick<true>(vpl) : pick<false>(vpl);
   int64_t grid = ((int64_t)units + kWaves - 1) / kWaves;
   size_t lds = 0;
   if (budget) {

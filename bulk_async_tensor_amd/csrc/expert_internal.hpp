@@ -9,6 +9,14 @@ namespace ep {
 constexpr int kScaleBlock = 128;  // values that share a scale (the ABI's EP_FP8_BLOCK)
 inline __host__ __device__ int scale_blocks(int n) { return (n + kScaleBlock - 1) / kScaleBlock; }
 
+// Whether the row movers stream their source rows (non-temporal loads) or load
+// them through the caches: the step before has just written them, so a source
+// that the 256 MB Infinity Cache holds is mostly still there.  Streamed
+// against cached, us: 8-bit dispatch of 59 MB (T = 4096, H = 7168, k = 8) 59 /
+// 52, of 235 MB 187 / 192; combine_backward with 34 MB of y 16 / 13, 67 MB 28
+// / 26, 470 MB 187 / 199; dispatch_backward of 67 MB 17 / 16, 470 MB 89 / 99.
+inline bool stream_rows(int64_t bytes) { return bytes > (int64_t)128 << 20; }
+
 // ---- dispatch_fp8.hip
 hipError_t launch_dispatch_fp8(const Budget& b, const void* x, int T, int H, const int32_t* dest_row, int k,
                                void* recv_q, float* recv_scale, int64_t recv_rows, hipStream_t stream);
