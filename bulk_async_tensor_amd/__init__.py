@@ -384,35 +384,69 @@ def ep_combine_reduce(y, src_token, dest_row, topk_w, out, workspace=None, strea
 
 
 # ------------------------------------------------------------------ expert side
+# These calls are small next to their launch, so their checks are kept short:
+# the dtypes and torch's raw accessors are looked up once, and one pass over a
+# tensor's attributes both checks it and gives its device.
+class _Torch:
+    """torch's objects that the expert side's calls use."""
+
+    def __init__(self):
+        import torch
+
+        lib()
+        self.bf16, self.f32, self.i32, self.f8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+        self.device = torch.cuda.device
+        self.current_device = torch.cuda.current_device
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+_torch = None
+
+
+def _torch_objects():
+    global _torch
+    if _torch is None or _lib is None:
+        _torch = _Torch()
+    return _torch
+
+
 def _blocks(n):
     return (n + EP_FP8_BLOCK - 1) // EP_FP8_BLOCK
 
 
-def _one_device(what, first, *others):
-    """The device index that every tensor given (None: not given) is on."""
-    dev = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{what}: the tensors are on different devices")
-    return dev
+def _operand(t, name, dtype):
+    """The device index of a contiguous device tensor of that dtype."""
+    try:
+        if t.dtype is dtype and t.is_contiguous():
+            dev = t.get_device()
+            if dev >= 0:
+                return dev
+    except AttributeError:
+        pass
+    _device_tensor(t, name, dtype)
+    return t.get_device()
 
 
-def _call_on(dev, stream, name, args):
-    """Calls entry point `name` with the current device set to `dev`, on the
-    given stream or on the current stream of that device."""
-    import torch
-
-    fn = getattr(_lib or lib(), name)
-    if stream is not None:
+def _call_on(th, devices, stream, name, args):
+    """Calls entry point `name` with the tensors' device as the current one, on
+    the given stream or on the current stream of that device."""
+    dev = devices[0]
+    if devices.count(dev) != len(devices):
+        raise ValueError(f"{name}: the tensors are on different devices")
+    if stream is None:
+        handle = th.raw_stream(dev)
+    else:
         if stream.device.index is not None and stream.device.index != dev:
             raise ValueError(f"{name}: the stream belongs to another device than the tensors")
         handle = stream.cuda_stream
+    fn = getattr(_lib, name)
+    if th.current_device() == dev:
+        rc = fn(*args, handle)
     else:
-        handle = torch._C._cuda_getCurrentRawStream(dev)
-    if torch.cuda.current_device() == dev:
-        return _check(fn(*args, handle), name)
-    with torch.cuda.device(dev):
-        return _check(fn(*args, handle), name)
+        with th.device(dev):
+            rc = fn(*args, handle)
+    if rc < 0:
+        _check(rc, name)
 
 
 def ep_dispatch_fp8(x, dest_row, recv_q, recv_scale, stream=None):
@@ -420,43 +454,35 @@ def ep_dispatch_fp8(x, dest_row, recv_q, recv_scale, stream=None):
     float32 scale for each 128 values: x [T, H] bf16, dest_row [T, k] int32,
     recv_q [R, H] float8_e4m3fn, recv_scale [R, ceil(H / 128)] float32.
     Returns (recv_q, recv_scale)."""
-    import torch
-
-    _device_tensor(x, "x", torch.bfloat16)
-    _device_tensor(dest_row, "dest_row", torch.int32)
-    _device_tensor(recv_q, "recv_q", torch.float8_e4m3fn)
-    _device_tensor(recv_scale, "recv_scale", torch.float32)
-    if x.dim() != 2 or dest_row.dim() != 2 or dest_row.shape[0] != x.shape[0]:
+    th = _torch_objects()
+    devices = (_operand(x, "x", th.bf16), _operand(dest_row, "dest_row", th.i32), _operand(recv_q, "recv_q", th.f8),
+               _operand(recv_scale, "recv_scale", th.f32))
+    xs, ds, qs = x.shape, dest_row.shape, recv_q.shape
+    if len(xs) != 2 or len(ds) != 2 or ds[0] != xs[0]:
         raise ValueError("x must be [T, H] and dest_row [T, k]")
-    T, H = x.shape
-    if recv_q.dim() != 2 or recv_q.shape[1] != H or tuple(recv_scale.shape) != (recv_q.shape[0], _blocks(H)):
+    T, H = xs
+    if len(qs) != 2 or qs[1] != H or recv_scale.shape != (qs[0], _blocks(H)):
         raise ValueError("recv_q must be [R, H] and recv_scale [R, ceil(H / 128)]")
-    dev = _one_device("ep_dispatch_fp8", x, dest_row, recv_q, recv_scale)
-    _call_on(dev, stream, "ep_dispatch_fp8", (x.data_ptr(), T, H, dest_row.data_ptr(), dest_row.shape[1],
-                                              recv_q.data_ptr(), recv_scale.data_ptr(), recv_q.shape[0]))
+    _call_on(th, devices, stream, "ep_dispatch_fp8", (x.data_ptr(), T, H, dest_row.data_ptr(), ds[1],
+                                                      recv_q.data_ptr(), recv_scale.data_ptr(), qs[0]))
     return recv_q, recv_scale
 
 
-def _grouped(what, a, a_scale, offsets, b, b_scale):
-    """Checks the operands of an expert product; (rows, K, E, weight rows)."""
-    import torch
-
-    _device_tensor(a, "a", torch.float8_e4m3fn)
-    _device_tensor(a_scale, "a_scale", torch.float32)
-    _device_tensor(offsets, "offsets", torch.int32)
-    _device_tensor(b, "b", torch.float8_e4m3fn)
-    _device_tensor(b_scale, "b_scale", torch.float32)
-    if a.dim() != 2 or b.dim() != 3 or b.shape[2] != a.shape[1]:
+def _grouped(th, what, a, a_scale, offsets, b, b_scale):
+    """Checks the operands of an expert product; their devices, and (rows, K, E, weight rows)."""
+    devices = (_operand(a, "a", th.f8), _operand(a_scale, "a_scale", th.f32), _operand(offsets, "offsets", th.i32),
+               _operand(b, "b", th.f8), _operand(b_scale, "b_scale", th.f32))
+    if len(a.shape) != 2 or len(b.shape) != 3 or b.shape[2] != a.shape[1]:
         raise ValueError(f"{what}: a must be [rows, K] and b [E, N, K]")
     rows, K = a.shape
     E, N, _ = b.shape
-    if tuple(a_scale.shape) != (rows, _blocks(K)):
+    if a_scale.shape != (rows, _blocks(K)):
         raise ValueError(f"{what}: a_scale must be [rows, ceil(K / 128)] = [{rows}, {_blocks(K)}]")
-    if tuple(b_scale.shape) != (E, _blocks(N), _blocks(K)):
+    if b_scale.shape != (E, _blocks(N), _blocks(K)):
         raise ValueError(f"{what}: b_scale must be [E, ceil(N / 128), ceil(K / 128)] = [{E}, {_blocks(N)}, {_blocks(K)}]")
-    if offsets.dim() != 1 or offsets.shape[0] != E + 1:
+    if offsets.shape != (E + 1,):
         raise ValueError(f"{what}: offsets must be [E + 1] = [{E + 1}]")
-    return rows, K, E, N
+    return devices, rows, K, E, N
 
 
 def ep_grouped_gemm_fp8(a, a_scale, offsets, b, b_scale, y, stream=None):
@@ -464,15 +490,14 @@ def ep_grouped_gemm_fp8(a, a_scale, offsets, b, b_scale, y, stream=None):
     each expert e: a [rows, K] and b [E, N, K] float8_e4m3fn, their float32
     scales [rows, ceil(K / 128)] and [E, ceil(N / 128), ceil(K / 128)], offsets
     [E + 1] int32 from ep_layout, y [rows, N] bf16.  Returns y."""
-    import torch
-
-    rows, K, E, N = _grouped("ep_grouped_gemm_fp8", a, a_scale, offsets, b, b_scale)
-    _device_tensor(y, "y", torch.bfloat16)
-    if tuple(y.shape) != (rows, N):
+    th = _torch_objects()
+    devices, rows, K, E, N = _grouped(th, "ep_grouped_gemm_fp8", a, a_scale, offsets, b, b_scale)
+    devices += (_operand(y, "y", th.bf16),)
+    if y.shape != (rows, N):
         raise ValueError(f"y must be [rows, N] = [{rows}, {N}]")
-    dev = _one_device("ep_grouped_gemm_fp8", a, a_scale, offsets, b, b_scale, y)
-    _call_on(dev, stream, "ep_grouped_gemm_fp8", (a.data_ptr(), a_scale.data_ptr(), rows, K, offsets.data_ptr(), E,
-                                                  b.data_ptr(), b_scale.data_ptr(), N, y.data_ptr()))
+    _call_on(th, devices, stream, "ep_grouped_gemm_fp8",
+             (a.data_ptr(), a_scale.data_ptr(), rows, K, offsets.data_ptr(), E, b.data_ptr(), b_scale.data_ptr(), N,
+              y.data_ptr()))
     return y
 
 
@@ -481,18 +506,15 @@ def ep_grouped_swiglu_fp8(a, a_scale, offsets, b, b_scale, out_q, out_scale, str
     scales: operands as for ep_grouped_gemm_fp8 with b [E, 2 I, K] (I gate rows,
     then I up rows), out_q [rows, I] float8_e4m3fn, out_scale
     [rows, ceil(I / 128)] float32.  Returns (out_q, out_scale)."""
-    import torch
-
-    rows, K, E, N = _grouped("ep_grouped_swiglu_fp8", a, a_scale, offsets, b, b_scale)
+    th = _torch_objects()
+    devices, rows, K, E, N = _grouped(th, "ep_grouped_swiglu_fp8", a, a_scale, offsets, b, b_scale)
     if N % 2:
         raise ValueError("ep_grouped_swiglu_fp8: b must hold as many gate as up rows")
     I = N // 2
-    _device_tensor(out_q, "out_q", torch.float8_e4m3fn)
-    _device_tensor(out_scale, "out_scale", torch.float32)
-    if tuple(out_q.shape) != (rows, I) or tuple(out_scale.shape) != (rows, _blocks(I)):
+    devices += (_operand(out_q, "out_q", th.f8), _operand(out_scale, "out_scale", th.f32))
+    if out_q.shape != (rows, I) or out_scale.shape != (rows, _blocks(I)):
         raise ValueError(f"out_q must be [rows, I] = [{rows}, {I}] and out_scale [rows, ceil(I / 128)]")
-    dev = _one_device("ep_grouped_swiglu_fp8", a, a_scale, offsets, b, b_scale, out_q, out_scale)
-    _call_on(dev, stream, "ep_grouped_swiglu_fp8",
+    _call_on(th, devices, stream, "ep_grouped_swiglu_fp8",
              (a.data_ptr(), a_scale.data_ptr(), rows, K, offsets.data_ptr(), E, b.data_ptr(), b_scale.data_ptr(), I,
               out_q.data_ptr(), out_scale.data_ptr()))
     return out_q, out_scale
@@ -504,50 +526,55 @@ def ep_combine_backward(dout, y, dest_row, topk_w, dy, dw, stream=None):
     [R, H] bf16, dest_row [T, k] int32, topk_w and dw [T, k] float32.  dy or dw
     may be None (not wanted); y may be None without dw, topk_w without dy.
     Returns (dy, dw)."""
-    import torch
-
-    _device_tensor(dout, "dout", torch.bfloat16)
-    _device_tensor(dest_row, "dest_row", torch.int32)
-    if dout.dim() != 2 or dest_row.dim() != 2 or dest_row.shape[0] != dout.shape[0]:
+    th = _torch_objects()
+    bf16, f32 = th.bf16, th.f32
+    devices = [_operand(dout, "dout", bf16), _operand(dest_row, "dest_row", th.i32)]
+    gs, ds = dout.shape, dest_row.shape
+    if len(gs) != 2 or len(ds) != 2 or ds[0] != gs[0]:
         raise ValueError("dout must be [T, H] and dest_row [T, k]")
-    T, H = dout.shape
-    k = dest_row.shape[1]
-    rows = None
-    for t, name in ((y, "y"), (dy, "dy")):
-        if t is not None:
-            _device_tensor(t, name, torch.bfloat16)
-            if t.dim() != 2 or t.shape[1] != H or (rows is not None and t.shape[0] != rows):
-                raise ValueError(f"{name} must be [R, H]")
-            rows = t.shape[0]
-    for t, name in ((topk_w, "topk_w"), (dw, "dw")):
-        if t is not None:
-            _device_tensor(t, name, torch.float32)
-            if tuple(t.shape) != (T, k):
-                raise ValueError(f"{name} must be [T, k]")
+    T, H = gs
+    rows = yp = dyp = wp = dwp = None
+    if y is not None:
+        devices.append(_operand(y, "y", bf16))
+        rows, yp = y.shape[0], y.data_ptr()
+        if y.shape != (rows, H):
+            raise ValueError("y must be [R, H]")
+    if dy is not None:
+        devices.append(_operand(dy, "dy", bf16))
+        if rows is None:
+            rows = dy.shape[0]
+        if dy.shape != (rows, H):
+            raise ValueError("dy must be [R, H]")
+        dyp = dy.data_ptr()
+    if topk_w is not None:
+        devices.append(_operand(topk_w, "topk_w", f32))
+        if topk_w.shape != ds:
+            raise ValueError("topk_w must be [T, k]")
+        wp = topk_w.data_ptr()
+    if dw is not None:
+        devices.append(_operand(dw, "dw", f32))
+        if dw.shape != ds:
+            raise ValueError("dw must be [T, k]")
+        dwp = dw.data_ptr()
     if rows is None:
         raise ValueError("ep_combine_backward needs y or dy")
-    dev = _one_device("ep_combine_backward", dout, y, dest_row, topk_w, dy, dw)
-    _call_on(dev, stream, "ep_combine_backward", (dout.data_ptr(), _ptr(y), rows, H, dest_row.data_ptr(), _ptr(topk_w),
-                                                  T, k, _ptr(dy), _ptr(dw)))
+    _call_on(th, devices, stream, "ep_combine_backward", (dout.data_ptr(), yp, rows, H, dest_row.data_ptr(), wp, T,
+                                                          ds[1], dyp, dwp))
     return dy, dw
 
 
 def ep_dispatch_backward(drecv, dest_row, dx, stream=None):
     """The gradient of ep_dispatch: dx[t] = bf16(sum_j drecv[dest_row[t, j]]) for
     drecv [R, H] and dx [T, H] bf16, dest_row [T, k] int32.  Returns dx."""
-    import torch
-
-    _device_tensor(drecv, "drecv", torch.bfloat16)
-    _device_tensor(dest_row, "dest_row", torch.int32)
-    _device_tensor(dx, "dx", torch.bfloat16)
-    if dx.dim() != 2 or dest_row.dim() != 2 or dest_row.shape[0] != dx.shape[0]:
+    th = _torch_objects()
+    devices = (_operand(drecv, "drecv", th.bf16), _operand(dest_row, "dest_row", th.i32), _operand(dx, "dx", th.bf16))
+    rs, ds, xs = drecv.shape, dest_row.shape, dx.shape
+    if len(xs) != 2 or len(ds) != 2 or ds[0] != xs[0]:
         raise ValueError("dx must be [T, H] and dest_row [T, k]")
-    T, H = dx.shape
-    if drecv.dim() != 2 or drecv.shape[1] != H:
+    if len(rs) != 2 or rs[1] != xs[1]:
         raise ValueError("drecv must be [R, H]")
-    dev = _one_device("ep_dispatch_backward", drecv, dest_row, dx)
-    _call_on(dev, stream, "ep_dispatch_backward", (drecv.data_ptr(), drecv.shape[0], H, dest_row.data_ptr(), T,
-                                                   dest_row.shape[1], dx.data_ptr()))
+    _call_on(th, devices, stream, "ep_dispatch_backward", (drecv.data_ptr(), rs[0], xs[1], dest_row.data_ptr(), xs[0],
+                                                           ds[1], dx.data_ptr()))
     return dx
 
 
