@@ -29,14 +29,45 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
 }
 
-// 16 x 16 product of 16 rows and 16 columns of 128 e4m3 values, float32 sums,
-// from +0 (v_mfma_f32_16x16x128_f8f6f4, no hardware scales).  Lane l holds 32
-// values of row (column) l % 16: those of its quarter l / 16, in an order that
-// only has to be the same on both sides.  Lane l's result i is row
-// 4 * (l / 16) + i, column l % 16.
+// 16 x 16 product of 16 rows and 16 columns of 128 e4m3 values, from +0
+// (v_mfma_f32_16x16x128_f8f6f4, no hardware scales).  Lane l holds 32 values of
+// row (column) l % 16: those of its quarter l / 16, in an order that only has
+// to be the same on both sides.  Lane l's result i is row 4 * (l / 16) + i,
+// column l % 16.
+//
+// The sum is not a float32 sum throughout: the instruction aligns each 8
+// adjacent products to the largest of them and drops what lies 14 or more
+// binary places below it (measured with powers of two); beyond the 8 it keeps
+// 24 places and more.  On normally distributed values a block's sum is off by
+// 1.35e-5 of its standard deviation, with no bias: a hundredth of a bf16
+// rounding, so results that end as bf16 take this product.
 __device__ __forceinline__ f32x4 mfma_e4m3(i32x8 a, i32x8 b) {
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
+}
+
+// The same product with float32 sums: e4m3 values and their products are exact
+// in bf16 operands, at half the rate.  A quarter of the block (8 values of
+// each lane) per instruction; 9e-9 off.
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+struct Bf16Frag {
+  bf16x8 part[4];
+};
+__device__ __forceinline__ Bf16Frag widen(i32x8 f) {
+  Bf16Frag r;
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const bf16x2 v = h & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * s + h / 2], 1.0f, true)
+                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * s + h / 2], 1.0f, false);
+      r.part[s][2 * h] = v[0];
+      r.part[s][2 * h + 1] = v[1];
+    }
+  return r;
+}
+__device__ __forceinline__ f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
 // Exchanges between the 16-lane rows of a wave (v_permlane16_swap_b32 and

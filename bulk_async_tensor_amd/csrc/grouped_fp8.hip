@@ -130,7 +130,14 @@ __global__ __launch_bounds__(kNarrowWaves * kWave) void grouped_narrow_kernel(Gr
           const float sa = ascale[m][kb];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const f32x4 p = mfma_e4m3(wv[h], av);
+            f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
+            if constexpr (SWIGLU) {  // float32 sums for float32 results
+              const Bf16Frag wb = widen(wv[h]), ab = widen(av);
+#pragma unroll
+              for (int s = 0; s < 4; ++s) p = mfma_bf16(wb.part[s], ab.part[s], p);
+            } else {
+              p = mfma_e4m3(wv[h], av);
+            }
             const float s = sa * wscale[h][kb];
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[h][m][i] = fmaf(p[i], s, acc[h][m][i]);

@@ -206,16 +206,19 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
 
   i32x8 t[MT], w[4];
   f32x4 p[4] = {};
+  Bf16Frag tb[MT];  // SWIGLU
   float s0[MT] = {}, s1[MT] = {}, v[MT], v0, v1;
-  // Product number q of a step (weight tile q / 4, token tile q % 4) is scaled
-  // and added three products after it started, when the matrix core has
-  // finished it: the last three of a step in the next step.
-  constexpr int kLag = 3;
-  auto add = [&](int q) {
-    const int n = (q + NT * MT) % (NT * MT) / MT, m = (q + MT) % MT;
+  auto add = [&](int n, int m, f32x4 v) {
     const float sc = n < HT ? s0[m] : s1[m];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][m][i] = fmaf(p[q & 3][i], sc, acc[n][m][i]);
+    for (int i = 0; i < 4; ++i) acc[n][m][i] = fmaf(v[i], sc, acc[n][m][i]);
+  };
+  auto new_scales = [&]() {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      s0[i] = v[i] * v0;
+      s1[i] = v[i] * v1;
+    }
   };
   auto weight_rows = [&](const uint8_t* stage, int n) {
     return stage + W::kT + (wn * HT * 16 + (n < HT ? n * 16 : kHalf + (n - HT) * 16)) * kStepBytes;
@@ -239,6 +242,14 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
   // its copy; and each token tile's of the next step once its last product has
   // started.  The scheduling barriers keep this order (left alone, the
   // compiler reads all tiles first and spills).
+  //
+  // Plain: product number q of a step (weight tile q / 4, token tile q % 4) is
+  // scaled and added three products after it started, when the matrix core has
+  // finished it: the last three of a step in the next step.  Swiglu, whose
+  // results are float32 and 8-bit values of them, takes the exact products:
+  // both sides are widened to bf16, two token tiles are multiplied together and
+  // added while the next two are.
+  constexpr int kLag = 3;
   auto products = [&](const uint8_t* stage, const uint8_t* next, int N0, int N1, int copy, bool loads) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -247,21 +258,52 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
       const int pair = n >= NT - 2 ? n - (NT - 2) : n + 2;
       if (pair < kPairs && loads) load(copy, 2 * pair, 2 * pair + 2);
       w[(n + 2) & 3] = n + 2 < NT ? frag(weight_rows(stage, n + 2)) : frag(weight_rows(next, n + 2 - NT));
+      if constexpr (SWIGLU) {
+        const Bf16Frag wb = widen(w[n & 3]);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int q = n * MT + m;
-        if (q == kLag)  // the last products of the step before are added: its scales are done
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            s0[i] = v[i] * v0;
-            s1[i] = v[i] * v1;
+        for (int m = 0; m < MT; m += 2) {
+          if (n == 0) {
+            tb[m] = widen(t[m]);
+            tb[m + 1] = widen(t[m + 1]);
           }
-        p[q & 3] = mfma_e4m3(w[n & 3], t[m]);
-        if (n == NT - 1) t[m] = frag(token_rows(next, m));
-        add(q - kLag);
+          f32x4 c0 = {0.0f, 0.0f, 0.0f, 0.0f}, c1 = c0;
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            c0 = mfma_bf16(wb.part[s], tb[m].part[s], c0);
+            c1 = mfma_bf16(wb.part[s], tb[m + 1].part[s], c1);
+          }
+          if (n == NT - 1) {
+            t[m] = frag(token_rows(next, m));
+            t[m + 1] = frag(token_rows(next, m + 1));
+          }
+          const int bn = m ? n : (n + NT - 1) % NT, bm = m ? m - 2 : MT - 2;  // the two before
+          add(bn, bm, p[bm]);
+          add(bn, bm + 1, p[bm + 1]);
+          p[m] = c0;
+          p[m + 1] = c1;
+          if (n == 0 && m == 0) new_scales();
+        }
+      } else {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const int q = n * MT + m, b = (q + NT * MT - kLag) % (NT * MT);
+          if (q == kLag) new_scales();  // the last products of the step before are added
+          p[q & 3] = mfma_e4m3(w[n & 3], t[m]);
+          if (n == NT - 1) t[m] = frag(token_rows(next, m));
+          add(b / MT, b % MT, p[b & 3]);
+        }
       }
     }
     __builtin_amdgcn_sched_barrier(0);
+  };
+  auto drain = [&]() {  // the products that are not added yet
+    if constexpr (SWIGLU) {
+      add(NT - 1, MT - 2, p[MT - 2]);
+      add(NT - 1, MT - 1, p[MT - 1]);
+    } else {
+#pragma unroll
+      for (int q = NT * MT - kLag; q < NT * MT; ++q) add(q / MT, q % MT, p[q & 3]);
+    }
   };
 
   auto finish = [&]() {  // the tile's results
@@ -354,39 +396,61 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
         read_scales(cur, ctile, cgroup, kb);
       }
     }
-    // and the rest of the loads that the step before began, into its copy
-    if (live) products(stage, next, 0, NT - 2, prev, !fresh);
-    else if (!fresh) load(prev, kEarly, kLoads);
-    if (!fresh) ++lk;
-    wide_barrier<(W::S - 2) * kLoads>();  // the next step's tiles are here; those after may be on the way
-    if (kb + 1 == full && full < KB) {
-      clear_tail(next, BM + kWideCols);
-      wide_barrier<63>();
-    }
-    if (lk == KB) {
-      lk = 0;
-      ltile ^= 1;
-      id += stride;
-      more = id < end;
-      if (!more) id -= stride;  // the stream loads its last tile again
-      aim();
-    }
-    if (lk % W::SS == 0) load_scales();
-    ++kb;
-    const bool last = kb == KB;
-    if (last || kb % W::SS == 0) cgroup = cgroup + 1 == W::S ? 0 : cgroup + 1;
-    if (live) {
+    bool last = false;
+    auto turn = [&]() {  // the barrier of the step
+      if (!fresh) ++lk;  // the loads that the step before began are all out
+      wide_barrier<(W::S - 2) * kLoads>();  // the next step's tiles are here; those after may be on the way
+      if (kb + 1 == full && full < KB) {
+        clear_tail(next, BM + kWideCols);
+        wide_barrier<63>();
+      }
+      if (lk == KB) {
+        lk = 0;
+        ltile ^= 1;
+        id += stride;
+        more = id < end;
+        if (!more) id -= stride;  // the stream loads its last tile again
+        aim();
+      }
+      if (lk % W::SS == 0) load_scales();
+      ++kb;
+      last = kb == KB;
+      if (last || kb % W::SS == 0) cgroup = cgroup + 1 == W::S ? 0 : cgroup + 1;
+    };
+    auto first = [&]() { products(stage, next, 0, NT - 2, prev, !fresh); };
+    auto second = [&]() {
       if (!last) read_scales(cur, ctile, cgroup, kb);  // the next step's
       products(stage, next, NT - 2, NT, copy, true);
+    };
+    auto first_loads = [&]() {
+      if (!fresh) load(prev, kEarly, kLoads);
+    };
+    auto second_loads = [&]() { load(copy, 0, kEarly); };
+    if constexpr (SWIGLU) {
+      // (a path for each case: with the turn between two conditions the widened
+      // rows would have to stay in registers from step to step.  The plain
+      // kernel of 256 rows spills the other way round.)
+      if (live) {
+        first();
+        turn();
+        second();
+      } else {
+        first_loads();
+        turn();
+        second_loads();
+      }
     } else {
-      load(copy, 0, kEarly);
+      if (live) first();
+      else first_loads();
+      turn();
+      if (live) second();
+      else second_loads();
     }
     fresh = last;
     if (last) {
       load(copy, kEarly, kLoads);
       ++lk;
-#pragma unroll
-      for (int q = NT * MT - kLag; q < NT * MT; ++q) add(q);
+      drain();
       finish();
       if (!more) break;
 #pragma unroll
@@ -435,8 +499,8 @@ bool grouped_wide_fits(const GroupedArgs& g) {
 }
 
 hipError_t launch_grouped_wide(const Budget& b, const GroupedArgs& g, bool swiglu, int bm, hipStream_t stream) {
-  if (bm == 256) return swiglu ? launch<256, true>(b, g, stream) : launch<256, false>(b, g, stream);
-  return swiglu ? launch<128, true>(b, g, stream) : launch<128, false>(b, g, stream);
+  if (swiglu) return launch<128, true>(b, g, stream);  // (the exact products' operands leave no registers for more)
+  return bm == 256 ? launch<256, false>(b, g, stream) : launch<128, false>(b, g, stream);
 }
 
 }  // namespace ep
