@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libep.so")
 SOURCES = ["ep_api.hip", "layout.hip", "dispatch.hip", "dispatch_rows.hip", "combine.hip", "combine_reduce.hip",
            "layout_dispatch.hip", "probe.hip", "expert_api.hip", "dispatch_fp8.hip", "grouped_fp8.hip",
-           "grouped_wide.hip", "backward.hip"]
+           "grouped_wide.hip", "grouped_swiglu.hip", "backward.hip"]
 ARCH = "gfx950"
 
 
@@ -32,8 +32,8 @@ KERNEL_SOURCES = {
     "combine_reduce": ["combine_reduce.hip", "row_io.hpp", "ep_device.hpp", "ep_internal.hpp"],
     "layout_dispatch": ["layout_dispatch.hip", "row_io.hpp", "ep_device.hpp", "ep_internal.hpp"],
     "dispatch_fp8": ["dispatch_fp8.hip", "fp8_device.hpp", "expert_internal.hpp", "ep_device.hpp", "ep_internal.hpp"],
-    "grouped_fp8": ["grouped_fp8.hip", "grouped_wide.hip", "grouped_tiles.hpp", "fp8_device.hpp", "expert_internal.hpp",
-                    "ep_device.hpp", "ep_internal.hpp"],
+    "grouped_fp8": ["grouped_fp8.hip", "grouped_wide.hip", "grouped_swiglu.hip", "grouped_tiles.hpp", "fp8_device.hpp",
+                    "expert_internal.hpp", "ep_device.hpp", "ep_internal.hpp"],
     "backward": ["backward.hip", "row_io.hpp", "expert_internal.hpp", "ep_device.hpp", "ep_internal.hpp"],
 }
 

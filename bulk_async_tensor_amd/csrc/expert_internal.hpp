@@ -36,12 +36,15 @@ struct GroupedArgs {
   void* y;
   float* y_scale;
 };
-// The kernel for experts with many rows (grouped_wide.hip), bm = 128 or 256
-// token rows at a time; fits: whether it takes this K.
-bool grouped_wide_fits(const GroupedArgs& g);
-hipError_t launch_grouped_wide(const Budget& b, const GroupedArgs& g, bool swiglu, int bm, hipStream_t stream);
-
 hipError_t launch_grouped_fp8(const Budget& b, const GroupedArgs& g, bool swiglu, hipStream_t stream);
+
+// ---- grouped_wide.hip: the plain product, bm = 128 or 256 token rows at a time
+bool grouped_wide_fits(const GroupedArgs& g);  // whether it takes this K
+hipError_t launch_grouped_wide(const Budget& b, const GroupedArgs& g, int bm, hipStream_t stream);
+
+// ---- grouped_swiglu.hip
+bool grouped_swiglu_fits(const GroupedArgs& g);  // whether it takes this K
+hipError_t launch_grouped_swiglu(const Budget& b, const GroupedArgs& g, hipStream_t stream);
 
 // ---- backward.hip
 hipError_t launch_combine_backward(const Budget& b, const void* dout, const void* y, int64_t recv_rows, int H,

@@ -50,22 +50,21 @@ __device__ __forceinline__ f32x4 mfma_e4m3(i32x8 a, i32x8 b) {
 // in bf16 operands, at half the rate.  A quarter of the block (8 values of
 // each lane) per instruction; 9e-9 off.
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi) {  // two dwords of four e4m3 values
+  bf16x8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t f = i < 2 ? lo : hi;
+    const bf16x2 v = i & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f, 1.0f, true)
+                           : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f, 1.0f, false);
+    r[2 * i] = v[0];
+    r[2 * i + 1] = v[1];
+  }
+  return r;
+}
 struct Bf16Frag {
   bf16x8 part[4];
 };
-__device__ __forceinline__ Bf16Frag widen(i32x8 f) {
-  Bf16Frag r;
-#pragma unroll
-  for (int s = 0; s < 4; ++s)
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const bf16x2 v = h & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * s + h / 2], 1.0f, true)
-                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * s + h / 2], 1.0f, false);
-      r.part[s][2 * h] = v[0];
-      r.part[s][2 * h + 1] = v[1];
-    }
-  return r;
-}
 __device__ __forceinline__ f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }

@@ -3,10 +3,11 @@
 //
 //   p[r, n] = sum_b sa[r, b] sb[e, n / 128, b] sum_{i in block b} a[r, i] w[e, n, i]
 //
-// for the rows r that the layout gives expert e.  The matrix-core instruction
-// takes 16 weight rows against 16 token rows over one whole block of 128, so
-// each result is one block's inner sum; it is then multiplied by the two
-// scales and added in float32.  Weights are the A operand and tokens the B
+// for the rows r that the layout gives expert e, in ascending blocks b.  The
+// matrix cores give the inner sum of one whole block for 16 weight rows and 16
+// token rows; it is multiplied by the two scales and added in float32.
+// grouped_wide.hip holds the plain kernel and grouped_swiglu.hip the fused one;
+// here are the choice and the kernel for the K they do not take.  Weights are the A operand and tokens the B
 // operand: a lane's results then belong to ONE token (its column) and four
 // adjacent weight rows, so the lane needs one token scale, and the block's
 // weight scale is the same for the whole tile.
@@ -61,9 +62,11 @@ constexpr int kNarrowTiles = 4;               // token tiles of 16 per workgroup
 constexpr int kNarrowRows = 16 * kNarrowTiles;
 constexpr int kNarrowCols = 128;              // swiglu: output columns per workgroup (256 weight rows)
 
-// Few rows per expert: each wave streams two tiles of 16 weight rows from
-// memory straight into the matrix cores against up to 64 token rows.  swiglu:
-// the two tiles are the gate and the up rows of the same 16 outputs.
+// For the K that the other kernels do not take (swiglu: one scale block; plain:
+// one or two, or more than the 128 whose weight scales fit in LDS): each wave
+// streams two tiles of 16 weight rows from memory straight into the matrix
+// cores against up to 64 token rows.  swiglu: the two tiles are the gate and
+// the up rows of the same 16 outputs.
 template <bool SWIGLU>
 __global__ __launch_bounds__(kNarrowWaves * kWave) void grouped_narrow_kernel(GroupedArgs g, int units_n) {
   __shared__ float s_max[kNarrowWaves][kNarrowRows];
@@ -132,9 +135,9 @@ __global__ __launch_bounds__(kNarrowWaves * kWave) void grouped_narrow_kernel(Gr
           for (int h = 0; h < 2; ++h) {
             f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
             if constexpr (SWIGLU) {  // float32 sums for float32 results
-              const Bf16Frag wb = widen(wv[h]), ab = widen(av);
 #pragma unroll
-              for (int s = 0; s < 4; ++s) p = mfma_bf16(wb.part[s], ab.part[s], p);
+              for (int s = 0; s < 4; ++s)
+                p = mfma_bf16(widen8(wv[h][2 * s], wv[h][2 * s + 1]), widen8(av[2 * s], av[2 * s + 1]), p);
             } else {
               p = mfma_e4m3(wv[h], av);
             }
@@ -202,11 +205,9 @@ __global__ __launch_bounds__(kNarrowWaves * kWave) void grouped_narrow_kernel(Gr
 // as long as one of 128 where the products bound it, so the choice goes by the
 // rounds of tiles that the compute units make (every expert's last tile is
 // taken as half full).  Measured, 128 against 256: 32 experts, K = N = 4096,
-// 128 rows each 148 / 163 us, 512 each 374 / 348, 2048 each 1365 / 1204; 16
-// experts, swiglu K 2048, I 1024, 128 each 27 / 40 us, 512 each 73 / 77.
-static int wide_rows(const Budget& b, const GroupedArgs& g, bool swiglu) {
-  const int64_t outs = swiglu ? g.N / 2 : g.N, per = swiglu ? 128 : 256;
-  const int64_t units_n = (outs + per - 1) / per, held = g.E < g.rows ? g.E : g.rows;
+// 128 rows each 148 / 163 us, 512 each 374 / 348, 2048 each 1365 / 1204.
+static int wide_rows(const Budget& b, const GroupedArgs& g) {
+  const int64_t units_n = (g.N + 255) / 256, held = g.E < g.rows ? g.E : g.rows;
   auto rounds = [&](int bm) {
     const int64_t tiles = units_n * (2 * g.rows / bm + held) / 2;
     return (tiles + b.device_cus - 1) / b.device_cus;
@@ -214,18 +215,21 @@ static int wide_rows(const Budget& b, const GroupedArgs& g, bool swiglu) {
   return 8 * rounds(256) <= 5 * rounds(128) ? 256 : 128;
 }
 
-hipError_t launch_grouped_fp8(const Budget& b, const GroupedArgs& g, bool swiglu, hipStream_t stream) {
-  if (grouped_wide_fits(g)) return launch_grouped_wide(b, g, swiglu, wide_rows(b, g, swiglu), stream);
-  const int units_n = swiglu ? (g.N / 2 + kNarrowCols - 1) / kNarrowCols : (g.N + 2 * kNarrowCols - 1) / (2 * kNarrowCols);
+template <bool SWIGLU>
+static hipError_t launch_narrow(const GroupedArgs& g, hipStream_t stream) {
+  const int outs = SWIGLU ? g.N / 2 : g.N, per = SWIGLU ? kNarrowCols : 2 * kNarrowCols;
+  const int units_n = (outs + per - 1) / per;
   // one workgroup for each tile there can be: every expert may end inside one
   const int64_t tiles = g.rows / kNarrowRows + (g.E < g.rows ? g.E : g.rows);
   const int64_t want = tiles * units_n, most = 1 << 22;
   const int grid = (int)(want < most ? want : most);
-  if (swiglu)
-    hipLaunchKernelGGL(grouped_narrow_kernel<true>, dim3(grid), dim3(kNarrowWaves * kWave), 0, stream, g, units_n);
-  else
-    hipLaunchKernelGGL(grouped_narrow_kernel<false>, dim3(grid), dim3(kNarrowWaves * kWave), 0, stream, g, units_n);
+  hipLaunchKernelGGL(grouped_narrow_kernel<SWIGLU>, dim3(grid), dim3(kNarrowWaves * kWave), 0, stream, g, units_n);
   return hipGetLastError();
+}
+
+hipError_t launch_grouped_fp8(const Budget& b, const GroupedArgs& g, bool swiglu, hipStream_t stream) {
+  if (swiglu) return grouped_swiglu_fits(g) ? launch_grouped_swiglu(b, g, stream) : launch_narrow<true>(g, stream);
+  return grouped_wide_fits(g) ? launch_grouped_wide(b, g, wide_rows(b, g), stream) : launch_narrow<false>(g, stream);
 }
 
 }  // namespace ep

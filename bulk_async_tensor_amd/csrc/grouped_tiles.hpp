@@ -16,6 +16,14 @@ constexpr int kWideMaxBlocks = 128;  // scale blocks along K that the wide kerne
 // Tiles there can be: every expert that holds a row may end inside one.
 inline int64_t wide_tiles_most(int64_t rows, int E, int bm) { return rows / bm + (E < rows ? E : rows); }
 
+// Workgroups that stay and share `tiles` tiles: one per CU, the same number on
+// each XCD.
+inline int stay_grid(const Budget& b, int64_t tiles) {
+  int64_t grid = b.device_cus / kXcds * kXcds;
+  if (grid > tiles) grid = (tiles + kXcds - 1) / kXcds * kXcds;
+  return (int)(grid < kXcds ? kXcds : grid);
+}
+
 struct Segment {
   int lo, hi;
 };

@@ -1,7 +1,6 @@
-// The experts' 8-bit products for experts with many rows: a workgroup of 8
-// waves computes 256 weight rows x BM token rows at a time (swiglu: 128 gate
-// rows and the 128 up rows of the same outputs) from tiles that both sides'
-// loads bring straight into LDS.
+// ep_grouped_gemm_fp8: a workgroup of 8 waves computes 256 weight rows x BM
+// token rows at a time from tiles that both sides' loads bring straight into
+// LDS.
 //
 // One step is one block of 128 values, so a step's matrix-core results are
 // whole inner sums: each is multiplied by its two scales and added to the
@@ -89,21 +88,19 @@ __device__ __forceinline__ void wide_barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <int BM, bool SWIGLU>
+template <int BM>
 __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) {
   using W = Wide<BM>;
   constexpr int HT = W::HT, MT = W::MT, NT = 2 * HT;
   static_assert(MT == 4, "a wave holds four token tiles");
   __shared__ __attribute__((aligned(1024))) uint8_t s_rows[W::S * W::kStage];
   __shared__ float s_sa[W::S][BM * W::SS];
-  __shared__ float s_sb[2][3][kWideMaxBlocks];
+  __shared__ float s_sb[2][2][kWideMaxBlocks];
   __shared__ int32_t s_first[EP_MAX_EXPERTS + 1];
-  __shared__ float s_max[W::WN][BM];
   const int lane = lane_id();
   const int wave = wave_in_group();
   const int col = lane & 15, quad = lane >> 4;
   const int K = g.K, N = g.N, KB = scale_blocks(K), NB = scale_blocks(N);
-  const int outs = SWIGLU ? N / 2 : N;
   const int wn = wave % W::WN, wm = wave / W::WN;
 
   // ---- the tiles of this workgroup: a run of them for each XCD
@@ -125,21 +122,20 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
   // weight's end are past the buffer's: they bring zeros, and their results
   // are never stored.
   const uint32_t at_row = (uint32_t)(lane >> 3) * K + ((lane & 7) ^ (lane >> 3)) * 16;
-  auto first_col = [&](const WideTile& t) { return t.n * (SWIGLU ? kHalf : kWideCols); };
+  auto first_col = [&](const WideTile& t) { return t.n * kWideCols; };
   auto aim = [&]() {
     find_tile_of<BM>(g.offsets, s_first, g.E, (int)g.rows, units_n, id, lane, &nxt);
-    const int n0 = first_col(nxt);
     const int64_t held = nxt.r1 - nxt.r0;
     ra = buffer_of(static_cast<const uint8_t*>(g.a) + nxt.r0 * K, held * K);
     rb = buffer_of(static_cast<const uint8_t*>(g.b) + (int64_t)nxt.e * N * K, (int64_t)N * K);
     rs = buffer_of(g.a_scale + nxt.r0 * KB, held * KB * 4);
     rw = buffer_of(g.b_scale + (int64_t)nxt.e * NB * KB, (int64_t)NB * KB * 4);
-    // The weight scales of all steps, 64 an instruction: block row n0 / 128
-    // and the next; swiglu: one gate and two up rows.  (Blocks past the last
-    // one bring a neighbour's scale, or zero past the buffer; no step uses them.)
-    for (int i = wave; i < 3 * ((KB + 63) / 64); i += kWideWaves) {
-      const int which = i % 3, k0 = i / 3 * 64;
-      int nb = SWIGLU ? (which == 0 ? n0 / kScaleBlock : (outs + n0) / kScaleBlock + which - 1) : n0 / kScaleBlock + which;
+    // The weight scales of all steps, 64 an instruction, of both halves.
+    // (Blocks past the last one bring a neighbour's scale, or zero past the
+    // buffer; no step uses them.)
+    for (int i = wave; i < 2 * ((KB + 63) / 64); i += kWideWaves) {
+      const int which = i % 2, k0 = i / 2 * 64;
+      int nb = 2 * nxt.n + which;
       if (nb >= NB) nb = NB - 1;
       load4_to_lds(rw, lds_addr_of(&s_sb[ltile][which][k0]), (k0 + lane) * 4, nb * KB * 4);
     }
@@ -168,7 +164,7 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
         const int h = (i - W::LT) / W::LW, j = (i - W::LT) % W::LW;
         const int r = wave * (kHalf / kWideWaves) + j * 8;
         load16_to_lds(rb, rows0 + copy * W::kStage + W::kT + (h * kHalf + r) * kStepBytes,
-                      at_row + (uint32_t)(first_col(nxt) + (h ? (SWIGLU ? outs : kHalf) : 0) + r) * K,
+                      at_row + (uint32_t)(first_col(nxt) + h * kHalf + r) * K,
                       lk * kStepBytes);
       }
     }
@@ -206,7 +202,6 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
 
   i32x8 t[MT], w[4];
   f32x4 p[4] = {};
-  Bf16Frag tb[MT];  // SWIGLU
   float s0[MT] = {}, s1[MT] = {}, v[MT], v0, v1;
   auto add = [&](int n, int m, f32x4 v) {
     const float sc = n < HT ? s0[m] : s1[m];
@@ -224,11 +219,9 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
     return stage + W::kT + (wn * HT * 16 + (n < HT ? n * 16 : kHalf + (n - HT) * 16)) * kStepBytes;
   };
   auto token_rows = [&](const uint8_t* stage, int m) { return stage + (wm * MT + m) * 16 * kStepBytes; };
-  auto read_scales = [&](const WideTile& at, int tile, int group, int k) {
-    const int c0 = outs + first_col(at);
-    const int up = SWIGLU ? 1 + (c0 + wn * HT * 16) / kScaleBlock - c0 / kScaleBlock : 1;
+  auto read_scales = [&](int tile, int group, int k) {
     v0 = s_sb[tile][0][k];
-    v1 = s_sb[tile][up][k];
+    v1 = s_sb[tile][1][k];
 #pragma unroll
     for (int m = 0; m < MT; ++m) v[m] = s_sa[group][((wm * MT + m) * 16 + col) * W::SS + k % W::SS];
   };
@@ -243,12 +236,9 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
   // started.  The scheduling barriers keep this order (left alone, the
   // compiler reads all tiles first and spills).
   //
-  // Plain: product number q of a step (weight tile q / 4, token tile q % 4) is
-  // scaled and added three products after it started, when the matrix core has
-  // finished it: the last three of a step in the next step.  Swiglu, whose
-  // results are float32 and 8-bit values of them, takes the exact products:
-  // both sides are widened to bf16, two token tiles are multiplied together and
-  // added while the next two are.
+  // Product number q of a step (weight tile q / 4, token tile q % 4) is scaled
+  // and added three products after it started, when the matrix core has
+  // finished it: the last three of a step in the next step.
   constexpr int kLag = 3;
   auto products = [&](const uint8_t* stage, const uint8_t* next, int N0, int N1, int copy, bool loads) {
 #pragma unroll
@@ -258,117 +248,40 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
       const int pair = n >= NT - 2 ? n - (NT - 2) : n + 2;
       if (pair < kPairs && loads) load(copy, 2 * pair, 2 * pair + 2);
       w[(n + 2) & 3] = n + 2 < NT ? frag(weight_rows(stage, n + 2)) : frag(weight_rows(next, n + 2 - NT));
-      if constexpr (SWIGLU) {
-        const Bf16Frag wb = widen(w[n & 3]);
 #pragma unroll
-        for (int m = 0; m < MT; m += 2) {
-          if (n == 0) {
-            tb[m] = widen(t[m]);
-            tb[m + 1] = widen(t[m + 1]);
-          }
-          f32x4 c0 = {0.0f, 0.0f, 0.0f, 0.0f}, c1 = c0;
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            c0 = mfma_bf16(wb.part[s], tb[m].part[s], c0);
-            c1 = mfma_bf16(wb.part[s], tb[m + 1].part[s], c1);
-          }
-          if (n == NT - 1) {
-            t[m] = frag(token_rows(next, m));
-            t[m + 1] = frag(token_rows(next, m + 1));
-          }
-          const int bn = m ? n : (n + NT - 1) % NT, bm = m ? m - 2 : MT - 2;  // the two before
-          add(bn, bm, p[bm]);
-          add(bn, bm + 1, p[bm + 1]);
-          p[m] = c0;
-          p[m + 1] = c1;
-          if (n == 0 && m == 0) new_scales();
-        }
-      } else {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const int q = n * MT + m, b = (q + NT * MT - kLag) % (NT * MT);
-          if (q == kLag) new_scales();  // the last products of the step before are added
-          p[q & 3] = mfma_e4m3(w[n & 3], t[m]);
-          if (n == NT - 1) t[m] = frag(token_rows(next, m));
-          add(b / MT, b % MT, p[b & 3]);
-        }
+      for (int m = 0; m < MT; ++m) {
+        const int q = n * MT + m, b = (q + NT * MT - kLag) % (NT * MT);
+        if (q == kLag) new_scales();  // the last products of the step before are added
+        p[q & 3] = mfma_e4m3(w[n & 3], t[m]);
+        if (n == NT - 1) t[m] = frag(token_rows(next, m));
+        add(b / MT, b % MT, p[b & 3]);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
   };
   auto drain = [&]() {  // the products that are not added yet
-    if constexpr (SWIGLU) {
-      add(NT - 1, MT - 2, p[MT - 2]);
-      add(NT - 1, MT - 1, p[MT - 1]);
-    } else {
 #pragma unroll
-      for (int q = NT * MT - kLag; q < NT * MT; ++q) add(q / MT, q % MT, p[q & 3]);
-    }
+    for (int q = NT * MT - kLag; q < NT * MT; ++q) add(q / MT, q % MT, p[q & 3]);
   };
 
   auto finish = [&]() {  // the tile's results
     const int n0 = first_col(cur), held = (int)(cur.r1 - cur.r0);
     // lane (col, quad) holds rows 4 quad .. + 3 of each weight tile, token col of each token tile
-    if constexpr (!SWIGLU) {
-      uint16_t* y = static_cast<uint16_t*>(g.y);
+    uint16_t* y = static_cast<uint16_t*>(g.y);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int r = (wm * MT + m) * 16 + col;
+    for (int m = 0; m < MT; ++m) {
+      const int r = (wm * MT + m) * 16 + col;
 #pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-          // two neighbouring tiles: lanes exchange so that each holds 8 adjacent outputs
-          const u32x2 d0 = swap_rows16(pack_bf16x2(acc[n][m][0], acc[n][m][1]),
-                                       pack_bf16x2(acc[n + 1][m][0], acc[n + 1][m][1]));
-          const u32x2 d1 = swap_rows16(pack_bf16x2(acc[n][m][2], acc[n][m][3]),
-                                       pack_bf16x2(acc[n + 1][m][2], acc[n + 1][m][3]));
-          const int tile = n + (quad & 1);
-          const int c = n0 + (n < HT ? 0 : kHalf - HT * 16) + (wn * HT + tile) * 16 + 8 * (quad >> 1);
-          if (r < held && c < N)
-            st16<true>(reinterpret_cast<u32x4*>(y + (cur.r0 + r) * N + c), u32x4{d0[0], d1[0], d0[1], d1[1]});
-        }
-      }
-    } else {
-      uint8_t* y = static_cast<uint8_t*>(g.y);
-      const int c0 = n0 + wn * HT * 16;  // the wave's first output; outs % 64 == 0: inside or outside as a whole
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        float top = kAmaxFloor;
-#pragma unroll
-        for (int n = 0; n < HT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float v = silu_mul(acc[n][m][i], acc[n + HT][m][i]);
-            acc[n][m][i] = v;
-            top = fmaxf(top, c0 < outs ? fabsf(v) : 0.0f);
-          }
-        top = fmaxf(top, __shfl_xor(top, 16, kWave));
-        top = fmaxf(top, __shfl_xor(top, 32, kWave));
-        if (quad == 0) s_max[wn][(wm * MT + m) * 16 + col] = top;
-      }
-      wide_barrier<63>();
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int r = (wm * MT + m) * 16 + col;
-        float top = s_max[0][r];
-#pragma unroll
-        for (int o = 1; o < W::WN; ++o) top = fmaxf(top, s_max[o][r]);
-        const float inv = block_inverse(top);
-        uint32_t d[HT];
-#pragma unroll
-        for (int n = 0; n < HT; ++n)
-          d[n] = pack_e4m3x4(acc[n][m][0] * inv, acc[n][m][1] * inv, acc[n][m][2] * inv, acc[n][m][3] * inv);
-        const bool in = r < held && c0 < outs;
-        uint8_t* out = y + (cur.r0 + r) * outs + c0;
-        if constexpr (HT == 4) {
-          // four tiles of 16 outputs: after two exchanges lane quad q holds tile q's 16
-          const u32x2 e0 = swap_rows32(d[0], d[2]), e1 = swap_rows32(d[1], d[3]);
-          const u32x2 f0 = swap_rows16(e0[0], e1[0]), f1 = swap_rows16(e0[1], e1[1]);
-          if (in) st16<true>(reinterpret_cast<u32x4*>(out + 16 * quad), u32x4{f0[0], f0[1], f1[0], f1[1]});
-        } else {
-          const u32x2 f = swap_rows16(d[0], d[1]);
-          if (in) __builtin_nontemporal_store(f, reinterpret_cast<u32x2*>(out + 16 * (quad & 1) + 8 * (quad >> 1)));
-        }
-        if (r < held && wn == 0 && quad == 0) g.y_scale[(cur.r0 + r) * scale_blocks(outs) + cur.n] = block_scale(top);
+      for (int n = 0; n < NT; n += 2) {
+        // two neighbouring tiles: lanes exchange so that each holds 8 adjacent outputs
+        const u32x2 d0 = swap_rows16(pack_bf16x2(acc[n][m][0], acc[n][m][1]),
+                                     pack_bf16x2(acc[n + 1][m][0], acc[n + 1][m][1]));
+        const u32x2 d1 = swap_rows16(pack_bf16x2(acc[n][m][2], acc[n][m][3]),
+                                     pack_bf16x2(acc[n + 1][m][2], acc[n + 1][m][3]));
+        const int tile = n + (quad & 1);
+        const int c = n0 + (n < HT ? 0 : kHalf - HT * 16) + (wn * HT + tile) * 16 + 8 * (quad >> 1);
+        if (r < held && c < N)
+          st16<true>(reinterpret_cast<u32x4*>(y + (cur.r0 + r) * N + c), u32x4{d0[0], d1[0], d0[1], d1[1]});
       }
     }
   };
@@ -393,7 +306,7 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
         for (int m = 0; m < MT; ++m) t[m] = frag(token_rows(stage, m));
         w[0] = frag(weight_rows(stage, 0));
         w[1] = frag(weight_rows(stage, 1));
-        read_scales(cur, ctile, cgroup, kb);
+        read_scales(ctile, cgroup, kb);
       }
     }
     bool last = false;
@@ -419,33 +332,18 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
     };
     auto first = [&]() { products(stage, next, 0, NT - 2, prev, !fresh); };
     auto second = [&]() {
-      if (!last) read_scales(cur, ctile, cgroup, kb);  // the next step's
+      if (!last) read_scales(ctile, cgroup, kb);  // the next step's
       products(stage, next, NT - 2, NT, copy, true);
     };
     auto first_loads = [&]() {
       if (!fresh) load(prev, kEarly, kLoads);
     };
     auto second_loads = [&]() { load(copy, 0, kEarly); };
-    if constexpr (SWIGLU) {
-      // (a path for each case: with the turn between two conditions the widened
-      // rows would have to stay in registers from step to step.  The plain
-      // kernel of 256 rows spills the other way round.)
-      if (live) {
-        first();
-        turn();
-        second();
-      } else {
-        first_loads();
-        turn();
-        second_loads();
-      }
-    } else {
-      if (live) first();
-      else first_loads();
-      turn();
-      if (live) second();
-      else second_loads();
-    }
+    if (live) first();
+    else first_loads();
+    turn();
+    if (live) second();
+    else second_loads();
     fresh = last;
     if (last) {
       load(copy, kEarly, kLoads);
@@ -471,22 +369,17 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
 }
 
 // One workgroup fills a CU's LDS: two waves per SIMD, 256 registers each.
-template <int BM, bool SWIGLU>
+template <int BM>
 __global__ __launch_bounds__(kWideWaves * kWave) __attribute__((amdgpu_waves_per_eu(2, 2))) void grouped_wide_kernel(
     GroupedArgs g, int units_n) {
-  grouped_wide<BM, SWIGLU>(g, units_n);
+  grouped_wide<BM>(g, units_n);
 }
 
-template <int BM, bool SWIGLU>
+template <int BM>
 hipError_t launch(const Budget& b, const GroupedArgs& g, hipStream_t stream) {
-  const int outs = SWIGLU ? g.N / 2 : g.N, per = SWIGLU ? kHalf : kWideCols;
-  const int units_n = (outs + per - 1) / per;
-  const int64_t most = wide_tiles_most(g.rows, g.E, BM) * units_n;
-  int64_t grid = b.device_cus / kXcds * kXcds;
-  if (grid > most) grid = (most + kXcds - 1) / kXcds * kXcds;
-  if (grid < kXcds) grid = kXcds;
-  hipLaunchKernelGGL((grouped_wide_kernel<BM, SWIGLU>), dim3((unsigned)grid), dim3(kWideWaves * kWave), 0, stream, g,
-                     units_n);
+  const int units_n = (g.N + kWideCols - 1) / kWideCols;
+  const int grid = stay_grid(b, wide_tiles_most(g.rows, g.E, BM) * units_n);
+  hipLaunchKernelGGL(grouped_wide_kernel<BM>, dim3(grid), dim3(kWideWaves * kWave), 0, stream, g, units_n);
   return hipGetLastError();
 }
 
@@ -498,9 +391,8 @@ bool grouped_wide_fits(const GroupedArgs& g) {
   return blocks >= Wide<128>::S && blocks <= kWideMaxBlocks;
 }
 
-hipError_t launch_grouped_wide(const Budget& b, const GroupedArgs& g, bool swiglu, int bm, hipStream_t stream) {
-  if (swiglu) return launch<128, true>(b, g, stream);  // (the exact products' operands leave no registers for more)
-  return bm == 256 ? launch<256, false>(b, g, stream) : launch<128, false>(b, g, stream);
+hipError_t launch_grouped_wide(const Budget& b, const GroupedArgs& g, int bm, hipStream_t stream) {
+  return bm == 256 ? launch<256>(b, g, stream) : launch<128>(b, g, stream);
 }
 
 }  // namespace ep
