@@ -5,8 +5,14 @@ Bounds.  A rounding to type t is off by at most half a step,
 torch.finfo(t).eps / 2 relative to the value: U = 2^-24 for float32, 2^-8 for
 bf16, 2^-4 for e4m3 (plus half the subnormal step, 2^-10, near zero).  A sum of
 float32 terms along a chain of n additions is off by at most about n U times
-the sum of the terms' magnitudes; sums inside the matrix instruction are taken
-at twice that, since its inner additions may truncate instead of rounding.
+the sum of the terms' magnitudes; sums inside the bf16 matrix instruction are
+taken at twice that, since its inner additions may truncate instead of rounding.
+
+The 8-bit matrix instruction lines each 8 adjacent products up with the largest
+of them and drops what lies 2^-13 of it and further below.  Each of the 8 loses
+at most 2^-13 of the group's largest, and the largest of all groups together
+are at most the sum of all magnitudes M: it is off by at most 8 * 2^-13 M.  On
+random values the losses mostly cancel; RMS_BF16 is what is left then.
 """
 
 import torch
@@ -17,6 +23,10 @@ AMAX_FLOOR = 2.0 ** -100
 U32 = 2.0 ** -24
 UBF16 = torch.finfo(torch.bfloat16).eps / 2
 UE4M3 = torch.finfo(torch.float8_e4m3fn).eps / 2
+U8 = 8 * 2.0 ** -13
+# The error of a rounding to bf16 is spread evenly over half a step on both sides: at most 2^-8 / sqrt(3) of the value
+# in the square mean (for values just above a power of two; 2^-8 / sqrt(7) when they are spread evenly up to the next).
+RMS_BF16 = UBF16 / 3 ** 0.5
 E4M3_SUB = 2.0 ** -10  # half of the smallest e4m3 step
 
 
@@ -75,12 +85,21 @@ def random_weights(E, N, K, seed, device):
     return q, s
 
 
-def product(a, a_scale, offsets, b, b_scale):
+def product(a, a_scale, offsets, b, b_scale, eight_bit=False):
     """(p, bound): the experts' products in 64 bits, NaN in rows that no expert
-    holds, and how far a float32 computation by blocks may be from them."""
+    holds, and how far a float32 computation by blocks may be from them, its
+    inner sums from the bf16 or the 8-bit matrix instruction."""
+    p, mag = terms(a, a_scale, offsets, b, b_scale)
+    # inner sums of 128, the two scale roundings and their product, the sum over the blocks
+    inner = U8 if eight_bit else 2 * BLOCK * U32
+    return p, mag * (inner + (blocks(a.shape[1]) + 3) * U32)
+
+
+def terms(a, a_scale, offsets, b, b_scale):
+    """(p, mag): the products, and the sum of the magnitudes of each one's
+    terms (0 in rows that no expert holds)."""
     rows, K = a.shape
     E, N, _ = b.shape
-    nb = blocks(K)
     p = torch.full((rows, N), float("nan"), dtype=torch.float64, device=a.device)
     mag = torch.zeros((rows, N), dtype=torch.float64, device=a.device)
     off = offsets.tolist()
@@ -93,15 +112,11 @@ def product(a, a_scale, offsets, b, b_scale):
         we = we * b_scale[e].double().repeat_interleave(BLOCK, 0)[:N].repeat_interleave(BLOCK, 1)[:, :K]
         p[lo:hi] = ae @ we.t()
         mag[lo:hi] = ae.abs() @ we.abs().t()
-    # inner sums of 128 (twice U each), the two scale roundings, the sum over the blocks in up to 16 runs
-    return p, mag * (BLOCK * 2 * U32 + (nb + 18) * U32)
+    return p, mag
 
 
 def magnitude(a, a_scale, offsets, b, b_scale):
-    """The sum of the magnitudes of each product's terms (0 in rows that no
-    expert holds)."""
-    _, bound = product(a, a_scale, offsets, b, b_scale)
-    return bound / (BLOCK * 2 * U32 + (blocks(a.shape[1]) + 18) * U32)
+    return terms(a, a_scale, offsets, b, b_scale)[1]
 
 
 def swiglu(p, bound):

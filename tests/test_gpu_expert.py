@@ -104,13 +104,15 @@ def held(offsets):
 
 def check_gemm(offsets, a, sa, b, sb):
     rows, N = a.shape[0], b.shape[1]
-    p, bound = ref.product(a, sa, offsets, b, sb)
+    p, bound = ref.product(a, sa, offsets, b, sb, eight_bit=True)
     y = torch.full((rows, N), 77.0, dtype=BF16, device=DEV)
     assert ep.ep_grouped_gemm_fp8(a, sa, offsets, b, sb, y) is y
     lo, hi = held(offsets)
     err = (y[lo:hi].double() - p[lo:hi]).abs()
     limit = ref.UBF16 * p[lo:hi].abs() + 1.01 * bound[lo:hi]
     assert bool((err <= limit).all()), f"off by up to {float((err / limit).max()):.3f} of the bound"
+    if err.numel() > 4000:  # enough for a mean
+        assert float(err.norm() / p[lo:hi].norm()) <= ref.RMS_BF16
     assert bool((y[:lo] == 77).all()) and bool((y[hi:] == 77).all())
     return y
 
@@ -176,6 +178,72 @@ def test_products_of_uneven_experts(counts):
     check_swiglu(offsets, a, sa, b, sb)
 
 
+# Calls whose workgroups go through several tiles each, at every tile height and at few, odd and many steps a tile:
+# T, E, k, K, N (swiglu: about N / 4 outputs, half a tile past whole ones).
+STREAMS = [(1500, 512, 4, 256, 2304), (1500, 512, 4, 528, 2304), (1500, 512, 4, 1168, 2304), (1500, 150, 4, 272, 2304),
+           (1500, 150, 4, 640, 2304), (1500, 150, 4, 1280, 2304), (4096, 4, 4, 272, 2304), (4096, 4, 4, 384, 2304),
+           (4096, 4, 4, 1040, 2304), (2100, 12, 4, 400, 4352), (2100, 12, 4, 1152, 4352)]
+
+
+@pytest.mark.parametrize("T, E, k, K, N", STREAMS)
+def test_streams_of_tiles(T, E, k, K, N):
+    offsets, _, a, sa, b, sb = operands(T, E, k, K, N, 0.05, T + K)
+    check_gemm(offsets, a, sa, b, sb)
+    I = N // 4 // 128 * 128 + 64
+    check_swiglu(offsets, a, sa, b[:, : 2 * I].contiguous(), sb[:, : ref.blocks(2 * I)].contiguous())
+
+
+@pytest.mark.parametrize("K", [16384, 16400, 20000])
+def test_long_rows(K):
+    offsets, _, a, sa, b, sb = operands(70, 3, 2, K, 384, 0, K)
+    check_gemm(offsets, a, sa, b, sb)
+    check_swiglu(offsets, a, sa, b, sb)
+
+
+def test_equal_calls_give_equal_bits():
+    offsets, _, a, sa, b, sb = operands(500, 6, 3, 912, 1280, 0, 1)
+    first = check_gemm(offsets, a, sa, b, sb), *check_swiglu(offsets, a, sa, b, sb)
+    for _ in range(3):
+        again = check_gemm(offsets, a, sa, b, sb), *check_swiglu(offsets, a, sa, b, sb)
+        for u, v in zip(first, again):
+            same(u, v)
+
+
+@pytest.mark.parametrize("K, E, counts", [(112, 3, [70, 1, 329]), (272, 3, [70, 1, 329]), (656, 3, [70, 1, 329]),
+                                          (656, 9, [20, 30, 50, 1, 0, 70, 40, 60, 80]),
+                                          (656, 20, [11, 1, 28] + [10] * 17)])
+def test_swiglu_does_not_mix_rows_or_experts(K, E, counts):
+    """As below; a NaN of h leaves the rest of its block of 128 as it is."""
+    rows, I = sum(counts), 192
+    offsets = torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), dtype=torch.int32, device=DEV)
+    a, sa = ref.random_rows(rows, K, 5, DEV)
+    b, sb = ref.random_weights(E, 2 * I, K, 6, DEV)
+
+    def run():
+        q, s = torch.zeros(rows, I, dtype=torch.uint8, device=DEV).view(F8), torch.zeros(rows, 2, device=DEV)
+        return ep.ep_grouped_swiglu_fp8(a, sa, offsets, b, sb, q, s)
+
+    q, s = run()
+    assert not bool(torch.isnan(q.float()).any())
+    bits(a)[10, K - 1] = NAN8
+    sa[rows - 2, 0] = float("nan")
+    bits(b)[2, 100, 0] = NAN8          # gate of output 100
+    bits(b)[2, I + 150, K - 16] = NAN8  # up of output 150
+    nq, ns = run()
+    bad = torch.isnan(nq.float())
+    want = torch.zeros_like(bad)
+    lo, hi = int(offsets[2]), int(offsets[3])
+    want[10] = want[rows - 2] = True
+    want[lo:hi, 100] = want[lo:hi, 150] = True
+    assert torch.equal(bad, want)
+    touched = torch.zeros(rows, 2, dtype=torch.bool, device=DEV)
+    touched[10] = touched[rows - 2] = True
+    touched[lo:hi] = True
+    assert torch.equal(bits(ns)[~touched], bits(s)[~touched])
+    rest = ~touched.repeat_interleave(128, 1)[:, :I]
+    assert torch.equal(bits(nq)[rest], bits(q)[rest])
+
+
 def test_products_do_not_mix_rows_or_experts():
     """A NaN in a row reaches that row only, a NaN in a weight row that output
     only, and a NaN scale its blocks."""
@@ -234,7 +302,7 @@ def test_products_past_four_gigabytes():
     y = torch.full((rows, N), 9.0, dtype=BF16, device=DEV)
     ep.ep_grouped_gemm_fp8(a, sa, offsets, b, sb, y)
     lo = rows - 40
-    p, bound = ref.product(a[lo:], sa[lo:], (offsets - lo)[70:72].contiguous(), b[70:71], sb[70:71])
+    p, bound = ref.product(a[lo:], sa[lo:], (offsets - lo)[70:72].contiguous(), b[70:71], sb[70:71], eight_bit=True)
     err = (y[lo : rows - 3].double() - p[:37]).abs()
     assert bool((err <= ref.UBF16 * p[:37].abs() + 1.01 * bound[:37]).all())
     assert bool((y[:lo] == 9).all()) and bool((y[rows - 3 :] == 9).all())
