@@ -273,7 +273,9 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
       const int r = (wm * MT + m) * 16 + col;
 #pragma unroll
       for (int n = 0; n < NT; n += 2) {
-        // two neighbouring tiles: lanes exchange so that each holds 8 adjacent outputs
+        // two neighbouring tiles: lanes exchange so that each holds 8 adjacent
+        // outputs.  (Cached stores: a row's 128-byte lines are filled by two
+        // of them, and streamed ones wrote 2.06 GB for 1.41, 1644 / 1597 us.)
         const u32x2 d0 = swap_rows16(pack_bf16x2(acc[n][m][0], acc[n][m][1]),
                                      pack_bf16x2(acc[n + 1][m][0], acc[n + 1][m][1]));
         const u32x2 d1 = swap_rows16(pack_bf16x2(acc[n][m][2], acc[n][m][3]),
@@ -281,7 +283,7 @@ __device__ __forceinline__ void grouped_wide(const GroupedArgs& g, int units_n) 
         const int tile = n + (quad & 1);
         const int c = n0 + (n < HT ? 0 : kHalf - HT * 16) + (wn * HT + tile) * 16 + 8 * (quad >> 1);
         if (r < held && c < N)
-          st16<true>(reinterpret_cast<u32x4*>(y + (cur.r0 + r) * N + c), u32x4{d0[0], d1[0], d0[1], d1[1]});
+          *reinterpret_cast<u32x4*>(y + (cur.r0 + r) * N + c) = u32x4{d0[0], d1[0], d0[1], d1[1]};
       }
     }
   };
