@@ -34,7 +34,12 @@ __device__ __forceinline__ Segment segment_of(const int32_t* __restrict__ offset
   return s;
 }
 
-// first[e] = tiles before expert e, first[E] = all of them.  One wave.
+// Offsets that ascend give at most rows / BM + E tiles; where they do not, the
+// segments overlap and their tiles are counted up to this many.
+constexpr int kTilesCap = 1 << 29;
+
+// first[e] = tiles before expert e, first[E] = all of them.  One wave.  (64
+// experts' tiles fit 30 bits: BM is 128 or more where rows pass 65536.)
 template <int BM>
 __device__ __forceinline__ void first_tiles(const int32_t* __restrict__ offsets, int E, int rows, int lane,
                                             int32_t* first) {
@@ -47,8 +52,8 @@ __device__ __forceinline__ void first_tiles(const int32_t* __restrict__ offsets,
       n = (int)(((int64_t)s.hi - s.lo + BM - 1) / BM);
     }
     const int incl = wave_incl_scan(n, lane);
-    if (e < E) first[e] = before + incl - n;
-    before += __builtin_amdgcn_readlane(incl, kWave - 1);
+    if (e < E) first[e] = min(before + incl - n, kTilesCap);
+    before = min(before + __builtin_amdgcn_readlane(incl, kWave - 1), kTilesCap);
   }
   if (lane == 0) first[E] = before;
 }

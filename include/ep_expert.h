@@ -6,7 +6,8 @@
  * owns, work only enqueued on `stream`, host-detectable errors before any HIP
  * call, nothing allocated, no synchronisation.  Every call below may be
  * captured into a HIP graph, and calls share no state: two of them on
- * different streams do not touch each other's memory.
+ * different streams do not touch each other's memory.  No output may overlap
+ * an input or another output.
  *
  * A layer runs them in this order (R = T * k receive rows):
  *
