@@ -23,7 +23,7 @@
 // that the next tile's rows are on the way while a tile's last steps and its
 // results are done.
 //
-// 98304 rows, K 7168, I 2048, 64 experts: 5.4 ms, 1.06 PFLOP/s, two thirds of
+// 98304 rows, K 7168, I 2048, 64 experts: 5.3 ms, 1.09 PFLOP/s, two thirds of
 // what a bf16 library product of 16384^3 reaches (1.6): the matrix cores are
 // busy 55 % of the cycles at 1.9 GHz, with 2.5 vector instructions to a matrix
 // instruction.  Each wave widening what it uses took 6.4 ms; 32 x 32 products
@@ -70,6 +70,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p, int64
 
 __device__ __forceinline__ bf16x8 widen_half(u32x4 f, int h) { return widen8(f[2 * h], f[2 * h + 1]); }
 
+// v in a register of its own.  (Left to share the load's register, the next
+// load into it would go to another one and be moved at the loop's end, which
+// waits for it there.)
+__device__ __forceinline__ float own_copy(float v) {
+  float r;
+  asm("v_mov_b32 %0, %1" : "=&v"(r) : "v"(v));
+  return r;
+}
+
 template <int TOKENS>
 __device__ __forceinline__ void swiglu_body(const GroupedArgs& g, int units_n) {
   using S = Shape<TOKENS>;
@@ -104,7 +113,7 @@ __device__ __forceinline__ void swiglu_body(const GroupedArgs& g, int units_n) {
   __amdgpu_buffer_rsrc_t ra, rb, rs, rw;
   uint32_t at_w[2], at_sb[2];
   int kb = 0, lk = 0;  // the step computed, and the step of nxt that loads next
-  bool more = true;
+  bool more = true, done = false;
   auto aim = [&]() {
     find_tile_of<TOKENS>(g.offsets, s_first, g.E, (int)g.rows, units_n, id, lane, &nxt);
     // Rows past the segment's or the weight's end are past the buffers: they
@@ -121,19 +130,33 @@ __device__ __forceinline__ void swiglu_body(const GroupedArgs& g, int units_n) {
       at_sb[h] = (uint32_t)((h * outs + n) / kScaleBlock) * KB * 4;
     }
   };
-  auto load = [&](Raw& raw, int i) {  // load i of step lk
-    if (i < 4)
-      raw.w[i >> 1][i & 1] = __builtin_amdgcn_raw_buffer_load_b128(rb, at_w[i >> 1] + (i & 1) * 64, lk * kScaleBlock, 0);
-    else if (i == 4)
-      raw.s = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at_scale, lk * 4, 0));
-    else if (i < 7)
-      raw.sb[i - 5] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rw, at_sb[i - 5], lk * 4, 0));
-    else if constexpr (S::kParts > 1)
-      raw.t[i - 7] = __builtin_amdgcn_raw_buffer_load_b128(ra, at_token + (i - 7) * 16, lk * kScaleBlock, 0);
-    else {
+  auto load_t = [&](Raw& raw, int i) {
+    if constexpr (S::kParts > 1) {
+      raw.t[i] = __builtin_amdgcn_raw_buffer_load_b128(ra, at_token + i * 16, lk * kScaleBlock, 0);
+    } else {
       const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(ra, at_token, lk * kScaleBlock, 0);
       raw.t[0] = u32x4{v[0], v[1], 0u, 0u};
     }
+  };
+  // Load i of step lk, in the order in which the step before it needs them:
+  // where latency bounds the kernel, that is faster than the weights first (one
+  // token 68 / 72 us, 4 rows to each of 256 experts 1195 / 1266, 32 rows 1436 /
+  // 1523).  Tiles of 128 token rows, which power bounds, are slower with it
+  // (128 rows to each expert 2840 / 2580 us, 1536 rows 5455 / 5320).
+  auto load = [&](Raw& raw, int i) {
+    // 0-3 weights, 4 and 5 tokens, 6 token scale, 7 and 8 weight scales
+    constexpr int kWeightsFirst[] = {0, 1, 2, 3, 6, 7, 8, 4, 5}, kAsNeeded[] = {4, 6, 0, 1, 2, 3, 7, 8};
+    static_assert(TOKENS == 128 || S::kTokenLoads == 1);
+    const int what = TOKENS == 128 ? kWeightsFirst[i] : kAsNeeded[i & 7];
+    if (what < 4)
+      raw.w[what >> 1][what & 1] =
+          __builtin_amdgcn_raw_buffer_load_b128(rb, at_w[what >> 1] + (what & 1) * 64, lk * kScaleBlock, 0);
+    else if (what < 6)
+      load_t(raw, what - 4);
+    else if (what == 6)
+      raw.s = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at_scale, lk * 4, 0));
+    else
+      raw.sb[what - 7] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rw, at_sb[what - 7], lk * 4, 0));
   };
   // A last block that is not full: the lanes hold other bytes past the row's
   // end (the next row's, or zeros past the buffer), which become zeros here.
@@ -215,12 +238,12 @@ __device__ __forceinline__ void swiglu_body(const GroupedArgs& g, int units_n) {
 
   Bf16Frag t;  // the first token rows of the step
   float sa;
+  float sb[2];  // the step's weight scales
   // Step kb of the current tile, from w and LDS copy `here`; `mine` is free,
   // `other` holds the next step's rows, which become wo and the other copy.
-  // False after the last one.
   auto step = [&](Raw& mine, Raw& other, Bf16Frag (&w)[2], Bf16Frag (&wo)[2], int here) {
     const bool last = kb + 1 == KB;
-    const float sb0 = mine.sb[0], sb1 = mine.sb[1];
+    const float sb0 = sb[0], sb1 = sb[1];
     if (!last && kb + 1 == full) clear_tail(other);
     if (lk == KB) {
       lk = 0;
@@ -249,6 +272,10 @@ __device__ __forceinline__ void swiglu_body(const GroupedArgs& g, int units_n) {
         c1 = mfma_bf16(w[1].part[s], now.part[s], c1);
       }
       if (m < S::kParts) widen_token(other, m, here ^ 1);
+      if (m == kTiles - 1) {
+        sb[0] = own_copy(other.sb[0]);
+        sb[1] = own_copy(other.sb[1]);
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (e * kTiles / 8 == m) wo[e >> 2].part[e & 3] = widen_half(other.w[e >> 2][(e >> 1) & 1], e & 1);
@@ -280,13 +307,12 @@ __device__ __forceinline__ void swiglu_body(const GroupedArgs& g, int units_n) {
     ++kb;
     if (last) {
       finish();
-      if (!more) return false;
+      done = !more;
 #pragma unroll
       for (int m = 0; m < kTiles; ++m) acc[0][m] = acc[1][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       cur = nxt;
       kb = 0;
     }
-    return true;
   };
 
   Raw raw[S::kDepth];
@@ -295,6 +321,7 @@ __device__ __forceinline__ void swiglu_body(const GroupedArgs& g, int units_n) {
   cur = nxt;
 #pragma unroll
   for (int d = 0; d < S::kDepth; ++d) {
+    __builtin_amdgcn_sched_barrier(0);  // (in order: the waits count them)
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) load(raw[d], i);
     ++lk;
@@ -303,17 +330,25 @@ __device__ __forceinline__ void swiglu_body(const GroupedArgs& g, int units_n) {
   for (int e = 0; e < 8; ++e) w[0][e >> 2].part[e & 3] = widen_half(raw[0].w[e >> 2][(e >> 1) & 1], e & 1);
 #pragma unroll
   for (int p = 0; p < S::kParts; ++p) widen_token(raw[0], p, 0);
+  sb[0] = raw[0].sb[0];
+  sb[1] = raw[0].sb[1];
   lds_barrier();
   t = token_frag(0, 0);
   sa = s_sa[0][col];
-  if constexpr (S::kDepth == 2) {
-    while (step(raw[0], raw[1], w[0], w[1], 0) && step(raw[1], raw[0], w[1], w[0], 1)) {
+  // One way out: with one after each step, the loads on the way would differ at
+  // the place where they meet, and the compiler's waits go by the fewest.  The
+  // up to kDepth - 1 steps past the end redo the last tile's first ones and
+  // store nothing (a tile has more steps than that).
+  do {
+    step(raw[0], raw[1], w[0], w[1], 0);
+    if constexpr (S::kDepth == 2) {
+      step(raw[1], raw[0], w[1], w[0], 1);
+    } else {
+      step(raw[1], raw[2], w[1], w[0], 1);
+      step(raw[2], raw[3], w[0], w[1], 0);
+      step(raw[3], raw[0], w[1], w[0], 1);
     }
-  } else {
-    while (step(raw[0], raw[1], w[0], w[1], 0) && step(raw[1], raw[2], w[1], w[0], 1) &&
-           step(raw[2], raw[3], w[0], w[1], 0) && step(raw[3], raw[0], w[1], w[0], 1)) {
-    }
-  }
+  } while (!done);
 }
 
 // Two waves per SIMD, 256 registers each.
@@ -337,13 +372,14 @@ hipError_t launch(const Budget& b, const GroupedArgs& g, hipStream_t stream) {
 bool grouped_swiglu_fits(const GroupedArgs& g) { return scale_blocks(g.K) >= Shape<128>::kDepth; }
 
 hipError_t launch_grouped_swiglu(const Budget& b, const GroupedArgs& g, hipStream_t stream) {
-  // Token rows of a tile by the rows there are for each expert.  K 7168, I
-  // 2048, 256 experts, us with 32 / 64 / 128: 4 rows each 1224 / 1357 / 1757,
-  // 16 each 1372 / 1439 / 1813, 32 each 1775 / 1579 / 1862, 64 each 2620 / 2054
-  // / 2061; 64 experts, 1536 each 11170 / 7050 / 5430.
+  // Token rows of a tile by the rows there are for each expert, us with 32 / 64
+  // / 128.  K 7168, I 2048, 256 experts: 4 rows each 1200 / 1280 / 1684, 16 each
+  // 1332 / 1324 / 1738, 32 each 1684 / 1436 / 1811, 64 each 2492 / 1908 / 1995,
+  // 128 each 4430 / 2884 / 2580.  K 2048, I 1024, 16 experts: 8 rows each 24 /
+  // 25 / 33, 64 each 41 / 27 / 34, 128 each 58 / 45 / 35.
   const int64_t each = g.rows / g.E;
-  if (each < 24 && scale_blocks(g.K) >= Shape<32>::kDepth) return launch<32>(b, g, stream);
-  if (each < 64 && scale_blocks(g.K) >= Shape<64>::kDepth) return launch<64>(b, g, stream);
+  if (each < 16 && scale_blocks(g.K) >= Shape<32>::kDepth) return launch<32>(b, g, stream);
+  if (each <= 80 && scale_blocks(g.K) >= Shape<64>::kDepth) return launch<64>(b, g, stream);
   return launch<128>(b, g, stream);
 }
 
