@@ -396,7 +396,7 @@ class _Torch:
         lib()
         self.bf16, self.f32, self.i32, self.f8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
         self.device = torch.cuda.device
-        self.current_device = torch.cuda.current_device
+        self.current_device = torch._C._cuda_getDevice  # (a device tensor is there: torch is initialised)
         self.raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -454,7 +454,7 @@ def ep_dispatch_fp8(x, dest_row, recv_q, recv_scale, stream=None):
     float32 scale for each 128 values: x [T, H] bf16, dest_row [T, k] int32,
     recv_q [R, H] float8_e4m3fn, recv_scale [R, ceil(H / 128)] float32.
     Returns (recv_q, recv_scale)."""
-    th = _torch_objects()
+    th = _torch if _torch is not None and _lib is not None else _torch_objects()
     devices = (_operand(x, "x", th.bf16), _operand(dest_row, "dest_row", th.i32), _operand(recv_q, "recv_q", th.f8),
                _operand(recv_scale, "recv_scale", th.f32))
     xs, ds, qs = x.shape, dest_row.shape, recv_q.shape
@@ -490,7 +490,7 @@ def ep_grouped_gemm_fp8(a, a_scale, offsets, b, b_scale, y, stream=None):
     each expert e: a [rows, K] and b [E, N, K] float8_e4m3fn, their float32
     scales [rows, ceil(K / 128)] and [E, ceil(N / 128), ceil(K / 128)], offsets
     [E + 1] int32 from ep_layout, y [rows, N] bf16.  Returns y."""
-    th = _torch_objects()
+    th = _torch if _torch is not None and _lib is not None else _torch_objects()
     devices, rows, K, E, N = _grouped(th, "ep_grouped_gemm_fp8", a, a_scale, offsets, b, b_scale)
     devices += (_operand(y, "y", th.bf16),)
     if y.shape != (rows, N):
@@ -506,7 +506,7 @@ def ep_grouped_swiglu_fp8(a, a_scale, offsets, b, b_scale, out_q, out_scale, str
     scales: operands as for ep_grouped_gemm_fp8 with b [E, 2 I, K] (I gate rows,
     then I up rows), out_q [rows, I] float8_e4m3fn, out_scale
     [rows, ceil(I / 128)] float32.  Returns (out_q, out_scale)."""
-    th = _torch_objects()
+    th = _torch if _torch is not None and _lib is not None else _torch_objects()
     devices, rows, K, E, N = _grouped(th, "ep_grouped_swiglu_fp8", a, a_scale, offsets, b, b_scale)
     if N % 2:
         raise ValueError("ep_grouped_swiglu_fp8: b must hold as many gate as up rows")
@@ -526,7 +526,7 @@ def ep_combine_backward(dout, y, dest_row, topk_w, dy, dw, stream=None):
     [R, H] bf16, dest_row [T, k] int32, topk_w and dw [T, k] float32.  dy or dw
     may be None (not wanted); y may be None without dw, topk_w without dy.
     Returns (dy, dw)."""
-    th = _torch_objects()
+    th = _torch if _torch is not None and _lib is not None else _torch_objects()
     bf16, f32 = th.bf16, th.f32
     devices = [_operand(dout, "dout", bf16), _operand(dest_row, "dest_row", th.i32)]
     gs, ds = dout.shape, dest_row.shape
@@ -566,7 +566,7 @@ def ep_combine_backward(dout, y, dest_row, topk_w, dy, dw, stream=None):
 def ep_dispatch_backward(drecv, dest_row, dx, stream=None):
     """The gradient of ep_dispatch: dx[t] = bf16(sum_j drecv[dest_row[t, j]]) for
     drecv [R, H] and dx [T, H] bf16, dest_row [T, k] int32.  Returns dx."""
-    th = _torch_objects()
+    th = _torch if _torch is not None and _lib is not None else _torch_objects()
     devices = (_operand(drecv, "drecv", th.bf16), _operand(dest_row, "dest_row", th.i32), _operand(dx, "dx", th.bf16))
     rs, ds, xs = drecv.shape, dest_row.shape, dx.shape
     if len(xs) != 2 or len(ds) != 2 or ds[0] != xs[0]:
