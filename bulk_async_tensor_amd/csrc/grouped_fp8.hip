@@ -7,12 +7,15 @@
 // matrix cores give the inner sum of one whole block for 16 weight rows and 16
 // token rows; it is multiplied by the two scales and added in float32.
 // grouped_wide.hip holds the plain kernel and grouped_swiglu.hip the fused one;
-// here are the choice and the kernel for the K they do not take.  Weights are the A operand and tokens the B
+// here are the choice, the plain kernel for a few rows and the one for the K
+// that those do not take.  Weights are the A operand and tokens the B
 // operand: a lane's results then belong to ONE token (its column) and four
 // adjacent weight rows, so the lane needs one token scale, and the block's
 // weight scale is the same for the whole tile.
 #include "expert_internal.hpp"
 #include "fp8_device.hpp"
+
+#include <type_traits>
 
 namespace ep {
 
@@ -55,6 +58,90 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, i
     before += __builtin_amdgcn_readlane(incl, kWave - 1);
   }
   return false;
+}
+
+constexpr int kFewWaves = 4;  // of 16 weight rows each
+constexpr int kFewCols = 16 * kFewWaves;
+constexpr int kFewRows = 16;
+constexpr int kFewDepth = 8;  // blocks on the way
+
+// A few rows against a few experts, plain: too few tiles of the wide kernel to
+// reach every CU, each of which keeps only so many reads outstanding (27 GB/s
+// of weights).  Each wave streams its 16 weight rows into registers, 8 blocks
+// ahead, against 16 token rows that it reads itself (the caches hold them); the
+// waves share nothing, so 64 weight rows are a workgroup.
+struct FewRaw {
+  u32x4 w[2], t[2];
+  float s, sb;
+};
+
+__global__ __launch_bounds__(kFewWaves * kWave) void grouped_few_kernel(GroupedArgs g, int units_n) {
+  constexpr int D = kFewDepth;
+  const int lane = lane_id();
+  const int col = lane & 15, quad = lane >> 4;
+  const int K = g.K, N = g.N, KB = scale_blocks(K), NB = scale_blocks(N), full = K / kScaleBlock;
+  uint16_t* y = static_cast<uint16_t*>(g.y);
+  for (int64_t u = blockIdx.x;; u += gridDim.x) {
+    RowTile tile;
+    if (!find_tile<kFewRows>(g.offsets, g.E, g.rows, u / units_n, lane, &tile)) break;
+    const int n0 = (int)(u % units_n) * kFewCols + wave_in_group() * 16;
+    if (n0 >= N) continue;
+    // rows past the end: computed on the last row, never stored
+    const uint8_t* wrow = static_cast<const uint8_t*>(g.b) + ((int64_t)tile.e * N + min(n0 + col, N - 1)) * K;
+    const float* wscale = g.b_scale + ((int64_t)tile.e * NB + n0 / kScaleBlock) * KB;
+    const int64_t r = tile.r0 + col, token = r < tile.r1 ? r : tile.r1 - 1;
+    const uint8_t* trow = static_cast<const uint8_t*>(g.a) + token * K;
+    const float* tscale = g.a_scale + token * KB;
+    FewRaw raw[D];
+    // Block kb (past the last one: the last one again; chunks past the row's end: its last one).
+    auto load = [&](FewRaw& f, int kb) {
+      kb = min(kb, KB - 1);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int c = min(kb * kScaleBlock + (quad + 4 * p) * 16, K - 16);
+        f.w[p] = *reinterpret_cast<const u32x4*>(wrow + c);
+        f.t[p] = *reinterpret_cast<const u32x4*>(trow + c);
+      }
+      f.sb = wscale[kb];
+      f.s = tscale[kb];
+    };
+    auto whole = [](const u32x4 (&v)[2], bool in0, bool in1) {
+      i32x8 f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f[q] = in0 ? (int)v[0][q] : 0;
+        f[4 + q] = in1 ? (int)v[1][q] : 0;
+      }
+      return f;
+    };
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    // D blocks from kb on; last: those past the row's end add zeros.
+    auto group = [&](int kb, auto is_last) {
+      constexpr bool kLast = decltype(is_last)::value;
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        __builtin_amdgcn_sched_barrier(0);  // (the loads stay in their order: the waits count them)
+        const int c = (kb + d) * kScaleBlock + quad * 16;
+        const bool in0 = !kLast || c < K, in1 = !kLast || c + 64 < K, in = !kLast || kb + d < KB;
+        const f32x4 p = mfma_e4m3(whole(raw[d].w, in0, in1), whole(raw[d].t, in0, in1));
+        const float s = in ? raw[d].s * raw[d].sb : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(p[i], s, acc[i]);
+        if (!kLast) load(raw[d], kb + D + d);
+      }
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      __builtin_amdgcn_sched_barrier(0);
+      load(raw[d], d);
+    }
+    int kb = 0;
+    for (; kb + D <= full; kb += D) group(kb, std::false_type());
+    group(kb, std::true_type());
+    const int n = n0 + 4 * quad;
+    if (r < tile.r1 && n < N)
+      *reinterpret_cast<u32x2*>(y + r * N + n) = u32x2{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3])};
+  }
 }
 
 constexpr int kNarrowWaves = 8;
@@ -215,21 +302,42 @@ static int wide_rows(const Budget& b, const GroupedArgs& g) {
   return 8 * rounds(256) <= 5 * rounds(128) ? 256 : 128;
 }
 
+// Whether the wide kernel's tiles leave half of the CUs without one, with a
+// tile of 16 rows enough for most experts.  Measured, wide against few: 8 rows
+// to 8 of 64 experts, K 7168, N 2048 (64 tiles) 47 / 23 us, K 2048, N 4096 (128)
+// 17.9 / 18.4, K 2048, N 7168 (224) 22 / 32; 5 rows to each of 16, K = N = 1024
+// (64) 11.2 / 11.1, 10 rows each 11.2 / 19.5.
+static bool few_rows(const Budget& b, const GroupedArgs& g) {
+  const int64_t units_n = (g.N + 255) / 256, held = g.E < g.rows ? g.E : g.rows;
+  return 2 * units_n * held <= b.device_cus && g.rows <= 8 * (int64_t)g.E;
+}
+
+// One workgroup for each tile there can be: every expert may end inside one.
+static int grid_of(const GroupedArgs& g, int rows, int64_t units_n) {
+  const int64_t tiles = g.rows / rows + (g.E < g.rows ? g.E : g.rows), most = 1 << 22;
+  return (int)(tiles * units_n < most ? tiles * units_n : most);
+}
+
+static hipError_t launch_few(const GroupedArgs& g, hipStream_t stream) {
+  const int units_n = (g.N + kFewCols - 1) / kFewCols;
+  hipLaunchKernelGGL(grouped_few_kernel, dim3(grid_of(g, kFewRows, units_n)), dim3(kFewWaves * kWave), 0, stream, g,
+                     units_n);
+  return hipGetLastError();
+}
+
 template <bool SWIGLU>
 static hipError_t launch_narrow(const GroupedArgs& g, hipStream_t stream) {
   const int outs = SWIGLU ? g.N / 2 : g.N, per = SWIGLU ? kNarrowCols : 2 * kNarrowCols;
   const int units_n = (outs + per - 1) / per;
-  // one workgroup for each tile there can be: every expert may end inside one
-  const int64_t tiles = g.rows / kNarrowRows + (g.E < g.rows ? g.E : g.rows);
-  const int64_t want = tiles * units_n, most = 1 << 22;
-  const int grid = (int)(want < most ? want : most);
-  hipLaunchKernelGGL(grouped_narrow_kernel<SWIGLU>, dim3(grid), dim3(kNarrowWaves * kWave), 0, stream, g, units_n);
+  hipLaunchKernelGGL(grouped_narrow_kernel<SWIGLU>, dim3(grid_of(g, kNarrowRows, units_n)),
+                     dim3(kNarrowWaves * kWave), 0, stream, g, units_n);
   return hipGetLastError();
 }
 
 hipError_t launch_grouped_fp8(const Budget& b, const GroupedArgs& g, bool swiglu, hipStream_t stream) {
   if (swiglu) return grouped_swiglu_fits(g) ? launch_grouped_swiglu(b, g, stream) : launch_narrow<true>(g, stream);
-  return grouped_wide_fits(g) ? launch_grouped_wide(b, g, wide_rows(b, g), stream) : launch_narrow<false>(g, stream);
+  if (!grouped_wide_fits(g)) return launch_narrow<false>(g, stream);
+  return few_rows(b, g) ? launch_few(g, stream) : launch_grouped_wide(b, g, wide_rows(b, g), stream);
 }
 
 }  // namespace ep

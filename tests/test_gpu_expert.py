@@ -193,6 +193,37 @@ def test_streams_of_tiles(T, E, k, K, N):
     check_swiglu(offsets, a, sa, b[:, : 2 * I].contiguous(), sb[:, : ref.blocks(2 * I)].contiguous())
 
 
+# A few rows against a few experts: T, E, k, K, N, with a step more, less and exactly the blocks that are read ahead.
+FEW = [(1, 8, 8, 272, 8), (1, 64, 8, 1024, 328), (1, 64, 8, 1040, 1024), (2, 16, 4, 7168, 2048), (3, 9, 5, 896, 40),
+       (1, 1, 1, 2048, 4096), (20, 16, 2, 2064, 1000), (40, 16, 2, 1152, 1024), (1, 64, 8, 16384, 520),
+       (128, 64, 4, 640, 264), (5, 1024, 8, 912, 72)]
+
+
+@pytest.mark.parametrize("T, E, k, K, N", FEW)
+def test_few_rows(T, E, k, K, N):
+    offsets, _, a, sa, b, sb = operands(T, E, k, K, N, 0, T + K)
+    check_gemm(offsets, a, sa, b, sb)
+    if T * k > 2:  # a NaN in a row's last value, one in a scale and one in a weight reach no other result
+        bits(a)[0, K - 1] = NAN8
+        sa[1, 0] = float("nan")
+        bits(b)[:, 3, K - 16] = NAN8
+        y = torch.zeros(T * k, N, dtype=BF16, device=DEV)
+        ep.ep_grouped_gemm_fp8(a, sa, offsets, b, sb, y)
+        want = torch.zeros(T * k, N, dtype=torch.bool, device=DEV)
+        want[:2] = True
+        want[:, 3] = True
+        assert torch.equal(torch.isnan(y), want)
+
+
+def test_few_rows_of_one_expert():
+    """Many tiles of 16 rows for one of many experts, and none for the others."""
+    rows, E, K, N = 100, 20, 1296, 520
+    a, sa = ref.random_rows(rows + 4, K, 1, DEV)
+    b, sb = ref.random_weights(E, N, K, 2, DEV)
+    offsets = torch.tensor([0] * 7 + [rows] * 14, dtype=torch.int32, device=DEV)
+    check_gemm(offsets, a, sa, b, sb)
+
+
 @pytest.mark.parametrize("K", [16384, 16400, 20000])
 def test_long_rows(K):
     offsets, _, a, sa, b, sb = operands(70, 3, 2, K, 384, 0, K)
