@@ -39,7 +39,7 @@ struct GroupedArgs {
 hipError_t launch_grouped_fp8(const Budget& b, const GroupedArgs& g, bool swiglu, hipStream_t stream);
 
 // ---- grouped_wide.hip: the plain product, bm = 128 or 256 token rows at a time
-bool grouped_wide_fits(const GroupedArgs& g);  // whether it takes this K
+bool grouped_wide_fits(const GroupedArgs& g, int bm);  // whether it takes this K
 hipError_t launch_grouped_wide(const Budget& b, const GroupedArgs& g, int bm, hipStream_t stream);
 
 // ---- grouped_swiglu.hip

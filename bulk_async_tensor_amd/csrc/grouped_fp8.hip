@@ -150,10 +150,10 @@ constexpr int kNarrowRows = 16 * kNarrowTiles;
 constexpr int kNarrowCols = 128;              // swiglu: output columns per workgroup (256 weight rows)
 
 // For the K that the other kernels do not take (swiglu: one scale block; plain:
-// one or two, or more than the 128 whose weight scales fit in LDS): each wave
-// streams two tiles of 16 weight rows from memory straight into the matrix
-// cores against up to 64 token rows.  swiglu: the two tiles are the gate and
-// the up rows of the same 16 outputs.
+// one, two with a few rows, or more than the 128 whose weight scales fit in
+// LDS): each wave streams two tiles of 16 weight rows from memory straight into
+// the matrix cores against up to 64 token rows.  swiglu: the two tiles are the
+// gate and the up rows of the same 16 outputs.
 template <bool SWIGLU>
 __global__ __launch_bounds__(kNarrowWaves * kWave) void grouped_narrow_kernel(GroupedArgs g, int units_n) {
   __shared__ float s_max[kNarrowWaves][kNarrowRows];
@@ -336,8 +336,13 @@ static hipError_t launch_narrow(const GroupedArgs& g, hipStream_t stream) {
 
 hipError_t launch_grouped_fp8(const Budget& b, const GroupedArgs& g, bool swiglu, hipStream_t stream) {
   if (swiglu) return grouped_swiglu_fits(g) ? launch_grouped_swiglu(b, g, stream) : launch_narrow<true>(g, stream);
-  if (!grouped_wide_fits(g)) return launch_narrow<false>(g, stream);
-  return few_rows(b, g) ? launch_few(g, stream) : launch_grouped_wide(b, g, wide_rows(b, g), stream);
+  // Two blocks (K <= 256) fit the wide kernel's tiles of 256 rows only.  N 4096,
+  // 16 experts, narrow against wide, us: 8 rows each 7.6 / 10.0, 32 each 12.6 /
+  // 10.6, 512 each 78 / 32.
+  const int bm = scale_blocks(g.K) == 2 ? 256 : wide_rows(b, g);
+  if (!grouped_wide_fits(g, bm) || (scale_blocks(g.K) == 2 && g.rows < 16 * (int64_t)g.E))
+    return launch_narrow<false>(g, stream);
+  return few_rows(b, g) ? launch_few(g, stream) : launch_grouped_wide(b, g, bm, stream);
 }
 
 }  // namespace ep

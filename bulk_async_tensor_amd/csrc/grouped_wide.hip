@@ -393,10 +393,10 @@ hipError_t launch(const Budget& b, const GroupedArgs& g, hipStream_t stream) {
 
 }  // namespace
 
-bool grouped_wide_fits(const GroupedArgs& g) {
+bool grouped_wide_fits(const GroupedArgs& g, int bm) {
   // (a tile shorter than the copies would be two tiles ahead of its results)
   const int blocks = scale_blocks(g.K);
-  return blocks >= Wide<128>::S && blocks <= kWideMaxBlocks;
+  return blocks >= (bm == 256 ? Wide<256>::S : Wide<128>::S) && blocks <= kWideMaxBlocks;
 }
 
 hipError_t launch_grouped_wide(const Budget& b, const GroupedArgs& g, int bm, hipStream_t stream) {

@@ -182,7 +182,8 @@ def test_products_of_uneven_experts(counts):
 # T, E, k, K, N (swiglu: about N / 4 outputs, half a tile past whole ones).
 STREAMS = [(1500, 512, 4, 256, 2304), (1500, 512, 4, 528, 2304), (1500, 512, 4, 1168, 2304), (1500, 150, 4, 272, 2304),
            (1500, 150, 4, 640, 2304), (1500, 150, 4, 1280, 2304), (4096, 4, 4, 272, 2304), (4096, 4, 4, 384, 2304),
-           (4096, 4, 4, 1040, 2304), (2100, 12, 4, 400, 4352), (2100, 12, 4, 1152, 4352)]
+           (4096, 4, 4, 1040, 2304), (2100, 12, 4, 400, 4352), (2100, 12, 4, 1152, 4352), (4096, 4, 4, 256, 2304),
+           (2100, 12, 4, 208, 4352), (3000, 8, 2, 144, 4352)]
 
 
 @pytest.mark.parametrize("T, E, k, K, N", STREAMS)
