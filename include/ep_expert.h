@@ -78,8 +78,9 @@ int ep_dispatch_fp8(const void* x, int T, int H, const int32_t* dest_row, int k,
  * 8-bit instruction: it lines each 8 adjacent products up with the largest of
  * them and drops what lies 2^-13 of it and further below; on random values a
  * block's sum is off by 1.4e-5 of its standard deviation, a hundredth of the
- * rounding to bf16 that follows.  Which of its kernels runs follows from the
- * sizes alone, so equal calls give equal bits.
+ * rounding to bf16 that follows.  Its kernels, chosen by the sizes and the
+ * compute units there are, take the same sums in the same order: a row's bits
+ * depend on the row and the weight alone.
  *   a        e4m3 [rows, K], K % 16 == 0       a_scale  float32 [rows, ceil(K / 128)]
  *   offsets  int32 [E + 1] from ep_layout, non-decreasing; they are clamped
  *            to [0, rows], so no value reaches outside the buffers

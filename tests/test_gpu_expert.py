@@ -241,6 +241,27 @@ def test_equal_calls_give_equal_bits():
             same(u, v)
 
 
+@pytest.mark.parametrize("K", [208, 912, 1024])
+def test_bits_do_not_depend_on_the_buffer(K):
+    """The kernel is chosen by the rows of the buffer; each takes the same sums
+    in the same order, so the rows that are held keep their bits."""
+    E, N, held_rows = 16, 384, 40
+    a, sa = ref.random_rows(6000, K, 1, DEV)
+    b, sb = ref.random_weights(E, N, K, 2, DEV)
+    ends = torch.arange(E + 1, device=DEV) * held_rows // E
+    out = []
+    for rows in (held_rows, 300, 1000, 6000):
+        y = torch.zeros(rows, N, dtype=BF16, device=DEV)
+        q, s = torch.zeros(rows, N // 2, dtype=torch.uint8, device=DEV).view(F8), torch.zeros(rows, 2, device=DEV)
+        off = ends.to(torch.int32)
+        ep.ep_grouped_gemm_fp8(a[:rows], sa[:rows], off, b, sb, y)
+        ep.ep_grouped_swiglu_fp8(a[:rows], sa[:rows], off, b, sb, q, s)
+        out.append((y[:held_rows], q[:held_rows], s[:held_rows]))
+    for other in out[1:]:
+        for u, v in zip(out[0], other):
+            same(u, v)
+
+
 @pytest.mark.parametrize("K, E, counts", [(112, 3, [70, 1, 329]), (272, 3, [70, 1, 329]), (656, 3, [70, 1, 329]),
                                           (656, 9, [20, 30, 50, 1, 0, 70, 40, 60, 80]),
                                           (656, 20, [11, 1, 28] + [10] * 17)])
