@@ -16,6 +16,7 @@
 // dispatch_backward 88.5 us, 6.0 TB/s (a 4 GiB copy reaches 4.8).
 #include "ep_device.hpp"
 #include "expert_internal.hpp"
+#include "expert_shapes.hpp"
 #include "row_io.hpp"
 
 namespace ep {
@@ -234,12 +235,12 @@ DispatchFn pick_steps(int steps) {
 }
 
 template <bool NT>
-DispatchFn pick_dispatch(int k, int steps) {
-  return k == 1   ? pick_steps<1, 4, true, NT>(steps)
-         : k == 2 ? pick_steps<2, 4, true, NT>(steps)
-         : k <= 4 ? pick_steps<4, 2, true, NT>(steps)
-         : k <= 8 ? pick_steps<8, 1, true, NT>(steps)
-                  : pick_steps<8, 1, false, NT>(steps);
+DispatchFn pick_dispatch(int k, const GatherShape& s) {
+  return k == 1   ? (s.vs == 4 ? pick_steps<1, 4, true, NT>(s.steps) : pick_steps<1, 2, true, NT>(s.steps))
+         : k == 2 ? (s.vs == 4 ? pick_steps<2, 4, true, NT>(s.steps) : pick_steps<2, 2, true, NT>(s.steps))
+         : k <= 4 ? pick_steps<4, 2, true, NT>(s.steps)
+         : k <= 8 ? pick_steps<8, 1, true, NT>(s.steps)
+                  : pick_steps<8, 1, false, NT>(s.steps);
 }
 
 }  // namespace
@@ -270,15 +271,9 @@ hipError_t launch_dispatch_backward(const Budget& b, const void* drecv, int64_t 
   // an empty buffer: every slot is out of range, and dx stands in for the row that such slots read
   if (recv_rows == 0) drecv = dx;
   const int cus = b.num_cus > 0 && b.num_cus < b.device_cus ? b.num_cus : b.device_cus;
-  // Segments of up to 8 KiB, of 4 KiB for k <= 4 (T = 8192, H = 4096: k = 4 57
-  // against 61 us, k = 2 35 against 36; k = 8, H = 7168 keeps 8: 88 against 93
-  // at T = 4096), shorter where a batch would leave CUs without 8 waves.
-  int most = k <= 4 ? 4 : 8;
-  while (most > 2 && (int64_t)T * ((nv + most - 1) / most) < 8LL * cus) most /= 2;
-  const int vs = k <= 2 ? 4 : k <= 4 ? 2 : 1;
-  const int nsteps = (nv + vs - 1) / vs, nseg = (nsteps * vs + most - 1) / most;
-  const int steps = (nsteps + nseg - 1) / nseg;
-  const DispatchFn fn = stream_rows((int64_t)T * k * H * 2) ? pick_dispatch<true>(k, steps) : pick_dispatch<false>(k, steps);
+  const GatherShape shape = dispatch_backward_shape(T, nv, k, cus);
+  const int nseg = shape.nseg;
+  const DispatchFn fn = stream_rows((int64_t)T * k * H * 2) ? pick_dispatch<true>(k, shape) : pick_dispatch<false>(k, shape);
   if (!fn) return hipErrorInvalidValue;
   const int units = T * nseg;  // at most EP_MAX_ENTRIES (checked by the ABI)
   constexpr int kWaves = 4;

@@ -1,0 +1,33 @@
+// How the expert side's launches cut their work, from sizes alone: plain C++
+// without HIP, so that the rules can be checked on any host.
+#pragma once
+
+#include <stdint.h>
+
+namespace ep {
+
+// ep_dispatch_backward: a token's row of nv vectors per lane in nseg segments
+// (one wave each) of `steps` steps of vs vectors.
+struct GatherShape {
+  int vs, nseg, steps;
+};
+
+// Segments of up to 8 KiB, of 4 KiB for k <= 4 (T = 8192, H = 4096: k = 4 57
+// against 61 us, k = 2 35 against 36; k = 8, H = 7168 keeps 8: 88 against 93
+// at T = 4096), shorter where a batch would leave CUs without 8 waves.  A step
+// gathers 4, 2 or 1 vectors at k <= 2, k <= 4 and above, and never more than a
+// segment holds: every segment starts inside the row.  Segments of 2 vectors
+// against segments of 4 at k = 2: T = 128, H = 7168 2.33 / 2.55 us, T = 1000,
+// H = 1024 2.34 / 2.56, T = 2000 2.76 / 3.02; k = 1 gains half of that.
+inline GatherShape dispatch_backward_shape(int64_t T, int nv, int k, int cus) {
+  int most = k <= 4 ? 4 : 8;
+  while (most > 2 && T * ((nv + most - 1) / most) < 8LL * cus) most /= 2;
+  GatherShape s;
+  s.vs = k <= 2 ? most : k <= 4 ? 2 : 1;
+  const int nsteps = (nv + s.vs - 1) / s.vs;
+  s.nseg = (nsteps * s.vs + most - 1) / most;
+  s.steps = (nsteps + s.nseg - 1) / s.nseg;
+  return s;
+}
+
+}  // namespace ep

@@ -1,0 +1,40 @@
+"""How the expert side's launches cut their work (csrc/expert_shapes.hpp),
+checked on the host: the header is plain C++ and is compiled here."""
+
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def shapes(tmp_path_factory):
+    """A function from lines of arguments to the rows of numbers chosen for them."""
+    exe = str(tmp_path_factory.mktemp("shapes") / "expert_shapes")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I",
+                    os.path.join(ROOT, "bulk_async_tensor_amd", "csrc"),
+                    os.path.join(ROOT, "tests", "expert_shapes.cpp"), "-o", exe], check=True)
+
+    def ask(lines):
+        res = subprocess.run([exe], input="\n".join(lines) + "\n", capture_output=True, text=True, check=True)
+        rows = [tuple(int(v) for v in line.split()) for line in res.stdout.splitlines()]
+        assert len(rows) == len(lines)
+        return rows
+
+    return ask
+
+
+def test_dispatch_backward_segments(shapes):
+    """The segments cover the row, and none of them starts past its end; the
+    steps are among those that kernels are compiled for."""
+    sizes = [(T, nv, k, cus) for T in (1, 2, 31, 128, 400, 777, 2000, 4096, 100000) for nv in range(1, 41)
+             for k in (1, 2, 3, 4, 5, 8, 9, 32) for cus in (1, 24, 256)]
+    for size, (vs, nseg, steps) in zip(sizes, shapes(["dispatch_backward %d %d %d %d" % s for s in sizes])):
+        nv, k = size[1], size[2]
+        assert nseg >= 1 and steps >= 1, size
+        assert nseg * steps * vs >= nv, f"{size}: the row's end is left out"
+        assert (nseg - 1) * steps * vs < nv, f"{size}: a segment holds nothing of the row"
+        assert (vs, steps) in ({(4, 1), (2, 1)} if k <= 2 else {(2, 1), (2, 2)} if k <= 4
+                               else {(1, n) for n in range(1, 9)}), size
