@@ -212,35 +212,22 @@ CombineFn pick_combine(int vpl, bool nt, bool dy, bool dw) {
 
 using DispatchFn = void (*)(const u32x4*, u32x4*, const int32_t*, int64_t, int, int, int, int, int);
 
-// Segments of `steps` steps (a last step may be partly past the row's end).
-template <int KS, int VS, bool ONE, bool NT>
+// The kernel of 1 .. MOST steps (a last step may be partly past the row's end).
+template <int KS, int VS, int MOST, bool ONE, bool NT>
 DispatchFn pick_steps(int steps) {
-  switch (steps) {
-    case 1: return dispatch_backward_kernel<KS, VS, 1, ONE, NT>;
-    case 2: return dispatch_backward_kernel<KS, VS, 2, ONE, NT>;
-    case 3:
-      if constexpr (VS <= 2) return dispatch_backward_kernel<KS, VS, 3, ONE, NT>;
-    case 4:
-      if constexpr (VS <= 2) return dispatch_backward_kernel<KS, VS, 4, ONE, NT>;
-    case 5:
-      if constexpr (VS == 1) return dispatch_backward_kernel<KS, VS, 5, ONE, NT>;
-    case 6:
-      if constexpr (VS == 1) return dispatch_backward_kernel<KS, VS, 6, ONE, NT>;
-    case 7:
-      if constexpr (VS == 1) return dispatch_backward_kernel<KS, VS, 7, ONE, NT>;
-    default:
-      if constexpr (VS == 1) return dispatch_backward_kernel<KS, VS, 8, ONE, NT>;
-      else return nullptr;
-  }
+  if (steps == MOST) return dispatch_backward_kernel<KS, VS, MOST, ONE, NT>;
+  if constexpr (MOST > 1) return pick_steps<KS, VS, MOST - 1, ONE, NT>(steps);
+  return nullptr;
 }
 
+// The shapes that dispatch_backward_shape gives: 4 vectors a segment for k <= 4, 8 above.
 template <bool NT>
 DispatchFn pick_dispatch(int k, const GatherShape& s) {
-  return k == 1   ? (s.vs == 4 ? pick_steps<1, 4, true, NT>(s.steps) : pick_steps<1, 2, true, NT>(s.steps))
-         : k == 2 ? (s.vs == 4 ? pick_steps<2, 4, true, NT>(s.steps) : pick_steps<2, 2, true, NT>(s.steps))
-         : k <= 4 ? pick_steps<4, 2, true, NT>(s.steps)
-         : k <= 8 ? pick_steps<8, 1, true, NT>(s.steps)
-                  : pick_steps<8, 1, false, NT>(s.steps);
+  return k == 1   ? (s.vs == 4 ? pick_steps<1, 4, 1, true, NT>(s.steps) : pick_steps<1, 2, 1, true, NT>(s.steps))
+         : k == 2 ? (s.vs == 4 ? pick_steps<2, 4, 1, true, NT>(s.steps) : pick_steps<2, 2, 1, true, NT>(s.steps))
+         : k <= 4 ? pick_steps<4, 2, 2, true, NT>(s.steps)
+         : k <= 8 ? pick_steps<8, 1, 8, true, NT>(s.steps)
+                  : pick_steps<8, 1, 8, false, NT>(s.steps);
 }
 
 }  // namespace

@@ -2,11 +2,19 @@
 checked on the host: the header is plain C++ and is compiled here."""
 
 import os
+import re
 import subprocess
 
 import pytest
 
+from bulk_async_tensor_amd import LIB_PATH
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+# T, vectors per lane of a row, k, compute units
+BACKWARD = [(T, nv, k, cus) for T in (1, 2, 31, 128, 400, 777, 2000, 4096, 100000) for nv in range(1, 41)
+            for k in (1, 2, 3, 4, 5, 8, 9, 32) for cus in (1, 24, 256)]
 
 
 @pytest.fixture(scope="module")
@@ -29,12 +37,21 @@ def shapes(tmp_path_factory):
 def test_dispatch_backward_segments(shapes):
     """The segments cover the row, and none of them starts past its end; the
     steps are among those that kernels are compiled for."""
-    sizes = [(T, nv, k, cus) for T in (1, 2, 31, 128, 400, 777, 2000, 4096, 100000) for nv in range(1, 41)
-             for k in (1, 2, 3, 4, 5, 8, 9, 32) for cus in (1, 24, 256)]
-    for size, (vs, nseg, steps) in zip(sizes, shapes(["dispatch_backward %d %d %d %d" % s for s in sizes])):
+    for size, (vs, nseg, steps) in zip(BACKWARD, shapes(["dispatch_backward %d %d %d %d" % s for s in BACKWARD])):
         nv, k = size[1], size[2]
         assert nseg >= 1 and steps >= 1, size
         assert nseg * steps * vs >= nv, f"{size}: the row's end is left out"
         assert (nseg - 1) * steps * vs < nv, f"{size}: a segment holds nothing of the row"
         assert (vs, steps) in ({(4, 1), (2, 1)} if k <= 2 else {(2, 1), (2, 2)} if k <= 4
                                else {(1, n) for n in range(1, 9)}), size
+
+
+def test_dispatch_backward_kernels_are_all_reached(shapes):
+    """The library holds the kernels that some call reaches, and no other."""
+    names = subprocess.run(["nm", "-C", LIB_PATH], capture_output=True, text=True, check=True).stdout
+    # rows at a time, vectors, steps, whether k is at most the rows at a time (and the load policy: both)
+    built = {m for m in re.findall(r"__device_stub__dispatch_backward_kernel<(\d+), (\d+), (\d+), (\w+), true>", names)}
+    reached = set()
+    for (_, _, k, _), (vs, _, steps) in zip(BACKWARD, shapes(["dispatch_backward %d %d %d %d" % s for s in BACKWARD])):
+        reached.add((str(k if k <= 2 else 4 if k <= 4 else 8), str(vs), str(steps), "true" if k <= 8 else "false"))
+    assert built == reached
