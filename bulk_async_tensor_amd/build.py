@@ -33,7 +33,7 @@ KERNEL_SOURCES = {
     "layout_dispatch": ["layout_dispatch.hip", "row_io.hpp", "ep_device.hpp", "ep_internal.hpp"],
     "dispatch_fp8": ["dispatch_fp8.hip", "fp8_device.hpp", "expert_internal.hpp", "ep_device.hpp", "ep_internal.hpp"],
     "grouped_fp8": ["grouped_fp8.hip", "grouped_wide.hip", "grouped_swiglu.hip", "grouped_tiles.hpp", "fp8_device.hpp",
-                    "expert_internal.hpp", "ep_device.hpp", "ep_internal.hpp"],
+                    "expert_shapes.hpp", "expert_internal.hpp", "ep_device.hpp", "ep_internal.hpp"],
     "backward": ["backward.hip", "expert_shapes.hpp", "row_io.hpp", "expert_internal.hpp", "ep_device.hpp",
                  "ep_internal.hpp"],
 }

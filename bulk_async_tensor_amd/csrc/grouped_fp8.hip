@@ -13,6 +13,7 @@
 // adjacent weight rows, so the lane needs one token scale, and the block's
 // weight scale is the same for the whole tile.
 #include "expert_internal.hpp"
+#include "expert_shapes.hpp"
 #include "fp8_device.hpp"
 
 #include <type_traits>
@@ -288,20 +289,6 @@ __global__ __launch_bounds__(kNarrowWaves * kWave) void grouped_narrow_kernel(Gr
 
 }  // namespace
 
-// Token rows per workgroup of the wide kernel.  A tile of 256 takes 1.6 times
-// as long as one of 128 where the products bound it, so the choice goes by the
-// rounds of tiles that the compute units make (every expert's last tile is
-// taken as half full).  Measured, 128 against 256: 32 experts, K = N = 4096,
-// 128 rows each 148 / 163 us, 512 each 374 / 348, 2048 each 1365 / 1204.
-static int wide_rows(const Budget& b, const GroupedArgs& g) {
-  const int64_t units_n = (g.N + 255) / 256, held = g.E < g.rows ? g.E : g.rows;
-  auto rounds = [&](int bm) {
-    const int64_t tiles = units_n * (2 * g.rows / bm + held) / 2;
-    return (tiles + b.device_cus - 1) / b.device_cus;
-  };
-  return 8 * rounds(256) <= 5 * rounds(128) ? 256 : 128;
-}
-
 // Whether the wide kernel's tiles leave half of the CUs without one, with a
 // tile of 16 rows enough for most experts.  Measured, wide against few: 8 rows
 // to 8 of 64 experts, K 7168, N 2048 (64 tiles) 47 / 23 us, K 2048, N 4096 (128)
@@ -339,7 +326,7 @@ hipError_t launch_grouped_fp8(const Budget& b, const GroupedArgs& g, bool swiglu
   // Two blocks (K <= 256) fit the wide kernel's tiles of 256 rows only.  N 4096,
   // 16 experts, narrow against wide, us: 8 rows each 7.6 / 10.0, 32 each 12.6 /
   // 10.6, 512 each 78 / 32.
-  const int bm = scale_blocks(g.K) == 2 ? 256 : wide_rows(b, g);
+  const int bm = scale_blocks(g.K) == 2 ? 256 : wide_rows(b.device_cus, g.rows, g.E, g.N);
   if (!grouped_wide_fits(g, bm) || (scale_blocks(g.K) == 2 && g.rows < 16 * (int64_t)g.E))
     return launch_narrow<false>(g, stream);
   return few_rows(b, g) ? launch_few(g, stream) : launch_grouped_wide(b, g, bm, stream);

@@ -14,6 +14,11 @@ int main() {
       if (scanf("%lld %d %d %d", &T, &nv, &k, &cus) != 4) return 1;
       const ep::GatherShape s = ep::dispatch_backward_shape(T, nv, k, cus);
       printf("%d %d %d\n", s.vs, s.nseg, s.steps);
+    } else if (!strcmp(what, "wide_rows")) {
+      long long rows;
+      int cus, E, N;
+      if (scanf("%d %lld %d %d", &cus, &rows, &E, &N) != 4) return 1;
+      printf("%d\n", ep::wide_rows(cus, rows, E, N));
     } else {
       return 1;
     }

@@ -55,3 +55,15 @@ def test_dispatch_backward_kernels_are_all_reached(shapes):
     for (_, _, k, _), (vs, _, steps) in zip(BACKWARD, shapes(["dispatch_backward %d %d %d %d" % s for s in BACKWARD])):
         reached.add((str(k if k <= 2 else 4 if k <= 4 else 8), str(vs), str(steps), "true" if k <= 8 else "false"))
     assert built == reached
+
+
+def test_wide_rows_follow_the_rounds(shapes):
+    """A tile of 256 rows, 1.6 times the work of one of 128, only where it saves
+    rounds: never where the tiles of 128 make a single round."""
+    sizes = [(cus, rows, E, N) for cus in (8, 64, 256) for rows in (1, 9, 100, 127, 128, 129, 200, 255, 300, 4096, 100000)
+             for E in (1, 2, 7, 64) for N in (8, 256, 264, 2048)]
+    for (cus, rows, E, N), (bm,) in zip(sizes, shapes(["wide_rows %d %d %d %d" % s for s in sizes])):
+        assert bm in (128, 256)
+        # even if every expert's segment ended in a tile of its own
+        if -(-N // 256) * (rows // 128 + min(E, rows)) <= cus:
+            assert bm == 128, (cus, rows, E, N)

@@ -690,3 +690,10 @@ def test_binding_refusals():
     ]:
         with pytest.raises(err):
             call()
+
+
+@pytest.mark.parametrize("rows", [9, 100, 127, 300])
+def test_one_expert_and_one_tile_of_columns(rows):
+    a, sa = ref.random_rows(rows, 656, rows, DEV)
+    b, sb = ref.random_weights(1, 248, 656, 2, DEV)
+    check_gemm(torch.tensor([0, rows], dtype=torch.int32, device=DEV), a, sa, b, sb)
