@@ -46,4 +46,28 @@ inline int wide_rows(int cus, int64_t rows, int E, int N) {
   return 8 * rounds(256) <= 5 * rounds(128) ? 256 : 128;
 }
 
+// ep_grouped_swiglu_fp8: token rows of a tile, and the steps (blocks along K)
+// whose rows are in registers or on the way; a tile has at least that many
+// (a shorter one would be two tiles ahead of its results).
+struct SwigluShape {
+  int tokens, depth;
+};
+
+// The token rows go by the rows that there are for each expert, us with 32 / 64
+// / 128.  K 7168, I 2048, 256 experts: 4 rows each 1200 / 1280 / 1684, 16 each
+// 1332 / 1324 / 1738, 32 each 1684 / 1436 / 1811, 64 each 2492 / 1908 / 1995,
+// 128 each 4430 / 2884 / 2580.  K 2048, I 1024, 16 experts: 8 rows each 24 /
+// 25 / 33, 64 each 41 / 27 / 34, 128 each 58 / 45 / 35.  Rows of 2 or 3 blocks
+// take the same tiles with 2 steps on the way, I 1024, 256 experts: K 256, 4
+// rows each 35 (32) / 75 (128), 64 each 65 (64) / 76 (128), 72 each 79.5 (64) /
+// 76.5 (128); K 384, 64 each 76 (64) / 87 (128).
+inline SwigluShape swiglu_shape(int64_t rows, int E, int blocks) {
+  const int64_t each = rows / E;
+  SwigluShape s;
+  s.tokens = each < 16 ? 32 : each <= (blocks >= 4 ? 80 : 64) ? 64 : 128;
+  s.depth = s.tokens < 128 && blocks >= 4 ? 4 : 2;
+  return s;
+}
+constexpr int kSwigluLeastBlocks = 2;
+
 }  // namespace ep

@@ -34,6 +34,7 @@
 // LDS rows hold 128 bf16 in 16 chunks of 16 bytes; row r keeps chunk c at place
 // c ^ (r & 15), so the 16 rows read together at one chunk cover all banks.
 #include "expert_internal.hpp"
+#include "expert_shapes.hpp"
 #include "fp8_device.hpp"
 #include "grouped_tiles.hpp"
 
@@ -45,14 +46,14 @@ constexpr int kWaves = 8;
 constexpr int kOuts = 128;      // outputs of a tile: one scale block
 constexpr int kRowBytes = 256;  // of a widened row in LDS
 
-template <int TOKENS>
+template <int TOKENS, int DEPTH>
 struct Shape {
   static constexpr int kTiles = TOKENS / 16;
   static constexpr int kLanes = 512 / TOKENS;           // lanes that widen a token row,
   static constexpr int kParts = TOKENS / 32;            // 8 values at a time
   static constexpr int kTokenLoads = (kParts + 1) / 2;  // of 16 values (or of all 8)
   static constexpr int kLoads = 4 + 3 + kTokenLoads;
-  static constexpr int kDepth = TOKENS == 128 ? 2 : 4;  // steps whose rows are in registers or on the way
+  static constexpr int kDepth = DEPTH;  // steps whose rows are in registers or on the way: 2 or 4
 };
 
 // The bytes a lane brings for a step: 32 of a gate row, 32 of an up row, its
@@ -79,9 +80,9 @@ __device__ __forceinline__ float own_copy(float v) {
   return r;
 }
 
-template <int TOKENS>
+template <int TOKENS, int DEPTH>
 __device__ __forceinline__ void swiglu_body(const GroupedArgs& g, int units_n) {
-  using S = Shape<TOKENS>;
+  using S = Shape<TOKENS, DEPTH>;
   constexpr int kTiles = S::kTiles;
   __shared__ __attribute__((aligned(16))) uint8_t s_t[2][TOKENS * kRowBytes];
   __shared__ float s_sa[2][TOKENS];
@@ -352,35 +353,31 @@ __device__ __forceinline__ void swiglu_body(const GroupedArgs& g, int units_n) {
 }
 
 // Two waves per SIMD, 256 registers each.
-template <int TOKENS>
+template <int TOKENS, int DEPTH>
 __global__ __launch_bounds__(kWaves * kWave) __attribute__((amdgpu_waves_per_eu(2, 2))) void grouped_swiglu_kernel(
     GroupedArgs g, int units_n) {
-  swiglu_body<TOKENS>(g, units_n);
+  swiglu_body<TOKENS, DEPTH>(g, units_n);
 }
 
-template <int TOKENS>
+template <int TOKENS, int DEPTH>
 hipError_t launch(const Budget& b, const GroupedArgs& g, hipStream_t stream) {
   const int units_n = (g.N / 2 + kOuts - 1) / kOuts;
   const int grid = stay_grid(b, wide_tiles_most(g.rows, g.E, TOKENS) * units_n);
-  hipLaunchKernelGGL(grouped_swiglu_kernel<TOKENS>, dim3(grid), dim3(kWaves * kWave), 0, stream, g, units_n);
+  hipLaunchKernelGGL((grouped_swiglu_kernel<TOKENS, DEPTH>), dim3(grid), dim3(kWaves * kWave), 0, stream, g, units_n);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// (a tile shorter than the steps on the way would be two tiles ahead of its results)
-bool grouped_swiglu_fits(const GroupedArgs& g) { return scale_blocks(g.K) >= Shape<128>::kDepth; }
+bool grouped_swiglu_fits(const GroupedArgs& g) { return scale_blocks(g.K) >= kSwigluLeastBlocks; }
 
 hipError_t launch_grouped_swiglu(const Budget& b, const GroupedArgs& g, hipStream_t stream) {
-  // Token rows of a tile by the rows there are for each expert, us with 32 / 64
-  // / 128.  K 7168, I 2048, 256 experts: 4 rows each 1200 / 1280 / 1684, 16 each
-  // 1332 / 1324 / 1738, 32 each 1684 / 1436 / 1811, 64 each 2492 / 1908 / 1995,
-  // 128 each 4430 / 2884 / 2580.  K 2048, I 1024, 16 experts: 8 rows each 24 /
-  // 25 / 33, 64 each 41 / 27 / 34, 128 each 58 / 45 / 35.
-  const int64_t each = g.rows / g.E;
-  if (each < 16 && scale_blocks(g.K) >= Shape<32>::kDepth) return launch<32>(b, g, stream);
-  if (each <= 80 && scale_blocks(g.K) >= Shape<64>::kDepth) return launch<64>(b, g, stream);
-  return launch<128>(b, g, stream);
+  const SwigluShape s = swiglu_shape(g.rows, g.E, scale_blocks(g.K));
+  switch (s.tokens) {
+    case 32: return s.depth == 4 ? launch<32, 4>(b, g, stream) : launch<32, 2>(b, g, stream);
+    case 64: return s.depth == 4 ? launch<64, 4>(b, g, stream) : launch<64, 2>(b, g, stream);
+    default: return launch<128, 2>(b, g, stream);
+  }
 }
 
 }  // namespace ep

@@ -19,6 +19,12 @@ int main() {
       int cus, E, N;
       if (scanf("%d %lld %d %d", &cus, &rows, &E, &N) != 4) return 1;
       printf("%d\n", ep::wide_rows(cus, rows, E, N));
+    } else if (!strcmp(what, "swiglu")) {
+      long long rows;
+      int E, blocks;
+      if (scanf("%lld %d %d", &rows, &E, &blocks) != 3) return 1;
+      const ep::SwigluShape s = ep::swiglu_shape(rows, E, blocks);
+      printf("%d %d\n", s.tokens, s.depth);
     } else {
       return 1;
     }

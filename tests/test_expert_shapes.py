@@ -67,3 +67,21 @@ def test_wide_rows_follow_the_rounds(shapes):
         # even if every expert's segment ended in a tile of its own
         if -(-N // 256) * (rows // 128 + min(E, rows)) <= cus:
             assert bm == 128, (cus, rows, E, N)
+
+
+def test_swiglu_tiles_fit_the_rows(shapes):
+    """An expert's few rows never take a tile of 128, whatever K; a tile has as
+    many blocks as there are steps on the way, and each shape has its kernel."""
+    names = subprocess.run(["nm", "-C", LIB_PATH], capture_output=True, text=True, check=True).stdout
+    built = {(int(t), int(d)) for t, d in re.findall(r"__device_stub__grouped_swiglu_kernel<(\d+), (\d+)>", names)}
+    sizes = [(each * E + E // 2, E, blocks) for each in (0, 1, 15, 16, 40, 64, 65, 80, 81, 128, 5000)
+             for E in (1, 8, 256, 1024) for blocks in (2, 3, 4, 5, 56) if each * E + E // 2 > 0]
+    reached = set()
+    for (rows, E, blocks), (tokens, depth) in zip(sizes, shapes(["swiglu %d %d %d" % s for s in sizes])):
+        each = rows // E
+        assert depth <= blocks, "a tile is shorter than the steps on the way"
+        assert tokens == (32 if each < 16 else 64) if each <= 64 else tokens in (64, 128), (rows, E, blocks)
+        # the scan of 64 experts' tile counts is 32 bits wide
+        assert 64 * (rows // tokens + 1) < 1 << 31
+        reached.add((tokens, depth))
+    assert built == reached

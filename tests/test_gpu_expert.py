@@ -697,3 +697,21 @@ def test_one_expert_and_one_tile_of_columns(rows):
     a, sa = ref.random_rows(rows, 656, rows, DEV)
     b, sb = ref.random_weights(1, 248, 656, 2, DEV)
     check_gemm(torch.tensor([0, rows], dtype=torch.int32, device=DEV), a, sa, b, sb)
+
+
+@pytest.mark.parametrize("K", [144, 272, 384, 400])
+@pytest.mark.parametrize("rows, E", [(900, 300), (6000, 150), (1600, 20)])
+def test_swiglu_of_short_rows(K, rows, E):
+    """Rows of two to four blocks at every tile height, workgroups with several
+    tiles, and the same bits from a buffer that takes the tallest tiles."""
+    g = torch.Generator().manual_seed(rows + K)
+    ends = torch.cat([torch.zeros(1, dtype=torch.int64), torch.randint(0, rows - 3, (E,), generator=g).sort().values])
+    offsets = ends.to(torch.int32).to(DEV)
+    tall = 90 * E
+    a, sa = ref.random_rows(tall, K, 1, DEV)
+    b, sb = ref.random_weights(E, 2 * 448, K, 2, DEV)
+    q, s = check_swiglu(offsets, a[:rows], sa[:rows], b, sb)
+    tq, ts = check_swiglu(offsets, a, sa, b, sb)
+    held_rows = int(ends[-1])
+    same(tq[:held_rows], q[:held_rows])
+    same(ts[:held_rows], s[:held_rows])
