@@ -39,7 +39,8 @@ __device__ __forceinline__ Segment segment_of(const int32_t* __restrict__ offset
 constexpr int kTilesCap = 1 << 29;
 
 // first[e] = tiles before expert e, first[E] = all of them.  One wave.  (64
-// experts' tiles fit 30 bits: BM is 128 or more where rows pass 65536.)
+// experts' tiles fit 30 bits: BM is 128 or more where there are more than 80
+// rows for each expert, 81920 with EP_MAX_EXPERTS of them.)
 template <int BM>
 __device__ __forceinline__ void first_tiles(const int32_t* __restrict__ offsets, int E, int rows, int lane,
                                             int32_t* first) {
