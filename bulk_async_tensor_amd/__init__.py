@@ -427,6 +427,12 @@ def _operand(t, name, dtype):
     return t.get_device()
 
 
+def _int_sizes(name, *sizes):
+    """The C calls take these sizes as int (ctypes would cut a larger one to its low 32 bits)."""
+    if max(sizes) >= 1 << 31:
+        raise ValueError(f"{name}: a size of {max(sizes)} is not below 2^31")
+
+
 def _call_on(th, devices, stream, name, args):
     """Calls entry point `name` with the tensors' device as the current one, on
     the given stream or on the current stream of that device."""
@@ -463,6 +469,7 @@ def ep_dispatch_fp8(x, dest_row, recv_q, recv_scale, stream=None):
     T, H = xs
     if len(qs) != 2 or qs[1] != H or recv_scale.shape != (qs[0], _blocks(H)):
         raise ValueError("recv_q must be [R, H] and recv_scale [R, ceil(H / 128)]")
+    _int_sizes("ep_dispatch_fp8", T, H, ds[1])
     _call_on(th, devices, stream, "ep_dispatch_fp8", (x.data_ptr(), T, H, dest_row.data_ptr(), ds[1],
                                                       recv_q.data_ptr(), recv_scale.data_ptr(), qs[0]))
     return recv_q, recv_scale
@@ -482,6 +489,7 @@ def _grouped(th, what, a, a_scale, offsets, b, b_scale):
         raise ValueError(f"{what}: b_scale must be [E, ceil(N / 128), ceil(K / 128)] = [{E}, {_blocks(N)}, {_blocks(K)}]")
     if offsets.shape != (E + 1,):
         raise ValueError(f"{what}: offsets must be [E + 1] = [{E + 1}]")
+    _int_sizes(what, K, E, N)
     return devices, rows, K, E, N
 
 
@@ -533,6 +541,7 @@ def ep_combine_backward(dout, y, dest_row, topk_w, dy, dw, stream=None):
     if len(gs) != 2 or len(ds) != 2 or ds[0] != gs[0]:
         raise ValueError("dout must be [T, H] and dest_row [T, k]")
     T, H = gs
+    _int_sizes("ep_combine_backward", T, H, ds[1])
     rows = yp = dyp = wp = dwp = None
     if y is not None:
         devices.append(_operand(y, "y", bf16))
@@ -573,6 +582,7 @@ def ep_dispatch_backward(drecv, dest_row, dx, stream=None):
         raise ValueError("dx must be [T, H] and dest_row [T, k]")
     if len(rs) != 2 or rs[1] != xs[1]:
         raise ValueError("drecv must be [R, H]")
+    _int_sizes("ep_dispatch_backward", *xs, ds[1])
     _call_on(th, devices, stream, "ep_dispatch_backward", (drecv.data_ptr(), rs[0], xs[1], dest_row.data_ptr(), xs[0],
                                                            ds[1], dx.data_ptr()))
     return dx

@@ -161,3 +161,39 @@ def test_plain_forms_agree_with_each_other():
     x, vx = torch.randn(5, 16, generator=g, dtype=torch.float64), torch.randn(10, 16, generator=g, dtype=torch.float64)
     dx = ref.dispatch_backward(vx, dest)
     assert abs(float((dx * x).sum()) - float((ref.dispatch(x, dest, 10) * vx).sum())) <= 1e-9
+
+
+def test_binding_refuses_sizes_past_32_bits(monkeypatch):
+    """The C calls take sizes as int: a larger one would arrive cut to its low 32
+    bits (2^32 + 4 tokens as 4).  Shapes only, without memory."""
+    monkeypatch.setattr(ep, "_operand", lambda t, name, dtype: 0)
+    monkeypatch.setattr(ep, "_call_on", lambda *args: pytest.fail("the call went through"))
+    f8, bf16, f32, i32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32
+
+    def t(dtype, *shape):
+        return torch.empty(*shape, dtype=dtype, device="meta")
+
+    big = (1 << 32) + 128
+    nb = big // 128
+    w = t(f32, 4, 2)
+    for call in (
+        lambda: ep.ep_dispatch_fp8(t(bf16, big, 128), t(i32, big, 2), t(f8, 8, 128), t(f32, 8, 1)),
+        lambda: ep.ep_dispatch_fp8(t(bf16, 4, big), t(i32, 4, 2), t(f8, 8, big), t(f32, 8, nb)),
+        lambda: ep.ep_dispatch_fp8(t(bf16, 4, 128), t(i32, 4, big), t(f8, 8, 128), t(f32, 8, 1)),
+        lambda: ep.ep_grouped_gemm_fp8(t(f8, 8, big), t(f32, 8, nb), t(i32, 3), t(f8, 2, 128, big), t(f32, 2, 1, nb),
+                                       t(bf16, 8, 128)),
+        lambda: ep.ep_grouped_gemm_fp8(t(f8, 8, 128), t(f32, 8, 1), t(i32, 3), t(f8, 2, big, 128), t(f32, 2, nb, 1),
+                                       t(bf16, 8, big)),
+        lambda: ep.ep_grouped_gemm_fp8(t(f8, 8, 128), t(f32, 8, 1), t(i32, big + 1), t(f8, big, 128, 128),
+                                       t(f32, big, 1, 1), t(bf16, 8, 128)),
+        lambda: ep.ep_grouped_swiglu_fp8(t(f8, 8, 128), t(f32, 8, 1), t(i32, 3), t(f8, 2, 2 * big, 128),
+                                         t(f32, 2, 2 * nb, 1), t(f8, 8, big), t(f32, 8, nb)),
+        lambda: ep.ep_combine_backward(t(bf16, big, 64), t(bf16, 8, 64), t(i32, big, 2), t(f32, big, 2),
+                                       t(bf16, 8, 64), t(f32, big, 2)),
+        lambda: ep.ep_combine_backward(t(bf16, 4, big), t(bf16, 8, big), t(i32, 4, 2), w, t(bf16, 8, big), w),
+        lambda: ep.ep_dispatch_backward(t(bf16, 8, 64), t(i32, big, 2), t(bf16, big, 64)),
+        lambda: ep.ep_dispatch_backward(t(bf16, 8, big), t(i32, 4, 2), t(bf16, 4, big)),
+        lambda: ep.ep_dispatch_backward(t(bf16, 8, 64), t(i32, 4, big), t(bf16, 4, 64)),
+    ):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
