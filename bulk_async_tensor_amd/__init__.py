@@ -545,16 +545,16 @@ def ep_combine_backward(dout, y, dest_row, topk_w, dy, dw, stream=None):
     rows = yp = dyp = wp = dwp = None
     if y is not None:
         devices.append(_operand(y, "y", bf16))
-        rows, yp = y.shape[0], y.data_ptr()
-        if y.shape != (rows, H):
+        ys = y.shape
+        if len(ys) != 2 or ys[1] != H:
             raise ValueError("y must be [R, H]")
+        rows, yp = ys[0], y.data_ptr()
     if dy is not None:
         devices.append(_operand(dy, "dy", bf16))
-        if rows is None:
-            rows = dy.shape[0]
-        if dy.shape != (rows, H):
+        ys = dy.shape
+        if len(ys) != 2 or ys[1] != H or (rows is not None and ys[0] != rows):
             raise ValueError("dy must be [R, H]")
-        dyp = dy.data_ptr()
+        rows, dyp = ys[0], dy.data_ptr()
     if topk_w is not None:
         devices.append(_operand(topk_w, "topk_w", f32))
         if topk_w.shape != ds:

@@ -197,3 +197,33 @@ def test_binding_refuses_sizes_past_32_bits(monkeypatch):
     ):
         with pytest.raises(ValueError, match="2\\^31"):
             call()
+
+
+def test_binding_refuses_wrong_ranks(monkeypatch):
+    """Every operand of another rank is a ValueError, not an IndexError of the check."""
+    monkeypatch.setattr(ep, "_operand", lambda t, name, dtype: 0)
+    monkeypatch.setattr(ep, "_call_on", lambda *args: pytest.fail("the call went through"))
+    bf16, f32, i32, f8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+
+    def t(dtype, *shape):
+        return torch.empty(shape, dtype=dtype, device="meta")
+
+    good = {
+        ep.ep_dispatch_fp8: [t(bf16, 4, 128), t(i32, 4, 2), t(f8, 8, 128), t(f32, 8, 1)],
+        ep.ep_grouped_gemm_fp8: [t(f8, 8, 128), t(f32, 8, 1), t(i32, 3), t(f8, 2, 128, 128), t(f32, 2, 1, 1),
+                                 t(bf16, 8, 128)],
+        ep.ep_grouped_swiglu_fp8: [t(f8, 8, 128), t(f32, 8, 1), t(i32, 3), t(f8, 2, 128, 128), t(f32, 2, 1, 1),
+                                   t(f8, 8, 64), t(f32, 8, 1)],
+        ep.ep_combine_backward: [t(bf16, 4, 64), t(bf16, 8, 64), t(i32, 4, 2), t(f32, 4, 2), t(bf16, 8, 64),
+                                 t(f32, 4, 2)],
+        ep.ep_dispatch_backward: [t(bf16, 8, 64), t(i32, 4, 2), t(bf16, 4, 64)],
+    }
+    for fn, args in good.items():
+        for i, a in enumerate(args):
+            for shape in ((), (a.numel(),), (*a.shape, 1)):
+                if shape != tuple(a.shape):
+                    with pytest.raises(ValueError):
+                        fn(*args[:i], t(a.dtype, *shape), *args[i + 1 :])
+    y_less = good[ep.ep_combine_backward]
+    with pytest.raises(ValueError):  # dy alone gives the rows
+        ep.ep_combine_backward(y_less[0], None, y_less[2], y_less[3], t(bf16), None)
