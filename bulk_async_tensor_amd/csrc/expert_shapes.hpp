@@ -33,15 +33,15 @@ inline GatherShape dispatch_backward_shape(int64_t T, int nv, int k, int cus) {
 // ep_grouped_gemm_fp8: token rows per workgroup of the wide kernel.  A tile of
 // 256 takes 1.6 times as long as one of 128 where the products bound it, so
 // the choice goes by the rounds of tiles that the compute units make (every
-// expert's last tile is taken as half full, and a tile there is even if it is
-// the only one).  Measured, 128 against 256: 32 experts, K = N = 4096, 128 rows
+// expert's last tile is taken as half full, and a lone half-full tile is a
+// round).  Measured, 128 against 256: 32 experts, K = N = 4096, 128 rows
 // each 148 / 163 us, 512 each 374 / 348, 2048 each 1365 / 1204; one expert of
 // 100 rows, K = 2048, N = 256 20.7 / 23.4.
 inline int wide_rows(int cus, int64_t rows, int E, int N) {
   const int64_t units_n = (N + 255) / 256, held = E < rows ? E : rows;
   auto rounds = [&](int bm) {
-    const int64_t tiles = (units_n * (2 * rows / bm + held) + 1) / 2;
-    return (tiles + cus - 1) / cus;
+    const int64_t tiles = units_n * (2 * rows / bm + held) / 2;
+    return tiles > cus ? (tiles + cus - 1) / cus : 1;
   };
   return 8 * rounds(256) <= 5 * rounds(128) ? 256 : 128;
 }

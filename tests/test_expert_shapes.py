@@ -85,3 +85,9 @@ def test_swiglu_tiles_fit_the_rows(shapes):
         assert 64 * (rows // tokens + 1) < 1 << 31
         reached.add((tokens, depth))
     assert built == reached
+
+
+def test_wide_rows_at_the_edge_of_a_round(shapes):
+    """14 experts of about 722 rows, 3 columns of tiles: 252 tiles of 128 in one
+    round of 256 compute units, where half a tile too many would count as two."""
+    assert shapes(["wide_rows 256 10107 14 608"]) == [(128,)]
