@@ -12,8 +12,8 @@
 // segment of a token's row, gathers it from the k rows step by step and holds
 // the finished vectors; the waves of a workgroup meet between their loads and
 // their stores, so that a CU's loads do not queue behind its own stores.
-// T = 4096, H = 7168, k = 8: combine_backward 184 us, 5.4 TB/s;
-// dispatch_backward 88.5 us, 6.0 TB/s (a 4 GiB copy reaches 4.8).
+// T = 4096, H = 7168, k = 8: combine_backward 183 us, 5.4 TB/s;
+// dispatch_backward 86.4 us, 6.1 TB/s (a 4 GiB copy reaches 4.8).
 #include "ep_device.hpp"
 #include "expert_internal.hpp"
 #include "expert_shapes.hpp"

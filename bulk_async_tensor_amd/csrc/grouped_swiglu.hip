@@ -23,10 +23,11 @@
 // that the next tile's rows are on the way while a tile's last steps and its
 // results are done.
 //
-// 98304 rows, K 7168, I 2048, 64 experts: 5.3 ms, 1.09 PFLOP/s, two thirds of
+// 98304 rows, K 7168, I 2048, 64 experts: 5.2 ms, 1.11 PFLOP/s, two thirds of
 // what a bf16 library product of 16384^3 reaches (1.6): the matrix cores are
-// busy 55 % of the cycles at 1.9 GHz, with 2.5 vector instructions to a matrix
-// instruction.  Each wave widening what it uses took 6.4 ms; 32 x 32 products
+// busy 56 % of the cycles at 1.9 GHz, with 2.4 vector instructions to a matrix
+// instruction.  A tile of one token takes 61 us there, alone or beside 127
+// others: 56 steps of 1.1 us, a pace whose cause is not known.  Each wave widening what it uses took 6.4 ms; 32 x 32 products
 // 5.6; a check for token tiles past the segment's end in each step 6.1 (the
 // branches keep the vector work from running beside the products), so a
 // segment's last tile is computed whole.

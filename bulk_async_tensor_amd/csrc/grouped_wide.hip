@@ -19,11 +19,12 @@
 // copies and two steps' loads on the way.  The stream goes on loading past its
 // end (the last tile again), so that the waits can count the loads.
 //
-// 98304 rows, K 2048, N 7168, 64 experts: 1.60 ms, 1.81 PFLOP/s, 56 % of what
-// an 8-bit library product of 16384^3 reaches.  The clock is down to 1.77 GHz
-// there: the power of both sides' LDS reads, 4 multiply-adds of the block
-// scales to each matrix instruction and the matrix cores together bound it.
-// 4 rows to each of 256 experts: 580 us, 6.4 TB/s of weights.
+// 98304 rows, K 2048, N 7168, 64 experts: 1.52 ms, 1.90 PFLOP/s, 59 % of what
+// an 8-bit library product of 16384^3 reaches, with the matrix cores busy 45 %
+// of the cycles at 1.8 GHz.  What is done once a tile (its results, the next
+// tile's first rows) takes 180 to 240 us of it: the same number of products
+// takes 1738 us at K 1024, 1499 at 2048, 1411 at 4096.  4 rows to each of 256
+// experts: 591 us, 6.3 TB/s of weights.
 //
 // LDS rows are 128 bytes, 8 chunks of 16; row r keeps chunk c at place
 // c ^ (r & 7), so the 16 rows that one instruction reads at one chunk fall on
