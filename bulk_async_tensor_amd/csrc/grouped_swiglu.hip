@@ -26,11 +26,12 @@
 // 98304 rows, K 7168, I 2048, 64 experts: 5.2 ms, 1.11 PFLOP/s, two thirds of
 // what a bf16 library product of 16384^3 reaches (1.6): the matrix cores are
 // busy 56 % of the cycles at 1.9 GHz, with 2.4 vector instructions to a matrix
-// instruction.  A tile of one token takes 61 us there, alone or beside 127
-// others: 56 steps of 1.1 us, a pace whose cause is not known.  Each wave widening what it uses took 6.4 ms; 32 x 32 products
+// instruction.  Each wave widening what it uses took 6.4 ms; 32 x 32 products
 // 5.6; a check for token tiles past the segment's end in each step 6.1 (the
 // branches keep the vector work from running beside the products), so a
-// segment's last tile is computed whole.
+// segment's last tile is computed whole.  A tile of one token takes 61 us at
+// that K, alone or beside 127 others: 56 steps of 1.1 us, a pace whose cause is
+// not known.
 //
 // LDS rows hold 128 bf16 in 16 chunks of 16 bytes; row r keeps chunk c at place
 // c ^ (r & 15), so the 16 rows read together at one chunk cover all banks.

@@ -715,3 +715,10 @@ def test_swiglu_of_short_rows(K, rows, E):
     held_rows = int(ends[-1])
     same(tq[:held_rows], q[:held_rows])
     same(ts[:held_rows], s[:held_rows])
+
+
+@pytest.mark.parametrize("K", [144, 272, 384])
+@pytest.mark.parametrize("E, counts", [(9, [20, 30, 50, 1, 0, 70, 40, 60, 80]), (20, [11, 1, 28] + [10] * 17)])
+def test_swiglu_of_short_rows_does_not_mix(K, E, counts):
+    """A NaN in the last value of a row that ends inside a block, and in weights, at the lower tile heights."""
+    test_swiglu_does_not_mix_rows_or_experts(K, E, counts)

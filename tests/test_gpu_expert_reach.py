@@ -22,9 +22,9 @@ def zeros8(*shape):
 
 
 # ------------------------------------------------------------------ past 4 GiB
-# With 72 experts of 64 MiB, rows of expert 70: a few rows against each expert (swiglu: tiles of 32), then tiles of 128;
-# then K past the wide kernel's.
-@pytest.mark.parametrize("rows, K", [(8, 16384), (40, 16384), (40, 16400)])
+# With 72 experts of 64 MiB, rows of expert 70.  Plain: the few-row kernel, tiles of 128, and (K past 16384) the kernel
+# for long rows; fused: tiles of 32, of 64 and of 128.
+@pytest.mark.parametrize("rows, K", [(8, 16384), (40, 16384), (40, 16400), (1200, 16384), (6000, 16384)])
 def test_weights_past_four_gigabytes(rows, K):
     N, E = 4096, 72
     b = zeros8(E, N, K)
