@@ -10,9 +10,10 @@ call raises ``EpLibraryMissing``.  Build it with
 ``python -m bulk_async_tensor_amd.build``.
 
 The expert side (``include/ep_expert.h``: the 8-bit dispatch, the experts'
-8-bit products, the gradients of combine and dispatch) follows the same
-pattern; its calls take tensors of one device, which need not be the current
-one.
+8-bit products, the gradients of combine and dispatch) and the rest of the
+layer (``include/ep_layer.h``: the router's choice and its gradient, the
+experts' bf16 products and theirs) follow the same pattern; their calls take
+tensors of one device, which need not be the current one.
 """
 
 import ctypes
@@ -33,12 +34,19 @@ EP_MAX_TOPK = 32
 EP_MAX_EXPERTS = 1024
 EP_MAX_ENTRIES = (1 << 31) - 1 - (1 << 22)
 EP_FP8_BLOCK = 128
+EP_BF16, EP_F32 = 0, 1
+EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
+EP_ACT_NONE, EP_ACT_SILU, EP_ACT_GELU, EP_ACT_SWIGLU = 0, 1, 2, 3
+EP_MAX_GROUPS = 64
+EP_LINEAR_MAX_SIDE = 1 << 20
+EP_LINEAR_MAX_WEIGHT = (1 << 30) - 1
 
 VARIANTS = ("auto", "vgpr", "vgpr2", "lds1", "lds2", "vgpr_cached", "phase", "lds3", "pc", "vgpr_wg")
 
 _c_int, _c_i64, _c_sz, _p = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
+_c_f32 = ctypes.c_float
 
-# name -> (restype, argtypes), mirroring include/ep.h and include/ep_expert.h
+# name -> (restype, argtypes), mirroring include/ep.h, include/ep_expert.h and include/ep_layer.h
 _SIGNATURES = {
     "ep_set_num_cus": (_c_int, [_c_int]),
     "ep_get_num_cus": (_c_int, []),
@@ -69,6 +77,17 @@ _SIGNATURES = {
     "ep_grouped_swiglu_fp8": (_c_int, [_p, _p, _c_i64, _c_int, _p, _c_int, _p, _p, _c_int, _p, _p, _p]),
     "ep_combine_backward": (_c_int, [_p, _p, _c_i64, _c_int, _p, _p, _c_int, _c_int, _p, _p, _p]),
     "ep_dispatch_backward": (_c_int, [_p, _c_i64, _c_int, _p, _c_int, _c_int, _p, _p]),
+    "ep_route": (_c_int, [_p, _c_int, _c_int, _c_int, _c_int, _p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_f32, _p,
+                          _p, _p]),
+    "ep_route_backward": (_c_int, [_p, _c_int, _c_int, _c_int, _c_int, _p, _c_int, _c_int, _c_f32, _p, _p, _c_int,
+                                   _p]),
+    "ep_grouped_linear_workspace_bytes": (_c_sz, [_c_i64, _c_int, _c_int, _c_int, _c_int]),
+    "ep_grouped_linear": (_c_int, [_p, _c_i64, _c_int, _p, _c_int, _p, _p, _c_int, _c_int, _p, _p, _c_int, _p, _p,
+                                   _c_sz, _p]),
+    "ep_grouped_linear_dgrad_workspace_bytes": (_c_sz, [_c_i64, _c_int, _c_int, _c_int]),
+    "ep_grouped_linear_dgrad": (_c_int, [_p, _c_i64, _c_int, _p, _c_int, _p, _c_int, _c_int, _p, _p, _p, _c_sz, _p]),
+    "ep_grouped_linear_wgrad_workspace_bytes": (_c_sz, [_c_i64, _c_int, _c_int, _c_int]),
+    "ep_grouped_linear_wgrad": (_c_int, [_p, _p, _c_i64, _c_int, _c_int, _p, _c_int, _p, _c_int, _p, _p, _c_sz, _p]),
 }
 
 
@@ -586,6 +605,222 @@ def ep_dispatch_backward(drecv, dest_row, dx, stream=None):
     _call_on(th, devices, stream, "ep_dispatch_backward", (drecv.data_ptr(), rs[0], xs[1], dest_row.data_ptr(), xs[0],
                                                            ds[1], dx.data_ptr()))
     return dx
+
+
+# ------------------------------------------------------------------ the rest of the layer
+_SCORES = {"softmax": EP_SCORE_SOFTMAX, "sigmoid": EP_SCORE_SIGMOID}
+_ACTS = {"none": EP_ACT_NONE, "silu": EP_ACT_SILU, "gelu": EP_ACT_GELU, "swiglu": EP_ACT_SWIGLU}
+
+
+def _one_of(table, value, what):
+    code = table.get(value) if isinstance(value, str) else None
+    if code is None:
+        raise ValueError(f"{what} must be one of {', '.join(table)}, got {value!r}")
+    return code
+
+
+def _either(th, t, name):
+    """The device index and the type code of a contiguous device tensor, bf16 or float32."""
+    dtype = getattr(t, "dtype", None)
+    if dtype is not th.bf16 and dtype is not th.f32:
+        _device_tensor(t, name)
+        raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
+    return _operand(t, name, dtype), (EP_BF16 if dtype is th.bf16 else EP_F32)
+
+
+def ep_route(logits, topk_idx, topk_w, score="softmax", bias=None, groups=1, top_groups=1, group_best=1,
+             renormalize=True, scale=1.0, stream=None):
+    """The router's choice: the k experts of largest score (softmax or sigmoid of
+    logits [T, E], bf16 or float32) plus bias [E] (float32, for the choice only)
+    within the top_groups of `groups` equal runs of experts, a run ranked by the
+    sum of its group_best largest; topk_idx [T, k] int32 in descending order, topk_w
+    [T, k] float32 their scores times scale, divided by their sum if renormalize.
+    Returns (topk_idx, topk_w)."""
+    th = _torch if _torch is not None and _lib is not None else _torch_objects()
+    dev, kind = _either(th, logits, "logits")
+    devices = [dev, _operand(topk_idx, "topk_idx", th.i32), _operand(topk_w, "topk_w", th.f32)]
+    ls, ts = logits.shape, topk_idx.shape
+    if len(ls) != 2 or len(ts) != 2 or ts[0] != ls[0] or topk_w.shape != ts:
+        raise ValueError("logits must be [T, E], topk_idx and topk_w [T, k]")
+    T, E = ls
+    _int_sizes("ep_route", T, E, ts[1], groups, top_groups, group_best)
+    bp = None
+    if bias is not None:
+        devices.append(_operand(bias, "bias", th.f32))
+        if bias.shape != (E,):
+            raise ValueError(f"bias must be [E] = [{E}]")
+        bp = bias.data_ptr()
+    _call_on(th, devices, stream, "ep_route",
+             (logits.data_ptr(), kind, T, E, _one_of(_SCORES, score, "score"), bp, groups, top_groups, group_best, ts[1],
+              int(bool(renormalize)), scale, topk_idx.data_ptr(), topk_w.data_ptr()))
+    return topk_idx, topk_w
+
+
+def ep_route_backward(logits, topk_idx, dw, dlogits, score="softmax", renormalize=True, scale=1.0, stream=None):
+    """The gradient of ep_route's weights to its logits: dw [T, k] float32 that of
+    topk_w, dlogits [T, E] (bf16 or float32) written whole.  Returns dlogits."""
+    th = _torch if _torch is not None and _lib is not None else _torch_objects()
+    dev, kind = _either(th, logits, "logits")
+    out_dev, out_kind = _either(th, dlogits, "dlogits")
+    devices = (dev, out_dev, _operand(topk_idx, "topk_idx", th.i32), _operand(dw, "dw", th.f32))
+    ls, ts = logits.shape, topk_idx.shape
+    if len(ls) != 2 or len(ts) != 2 or ts[0] != ls[0] or dw.shape != ts or dlogits.shape != ls:
+        raise ValueError("logits and dlogits must be [T, E], topk_idx and dw [T, k]")
+    T, E = ls
+    _int_sizes("ep_route_backward", T, E, ts[1])
+    _call_on(th, devices, stream, "ep_route_backward",
+             (logits.data_ptr(), kind, T, E, _one_of(_SCORES, score, "score"), topk_idx.data_ptr(), ts[1],
+              int(bool(renormalize)), scale, dw.data_ptr(), dlogits.data_ptr(), out_kind))
+    return dlogits
+
+
+def _weight_of(th, what, name, w, offsets, devices):
+    """Checks a weight [E, N, K] (one weight: [N, K] too) and its offsets; (E, N, K, offsets' address)."""
+    shape = w.shape
+    if len(shape) == 2:
+        shape = (1, *shape)
+    if len(shape) != 3:
+        raise ValueError(f"{what}: {name} must be [E, N, K]")
+    E, N, K = shape
+    _int_sizes(what, E, N, K)
+    if offsets is None:
+        if E != 1:
+            raise ValueError(f"{what}: without offsets there is one weight, got {E}")
+        return E, N, K, None
+    devices.append(_operand(offsets, "offsets", th.i32))
+    if offsets.shape != (E + 1,):
+        raise ValueError(f"{what}: offsets must be [E + 1] = [{E + 1}]")
+    return E, N, K, offsets.data_ptr()
+
+
+def ep_grouped_linear_workspace_bytes(rows, K, E, N, act="none"):
+    return lib().ep_grouped_linear_workspace_bytes(int(rows), int(K), int(E), int(N), _one_of(_ACTS, act, "act"))
+
+
+def ep_grouped_linear_dgrad_workspace_bytes(rows, K, E, N):
+    return lib().ep_grouped_linear_dgrad_workspace_bytes(int(rows), int(K), int(E), int(N))
+
+
+def ep_grouped_linear_wgrad_workspace_bytes(rows, K, E, N):
+    return lib().ep_grouped_linear_wgrad_workspace_bytes(int(rows), int(K), int(E), int(N))
+
+
+def _with_workspace(th, what, need, workspace, like, devices, stream, args):
+    if workspace is None and need:
+        import torch
+
+        # torch hands its memory out again in the order of the stream it was
+        # taken on, so it is taken on the stream that the call runs on
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    if workspace is None:
+        space = (None, 0)
+    else:
+        _device_tensor(workspace, "workspace")
+        devices.append(workspace.get_device())
+        space = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _call_on(th, devices, stream, what, (*args, *space))
+
+
+def ep_grouped_linear(a, offsets, b, y, bias=None, act="none", residual=None, pre=None, workspace=None, stream=None):
+    """y[r] = act(a[r] @ b[e]^T + bias[e]) + residual[r] for the rows offsets[e] <= r <
+    offsets[e + 1] of each expert e: a [rows, K] and b [E, N, K] bf16, offsets
+    [E + 1] int32 from ep_layout (None: one weight, [N, K] or [1, N, K], for all
+    rows), bias [E, N] float32, y bf16 or float32 and residual bf16 [rows, N]; act
+    "none", "silu", "gelu" or "swiglu" (N/2 gate rows, then N/2 up rows in b; y and
+    residual have N/2 values a row).  pre [rows, N] bf16 receives the values before
+    the activation.  Returns y."""
+    what = "ep_grouped_linear"
+    th = _torch if _torch is not None and _lib is not None else _torch_objects()
+    y_dev, kind = _either(th, y, "y")
+    devices = [_operand(a, "a", th.bf16), _operand(b, "b", th.bf16), y_dev]
+    E, N, K, off = _weight_of(th, what, "b", b, offsets, devices)
+    code = _one_of(_ACTS, act, "act")
+    if len(a.shape) != 2 or a.shape[1] != K:
+        raise ValueError(f"{what}: a must be [rows, K] = [rows, {K}]")
+    rows = a.shape[0]
+    if code == EP_ACT_SWIGLU and N % 2:
+        raise ValueError(f"{what}: b must hold as many gate as up rows")
+    outs = N // 2 if code == EP_ACT_SWIGLU else N
+    if y.shape != (rows, outs):
+        raise ValueError(f"{what}: y must be [{rows}, {outs}]")
+    bp = rp = pp = None
+    if bias is not None:
+        devices.append(_operand(bias, "bias", th.f32))
+        if bias.shape != (E, N) and (E > 1 or bias.shape != (N,)):
+            raise ValueError(f"{what}: bias must be [E, N] = [{E}, {N}]")
+        bp = bias.data_ptr()
+    if residual is not None:
+        devices.append(_operand(residual, "residual", th.bf16))
+        if residual.shape != (rows, outs):
+            raise ValueError(f"{what}: residual must be [{rows}, {outs}]")
+        rp = residual.data_ptr()
+    if pre is not None:
+        devices.append(_operand(pre, "pre", th.bf16))
+        if pre.shape != (rows, N):
+            raise ValueError(f"{what}: pre must be [{rows}, {N}]")
+        pp = pre.data_ptr()
+    _with_workspace(th, what, _lib.ep_grouped_linear_workspace_bytes(rows, K, E, N, code), workspace, a, devices, stream,
+                    (a.data_ptr(), rows, K, off, E, b.data_ptr(), bp, N, code, rp, y.data_ptr(), kind, pp))
+    return y
+
+
+def ep_grouped_linear_dgrad(dy, offsets, b, dx, act="none", pre=None, workspace=None, stream=None):
+    """The gradient of ep_grouped_linear to its rows, and through the activation
+    that made those rows: dx[r] = act'(pre[r]) * (dy[r] @ b[e]) for dy [rows, N], b
+    [E, N, K], dx and pre [rows, K] bf16 ("swiglu": [rows, 2 K], gate and up
+    halves); pre is None with act "none".  Returns dx."""
+    what = "ep_grouped_linear_dgrad"
+    th = _torch if _torch is not None and _lib is not None else _torch_objects()
+    devices = [_operand(dy, "dy", th.bf16), _operand(b, "b", th.bf16), _operand(dx, "dx", th.bf16)]
+    E, N, K, off = _weight_of(th, what, "b", b, offsets, devices)
+    code = _one_of(_ACTS, act, "act")
+    if len(dy.shape) != 2 or dy.shape[1] != N:
+        raise ValueError(f"{what}: dy must be [rows, N] = [rows, {N}]")
+    rows = dy.shape[0]
+    wide = 2 * K if code == EP_ACT_SWIGLU else K
+    if dx.shape != (rows, wide):
+        raise ValueError(f"{what}: dx must be [{rows}, {wide}]")
+    pp = None
+    if code != EP_ACT_NONE:
+        if pre is None:
+            raise ValueError(f"{what}: an activation's gradient needs pre")
+        devices.append(_operand(pre, "pre", th.bf16))
+        if pre.shape != (rows, wide):
+            raise ValueError(f"{what}: pre must be [{rows}, {wide}]")
+        pp = pre.data_ptr()
+    _with_workspace(th, what, _lib.ep_grouped_linear_dgrad_workspace_bytes(rows, K, E, N), workspace, dy, devices,
+                    stream, (dy.data_ptr(), rows, N, off, E, b.data_ptr(), K, code, pp, dx.data_ptr()))
+    return dx
+
+
+def ep_grouped_linear_wgrad(dy, a, offsets, db, dbias=None, workspace=None, stream=None):
+    """The gradient of ep_grouped_linear to its weights and bias: db[e] = sum of
+    dy[r]^T a[r], dbias[e] = sum of dy[r] over the rows of each expert, for dy
+    [rows, N] and a [rows, K] bf16, db [E, N, K] bf16 or float32, dbias [E, N]
+    float32 or None; zeros for an expert without rows.  Returns (db, dbias)."""
+    what = "ep_grouped_linear_wgrad"
+    th = _torch if _torch is not None and _lib is not None else _torch_objects()
+    db_dev, kind = _either(th, db, "db")
+    devices = [_operand(dy, "dy", th.bf16), _operand(a, "a", th.bf16), db_dev]
+    E, N, K, off = _weight_of(th, what, "db", db, offsets, devices)
+    if len(dy.shape) != 2 or dy.shape[1] != N:
+        raise ValueError(f"{what}: dy must be [rows, N] = [rows, {N}]")
+    rows = dy.shape[0]
+    if a.shape != (rows, K):
+        raise ValueError(f"{what}: a must be [rows, K] = [{rows}, {K}]")
+    bp = None
+    if dbias is not None:
+        devices.append(_operand(dbias, "dbias", th.f32))
+        if dbias.shape != (E, N) and (E > 1 or dbias.shape != (N,)):
+            raise ValueError(f"{what}: dbias must be [E, N] = [{E}, {N}]")
+        bp = dbias.data_ptr()
+    _with_workspace(th, what, _lib.ep_grouped_linear_wgrad_workspace_bytes(rows, K, E, N), workspace, dy, devices,
+                    stream, (dy.data_ptr(), a.data_ptr(), rows, N, K, off, E, db.data_ptr(), kind, bp))
+    return db, dbias
 
 
 # ------------------------------------------------------------------ probes
