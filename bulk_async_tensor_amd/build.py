@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libep.so")
 SOURCES = ["ep_api.hip", "layout.hip", "dispatch.hip", "dispatch_rows.hip", "combine.hip", "combine_reduce.hip",
            "layout_dispatch.hip", "probe.hip", "expert_api.hip", "dispatch_fp8.hip", "grouped_fp8.hip",
-           "grouped_wide.hip", "grouped_swiglu.hip", "backward.hip", "layer_api.hip", "route.hip", "linear.hip"]
+           "grouped_wide.hip", "grouped_swiglu.hip", "backward.hip", "layer_api.hip", "route.hip", "linear_wide.hip"]
 ARCH = "gfx950"
 
 
@@ -35,8 +35,8 @@ KERNEL_SOURCES = {
     "grouped_fp8": ["grouped_fp8.hip", "grouped_wide.hip", "grouped_swiglu.hip", "grouped_tiles.hpp", "fp8_device.hpp",
                     "expert_shapes.hpp", "expert_internal.hpp", "ep_device.hpp", "ep_internal.hpp"],
     "route": ["route.hip", "layer_internal.hpp", "ep_device.hpp", "ep_internal.hpp"],
-    "linear": ["linear.hip", "linear_epilogue.hpp", "layer_internal.hpp", "grouped_tiles.hpp", "ep_device.hpp",
-               "ep_internal.hpp"],
+    "linear": ["linear_wide.hip", "linear_shapes.hpp", "linear_epilogue.hpp", "layer_internal.hpp", "grouped_tiles.hpp",
+               "fp8_device.hpp", "expert_internal.hpp", "ep_device.hpp", "ep_internal.hpp"],
     "backward": ["backward.hip", "expert_shapes.hpp", "row_io.hpp", "expert_internal.hpp", "ep_device.hpp",
                  "ep_internal.hpp"],
 }
