@@ -18,12 +18,13 @@
 // A side that lies along the sum in memory (its rows are the tile's rows) has
 // LDS rows of 128 bytes, 8 chunks of 16; row r keeps chunk c at place
 // c ^ (r & 7).  A side that lies across it has one LDS row for each of the 64
-// places, chunks of 32 bytes: the 16 columns of one product tile.  Row r keeps
-// chunk c at place c ^ (r % 4 + 4 * (r / 8 % 4)), and ds_read_b64_tr_b16 turns
-// four rows of 16 columns into four places along the sum for each lane: the 16
-// rows that one such read touches lie on different banks.  The loads write
-// LDS in lane order, so both exchanges are made in the address each lane loads
-// from.
+// places (the column side one for each half of the columns), chunks of 32
+// bytes: the 16 columns of one product tile.  Row r keeps chunk c at place
+// c ^ (r % 4 + 4 * (r / 8 % 4)), or the low bits of that where a row has 8
+// chunks, and ds_read_b64_tr_b16 turns four rows of 16 columns into four places
+// along the sum for each lane: the 16 rows that one such read touches spread
+// over all banks.  The loads write LDS in lane order, so both exchanges are
+// made in the address each lane loads from.
 //
 // A sum's end inside a step: lanes whose places lie past it load from past the
 // buffer, which brings zeros.  The same holds for steps that only fill a tile
@@ -186,7 +187,7 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   int lk = 0;  // the step of nxt that loads next
   // A lane's place in a load: of 8 rows along the sum, or of 1 KiB of rows across it.
   const int chunk = (lane & 7) ^ (lane >> 3);
-  constexpr int kRowUnits = BM / 8, kColUnits = kCols / 8;  // 16-byte units in an LDS row across the sum
+  constexpr int kRowUnits = BM / 8, kColUnits = kHalf / 8;  // 16-byte units in an LDS row across the sum
   auto across = [&](int units16, int64_t ld, int i) -> uint32_t {  // offset of load i of a side across the sum
     const int ri = kWave / units16;  // rows of a load
     const int r = wave * 8 + i * ri + lane / units16, u = lane % units16;
@@ -202,7 +203,7 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   }
   if constexpr (kColsAcross) {
 #pragma unroll
-    for (int i = 0; i < W::LW; ++i) c_at[i] = across(kColUnits, cld, i);
+    for (int j = 0; j < W::LW; ++j) c_at[j] = across(kColUnits, cld, j % (W::LW / 2)) + j / (W::LW / 2) * kHalf * 2;
   } else {
     c_at[0] = (uint32_t)((lane >> 3) * cld * 2) + chunk * 16;
   }
@@ -295,11 +296,13 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
         if constexpr (kRowsAcross) load16_to_lds(rb, lds, r_at[i], 0);
         else load16_to_lds(rb, lds, (r_at[0] + (uint32_t)((wave * (BM / kWaves) + i * 8) * rld * 2)) | mask, base_k);
       } else {
-        const int j = i - W::LT;
+        const int j = i - W::LT, h = j / (W::LW / 2);
         if constexpr (kColsAcross) {
-          load16_to_lds(cb, stage + W::kT + wave * (kCols * kStepBytes / kWaves) + j * 1024, c_at[j], 0);
+          load16_to_lds(cb, stage + W::kT + h * kHalf * kStepBytes + wave * (kHalf * kStepBytes / kWaves) +
+                                j % (W::LW / 2) * 1024,
+                        c_at[j], 0);
         } else {
-          const int h = j / (W::LW / 2), r = wave * (kHalf / kWaves) + j % (W::LW / 2) * 8;
+          const int r = wave * (kHalf / kWaves) + j % (W::LW / 2) * 8;
           const int row = (h ? half1 : nxt.c0) + r;
           load16_to_lds(cb, stage + W::kT + (h * kHalf + r) * kStepBytes, (c_at[0] + (uint32_t)(row * cld * 2)) | mask,
                         base_k);
@@ -335,9 +338,10 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
     return r;
   };
   auto col_frag = [&](uint32_t stage, int n) {
-    const int t = (n < HT ? 0 : kHalf / 16) + wn * HT + n % HT;
-    if constexpr (kColsAcross) return across_frag(stage + W::kT, kCols, t);
-    else return along_frag(stage + W::kT + t * 16 * kStepBytes);
+    const uint32_t half = stage + W::kT + n / HT * kHalf * kStepBytes;
+    const int t = wn * HT + n % HT;
+    if constexpr (kColsAcross) return across_frag(half, kHalf, t);
+    else return along_frag(half + t * 16 * kStepBytes);
   };
   auto row_frag = [&](uint32_t stage, int m) {
     if constexpr (kRowsAcross) return across_frag(stage, BM, wm * MT + m);
@@ -348,22 +352,25 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   int kb = 0;
   bool more = true, sums = false;
   Frag t[MT], w[4];
-  // The loads of a step are issued two with each column tile's products: all
-  // at once they would hold the waves up until the memory pipeline has taken
-  // them, with the matrix cores idle.
-  constexpr int kPairs = (kLoads + 1) / 2, kEarly = 2 * 2;  // the first two pairs before the step's end
-  static_assert(kPairs <= NT, "the loads are out before the next barrier");
-  // The products of column tiles [N0, N1) of the step in `stage`.  The
-  // fragments of the tile two ahead are read meanwhile, those of the next step
-  // from its copy; and each row tile's of the next step once its last product
-  // has started.  The scheduling barriers keep this order.
-  auto multiply = [&](uint32_t stage, uint32_t next, int N0, int N1, int copy, bool loads) {
+  // A step has two barriers.  Before the first, ahead of column tile kOpen,
+  // every wave has read the step's rows and the first half of its columns: the
+  // loads of the step S ahead into those places start behind it (X), two with
+  // each column tile's products.  Before the second, ahead of tile NT - 2, the
+  // second half is read too, and its loads follow (Y).  Each load has S - 1/2
+  // steps until it is waited for: X of the next step at the second barrier, Y
+  // of this step at the first, with (S - 1) * kLoads newer loads on the way.
+  constexpr int kX = W::LT + W::LW / 2, kOpen = HT - 2;
+  static_assert(2 * (NT - 2 - kOpen) >= kX && W::LW / 2 <= 4, "the loads are out before the next barrier");
+  // The products of column tiles [N0, N1) of the step in `stage`, and loads
+  // [i0, i1) into it.  The fragments of the tile two ahead are read meanwhile,
+  // those of the next step from its copy; and each row tile's of the next step
+  // once its last product has started.  The scheduling barriers keep this order.
+  auto multiply = [&](uint32_t stage, uint32_t next, int N0, int N1, int copy, int i0, int i1) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       if (n < N0 || n >= N1) continue;
       __builtin_amdgcn_sched_barrier(0);
-      const int two = n >= NT - 2 ? n - (NT - 2) : n + 2;
-      if (two < kPairs && loads) load(copy, 2 * two, 2 * two + 2);
+      load(copy, i0 + 2 * (n - N0), i0 + 2 * (n - N0) + 2 < i1 ? i0 + 2 * (n - N0) + 2 : i1);
       w[(n + 2) & 3] = n + 2 < NT ? col_frag(stage, n + 2) : col_frag(next, n + 2 - NT);
 #pragma unroll
       for (int m = 0; m < MT; ++m) acc[n][m] = mfma_bf16(w[n & 3].lo, t[m].lo, acc[n][m]);
@@ -448,7 +455,7 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   step_barrier<0>();
   bool fresh = true;  // the current step is a tile's first
   bool live = false;  // waves past the tile's last row only load
-  for (int copy = 0, prev = W::S - 1;; prev = copy, copy = copy + 1 == W::S ? 0 : copy + 1) {
+  for (int copy = 0;; copy = copy + 1 == W::S ? 0 : copy + 1) {
     // step kb of the current tile
     const uint32_t stage = rows0 + copy * W::kStage;
     const uint32_t next = rows0 + (copy + 1 == W::S ? 0 : copy + 1) * W::kStage;
@@ -461,10 +468,11 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
       w[0] = col_frag(stage, 0);
       w[1] = col_frag(stage, 1);
     }
-    if (live) multiply(stage, next, 0, NT - 2, prev, !fresh);
-    else if (!fresh) load(prev, kEarly, kLoads);
-    if (!fresh) ++lk;                       // the loads that the step before began are all out
-    step_barrier<(W::S - 2) * kLoads>();    // the next step's tiles are here; those after may be on the way
+    if (live) multiply(stage, next, 0, kOpen, copy, 0, 0);
+    // A tile's first step finds its loads landed (below), and the results of
+    // the tile before still on their way out.
+    if (fresh) step_barrier<63>();
+    else step_barrier<(W::S - 1) * kLoads>();
     if (lk >= nxt.steps && lk >= W::S) {
       lk = 0;
       const int then = item_no(turn_no + slots);
@@ -476,14 +484,17 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
       aim();
     }
     begin_step();
+    if (live) multiply(stage, next, kOpen, NT - 2, copy, 0, kX);
+    else load(copy, 0, kX);
+    if (fresh) step_barrier<63>();
+    else step_barrier<(W::S - 1) * kLoads>();
+    if (live) multiply(stage, next, NT - 2, NT, copy, kX, kLoads);
+    else load(copy, kX, kLoads);
+    ++lk;
     ++kb;
-    const bool last = kb >= cur.steps && kb >= W::S;
-    if (live) multiply(stage, next, NT - 2, NT, copy, true);
-    else load(copy, 0, kEarly);
-    fresh = last;
-    if (last) {
-      load(copy, kEarly, kLoads);
-      ++lk;
+    fresh = kb >= cur.steps && kb >= W::S;
+    if (fresh) {
+      wait_vmcnt<0>();  // before the stores: the next tile's first step waits for none of them
       if (live) finish();
       if (!more) break;
 #pragma unroll
