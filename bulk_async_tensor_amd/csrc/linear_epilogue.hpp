@@ -15,17 +15,24 @@ typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
 __device__ __forceinline__ f32x4 load4_f32(const float* p, int64_t at) {
   return *reinterpret_cast<const f32x4_at4*>(p + at);
 }
+__device__ __forceinline__ f32x4 widen4(uint32_t lo, uint32_t hi) {
+  return f32x4{bf16_lo(lo), bf16_hi(lo), bf16_lo(hi), bf16_hi(hi)};
+}
+__device__ __forceinline__ u32x2 narrow4(f32x4 v) { return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}; }
 __device__ __forceinline__ f32x4 load4_bf16(const void* p, int64_t at) {
   const u32x2 v = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p) + at);
-  return f32x4{bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])};
+  return widen4(v[0], v[1]);
 }
 __device__ __forceinline__ void store4_bf16(void* p, int64_t at, f32x4 v) {
-  *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p) + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p) + at) = narrow4(v);
 }
 
+// exp(z) by the hardware's 2^x: the argument's rounding costs 1.5 |z| steps of
+// float32 at most, the instruction one.
+__device__ __forceinline__ float exp_of(float z) { return __builtin_amdgcn_exp2f(z * 1.44269504f); }
 // 1 / (1 + exp(-z)): exp overflows below -88.7, where the quotient is 0.  (The
 // hardware's reciprocal, one step off, for the 10 instructions of a division.)
-__device__ __forceinline__ float sigmoid_of(float z) { return __builtin_amdgcn_rcpf(1.0f + expf(-z)); }
+__device__ __forceinline__ float sigmoid_of(float z) { return __builtin_amdgcn_rcpf(1.0f + exp_of(-z)); }
 
 // (1 + erf(z / sqrt 2)) / 2, to a few steps of float32 relative to its value
 // far below zero too.  With x = |z| / sqrt 2 and t = 1 / (1 + x / 3),
@@ -64,13 +71,28 @@ __device__ __forceinline__ float activate_slope(float z) {
   return 1.0f;
 }
 
+template <int ACT>
+__device__ __forceinline__ f32x4 activate4(f32x4 z) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z[i] = activate<ACT>(z[i]);
+  return z;
+}
+template <int ACT>
+__device__ __forceinline__ f32x4 slope4(f32x4 z) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z[i] = activate_slope<ACT>(z[i]);
+  return z;
+}
+
+// ---- four neighbouring results of a row, from and to plain pointers (the join
+// of a cut sum)
+
 // Results n .. n + 3 of row r of expert e, not EP_ACT_SWIGLU.
 template <int ACT>
 __device__ __forceinline__ void finish_linear(const LinearArgs& g, int e, int64_t r, int n, f32x4 z) {
   if (g.bias) z += load4_f32(g.bias, (int64_t)e * g.N + n);
   if (g.pre_out) store4_bf16(g.pre_out, r * g.N + n, z);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) z[i] = activate<ACT>(z[i]);
+  z = activate4<ACT>(z);
   if (g.residual) z += load4_bf16(g.residual, r * g.N + n);
   if (g.out_f32) *reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + r * g.N + n) = z;
   else store4_bf16(g.out, r * g.N + n, z);
@@ -86,9 +108,7 @@ __device__ __forceinline__ void finish_swiglu(const LinearArgs& g, int e, int64_
     store4_bf16(g.pre_out, r * g.N + n, gate);
     store4_bf16(g.pre_out, r * g.N + outs + n, up);
   }
-  f32x4 z;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) z[i] = activate<EP_ACT_SILU>(gate[i]) * up[i];
+  f32x4 z = activate4<EP_ACT_SILU>(gate) * up;
   if (g.residual) z += load4_bf16(g.residual, r * outs + n);
   if (g.out_f32) *reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + r * outs + n) = z;
   else store4_bf16(g.out, r * outs + n, z);
@@ -99,25 +119,14 @@ __device__ __forceinline__ void finish_dgrad(const LinearArgs& g, int64_t r, int
   if constexpr (ACT == EP_ACT_SWIGLU) {
     const int64_t at = r * 2 * g.K + i;
     const f32x4 gate = load4_bf16(g.pre_in, at), up = load4_bf16(g.pre_in, at + g.K);
-    f32x4 dg, du;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      dg[j] = activate_slope<EP_ACT_SILU>(gate[j]) * up[j] * d[j];
-      du[j] = activate<EP_ACT_SILU>(gate[j]) * d[j];
-    }
-    store4_bf16(g.out, at, dg);
-    store4_bf16(g.out, at + g.K, du);
-    return;
+    store4_bf16(g.out, at, slope4<EP_ACT_SILU>(gate) * up * d);
+    store4_bf16(g.out, at + g.K, activate4<EP_ACT_SILU>(gate) * d);
+  } else {
+    const int64_t at = r * g.K + i;
+    if constexpr (ACT != EP_ACT_NONE) d *= slope4<ACT>(load4_bf16(g.pre_in, at));
+    store4_bf16(g.out, at, d);
   }
-  const int64_t at = r * g.K + i;
-  if constexpr (ACT != EP_ACT_NONE) {
-    const f32x4 z = load4_bf16(g.pre_in, at);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) d[j] *= activate_slope<ACT>(z[j]);
-  }
-  store4_bf16(g.out, at, d);
 }
-
 // Four neighbouring values of a weight's gradient.
 __device__ __forceinline__ void finish_wgrad(const LinearArgs& g, int64_t at, f32x4 v) {
   if (g.out_f32) *reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + at) = v;

@@ -28,8 +28,7 @@
 //
 // A sum's end inside a step: lanes whose places lie past it load from past the
 // buffer, which brings zeros.  The same holds for steps that only fill a tile
-// up to the number of copies (a shorter one would be two tiles ahead of its
-// results).
+// up to the number of copies and one.
 //
 // Few tiles: the sum is cut into `splits` runs of steps, each an item of its
 // own whose float32 results go to the workspace; join_kernel adds them in
@@ -67,40 +66,45 @@ struct Wide {
   static constexpr int MT = BM / 16 / WM;  // row tiles of a wave
   static constexpr int kT = BM * kStepBytes, kStage = kT + kCols * kStepBytes;  // rows, then columns
   static constexpr int S = linear_copies(BM);  // copies: steps whose tiles are in LDS or on the way
+  static constexpr int kLeast = S + 1;         // steps of a tile: the loads are S steps and one tile ahead at most
   static constexpr int LT = BM / 64;           // load instructions of a wave a step: rows,
   static constexpr int LW = kCols / 64;        // and columns
 };
 
-// A raw buffer of `bytes` at p: loads past its end bring zeros.
-__device__ __forceinline__ u32x4 buffer_of(const void* p, int64_t bytes) {
-  const uint64_t at = (uint64_t)(uintptr_t)p;
-  const uint32_t size = bytes < 0 ? 0u : bytes > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)bytes;
-  u32x4 r = {(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, size, 0x00020000u};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = (uint32_t)__builtin_amdgcn_readfirstlane((int)r[i]);
-  return r;
+// A raw buffer of `bytes` at p: loads past its end bring zeros, stores go nowhere.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes > 0x7FFFFFFF ? 0x7FFFFFFF : (int)bytes,
+                                           0x00020000);
 }
 
-// Buffer load straight to LDS: every lane's 16 bytes from its own offset land at
-// lds + 16 * lane.  Written as an instruction because the compiler, which
-// cannot tell the copies of an array apart, would wait for all of them before
-// any LDS read; the barriers below wait for the ones that are due.  It has no
-// result registers, and the next instruction may change the address registers.
-// The s_nop covers M0 and buffer registers that a vector instruction has just
-// written (5 wait states).
+// Buffer loads straight to LDS: every lane's 16 bytes from its own offset land
+// at lds + 16 * lane, those of the second load of a pair kNext bytes further.
+// Written as instructions because the compiler, which cannot tell the copies of
+// an array apart, would wait for all of them before any LDS read; the barriers
+// below wait for the ones that are due.  They have no result registers, and the
+// next instruction may change the address registers.  The s_nop covers M0 and
+// buffer registers that a vector instruction has just written (5 wait states).
 __device__ __forceinline__ void load16_to_lds(const u32x4& buf, uint32_t lds, uint32_t offset, uint32_t base) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(offset),
                "s"(buf), "s"(base)
                : "memory");
 }
+template <int kNext>
+__device__ __forceinline__ void load16_pair_to_lds(const u32x4& buf, uint32_t lds, uint32_t offset0, uint32_t offset1,
+                                                   uint32_t base) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %3, %4 offen lds\n\t"
+      "s_add_u32 m0, %0, %5\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds" ::"s"(lds),
+      "v"(offset0), "v"(offset1), "s"(buf), "s"(base), "i"(kNext)
+      : "memory", "scc");
+}
 
-// Every wave's loads but its newest N have landed, and its LDS accesses are
-// done.  vmcnt retires in issue order.
-template <int N>
+// Every wave's LDS accesses are done, and the loads that it has waited for are
+// there for all (wait_vmcnt<N>: all but its newest N; vmcnt retires in issue
+// order).
 __device__ __forceinline__ void step_barrier() {
-  constexpr int imm = (N & 0xF) | (0x7 << 4) | ((N >> 4) << 14);  // vmcnt(N), lgkmcnt(0)
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(imm);
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -109,8 +113,8 @@ __device__ __forceinline__ void step_barrier() {
 // steps [k0, k0 + steps) of run `split` of its sum.
 struct Item {
   int e, c0, split;
-  int64_t r0, r1;
-  int64_t lo, hi;  // wgrad: the expert's token rows
+  int r0, r1;
+  int lo, hi;  // wgrad: the expert's token rows
   int k0, steps;
 };
 
@@ -133,6 +137,11 @@ __device__ __forceinline__ float add_places(bf16x8 f, float v) {
   return v;
 }
 
+// Whether step k of an item is the sum's last, and not full.
+__device__ __forceinline__ bool late_step(const Item& t, int k, int deep) {
+  return k < t.steps && (t.k0 + k + 1) * kDeep > deep;
+}
+
 struct Frag {  // 64 places of 16 rows (columns): those of chunk `quad` and of chunk quad + 4
   bf16x8 lo, hi;
 };
@@ -151,7 +160,7 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   const int outs = P == kForward ? (pair ? g.N / 2 : g.N) : g.K;  // columns there are
   const int per_unit = pair ? kHalf : kCols;
   const int units = (outs + per_unit - 1) / per_unit;
-  const int64_t rld = P == kForward ? g.K : g.N, cld = g.K;  // values of a row in memory
+  const int rld = P == kForward ? g.K : g.N, cld = g.K;  // values of a row in memory
 
   // ---- the items of this workgroup
   const int un = (g.N + BM - 1) / BM;  // wgrad: tiles along the weight rows
@@ -182,37 +191,69 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   if (id >= total) return;
 
   // ---- the loads of the stream
-  u32x4 rb, cb;
+  u32x4 rb = {}, cb = {};
   Item nxt;
   int lk = 0;  // the step of nxt that loads next
   // A lane's place in a load: of 8 rows along the sum, or of 1 KiB of rows across it.
   const int chunk = (lane & 7) ^ (lane >> 3);
   constexpr int kRowUnits = BM / 8, kColUnits = kHalf / 8;  // 16-byte units in an LDS row across the sum
-  auto across = [&](int units16, int64_t ld, int i) -> uint32_t {  // offset of load i of a side across the sum
+  auto across = [&](int units16, int ld, int i) -> uint32_t {  // offset of load i of a side across the sum
     const int ri = kWave / units16;  // rows of a load
     const int r = wave * 8 + i * ri + lane / units16, u = lane % units16;
     const int f = ((r & 3) | (wave & 3) << 2) & (units16 / 2 - 1);
     return (uint32_t)(r * ld * 2) + (((u >> 1) ^ f) * 2 + (u & 1)) * 16;
   };
-  uint32_t r_at[kRowsAcross ? W::LT : 1], c_at[kColsAcross ? W::LW : 1];
-  if constexpr (kRowsAcross) {
+  uint32_t r_at[W::LT], c_at[W::LW];
 #pragma unroll
-    for (int i = 0; i < W::LT; ++i) r_at[i] = across(kRowUnits, rld, i);
-  } else {
-    r_at[0] = (uint32_t)((lane >> 3) * rld * 2) + chunk * 16;
-  }
-  if constexpr (kColsAcross) {
+  for (int i = 0; i < W::LT; ++i)
+    r_at[i] = kRowsAcross ? across(kRowUnits, rld, i)
+                          : (uint32_t)((wave * (BM / kWaves) + i * 8 + (lane >> 3)) * rld * 2) + chunk * 16;
+  // from the first half of the columns to the second
+  const uint32_t half = kColsAcross ? kHalf * 2 : (uint32_t)((pair ? outs : kHalf) * cld * 2);
 #pragma unroll
-    for (int j = 0; j < W::LW; ++j) c_at[j] = across(kColUnits, cld, j % (W::LW / 2)) + j / (W::LW / 2) * kHalf * 2;
-  } else {
-    c_at[0] = (uint32_t)((lane >> 3) * cld * 2) + chunk * 16;
-  }
-  const int64_t deep = P == kForward ? g.K : g.N;  // (not wgrad)
+  for (int j = 0; j < W::LW; ++j)
+    c_at[j] = (kColsAcross ? across(kColUnits, cld, j % 2)
+                           : (uint32_t)((wave * (kHalf / kWaves) + j % 2 * 8 + (lane >> 3)) * cld * 2) + chunk * 16) +
+              j / 2 * half;
+  const int deep = P == kForward ? g.K : g.N;  // (not wgrad)
   // lanes past the end of the sum's last step
-  const uint32_t late = chunk * 8 >= (int)(deep % kDeep) ? kNowhere : 0u;
-  int half1 = 0;  // forward: weight row of the second half's first
-  const uint8_t *rbase, *cbase;
-  int64_t rleft, cleft;
+  const uint32_t late = chunk * 8 >= deep % kDeep ? kNowhere : 0u;
+  bool cut = false;          // the offsets are those of that step
+  uint32_t base = 0;         // sides along the sum: of step lk
+  uint32_t r_size = 0, c_size = 0;
+  uint64_t r_from = 0, c_from = 0;  // sides across the sum: the step's first row,
+  int left = 0;                     // and the places that are left
+  auto set_buffer = [&](u32x4& b, uint64_t from, uint32_t size) {
+    b[0] = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)from);
+    b[1] = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(from >> 32));
+    b[2] = (uint32_t)__builtin_amdgcn_readfirstlane((int)size);
+    b[3] = 0x00020000u;
+  };
+  // The buffers of step lk, once the item or the step has changed.
+  auto set_step = [&]() {
+    if constexpr (!kRowsAcross) {
+      // a step past the item's end: buffers of no size (and a base of zero, which the range check takes from the size)
+      const bool in = lk < nxt.steps;
+      base = (uint32_t)__builtin_amdgcn_readfirstlane(in ? (nxt.k0 + lk) * kStepBytes : 0);
+      rb[2] = (uint32_t)__builtin_amdgcn_readfirstlane(in ? (int)r_size : 0);
+      if constexpr (!kColsAcross) cb[2] = (uint32_t)__builtin_amdgcn_readfirstlane(in ? (int)c_size : 0);
+      if (late_step(nxt, lk, deep)) {
+        cut = true;
+#pragma unroll
+        for (int i = 0; i < W::LT; ++i) r_at[i] |= late;
+        if constexpr (!kColsAcross)
+#pragma unroll
+          for (int j = 0; j < W::LW; ++j) c_at[j] |= late;
+      }
+    }
+    if constexpr (kColsAcross) {
+      // the rows (places) of this step that there are; past its row's end a
+      // last row has other values, whose results are not stored, or the end
+      const int rows = max(min(left, kDeep), 0);
+      set_buffer(cb, c_from, (uint32_t)max(rows * cld * 2 - nxt.c0 * 2, 0));
+      if constexpr (kRowsAcross) set_buffer(rb, r_from, (uint32_t)max(rows * rld * 2 - nxt.r0 * 2, 0));
+    }
+  };
   auto aim = [&]() {
     nxt.split = shape.splits > 1 ? (int)((uint32_t)id / (uint32_t)products) : 0;
     const uint32_t p = id - nxt.split * products;
@@ -222,111 +263,122 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
       nxt.c0 = (int)(p - tile * units) * kCols;
       nxt.e = (int)(tile / (uint32_t)un);
       nxt.r0 = (int)(tile - nxt.e * un) * BM;
-      nxt.r1 = nxt.r0 + BM < g.N ? nxt.r0 + BM : g.N;
+      nxt.r1 = min(nxt.r0 + BM, g.N);
       const Segment s = linear_segment(g, nxt.e);
       nxt.lo = s.lo, nxt.hi = s.hi;
-      all = (int)((nxt.hi - nxt.lo + kDeep - 1) / kDeep);
+      all = (nxt.hi - nxt.lo + kDeep - 1) / kDeep;
     } else {
       // two rounds of 64 and 16 comparisons find the expert
       const int q = (int)(p / (uint32_t)units);
-      const int base = 16 * __builtin_popcountll(ballot(s_first[min((lane + 1) * 16, g.E)] <= q));
-      const int e = base + __builtin_popcountll(ballot(lane < 16 && s_first[min(base + lane + 1, g.E)] <= q));
+      const int base16 = 16 * __builtin_popcountll(ballot(s_first[min((lane + 1) * 16, g.E)] <= q));
+      const int e = base16 + __builtin_popcountll(ballot(lane < 16 && s_first[min(base16 + lane + 1, g.E)] <= q));
       const int before = __builtin_amdgcn_readfirstlane(s_first[e]);
       const int mine = __builtin_amdgcn_readfirstlane(s_first[e + 1]) - before;
       const uint32_t local = p - (uint32_t)before * units, unit = local / (uint32_t)mine;
       const Segment s = linear_segment(g, e);
       nxt.e = e;
       nxt.c0 = (int)unit * per_unit;
-      nxt.r0 = s.lo + (int64_t)(local - unit * mine) * BM;
-      nxt.r1 = nxt.r0 + BM < s.hi ? nxt.r0 + BM : s.hi;
-      all = (int)((deep + kDeep - 1) / kDeep);
+      nxt.r0 = s.lo + (int)(local - unit * mine) * BM;
+      nxt.r1 = min(nxt.r0 + BM, s.hi);
+      all = (deep + kDeep - 1) / kDeep;
     }
     nxt.k0 = 0, nxt.steps = all;
     if (shape.splits > 1) {
       nxt.k0 = (int)((uint32_t)all * (uint32_t)nxt.split / (uint32_t)shape.splits);
       nxt.steps = (int)((uint32_t)all * (uint32_t)(nxt.split + 1) / (uint32_t)shape.splits) - nxt.k0;
     }
+    if (cut) {
+      cut = false;
+#pragma unroll
+      for (int i = 0; i < W::LT; ++i) r_at[i] &= kNowhere - 1;
+      if constexpr (!kColsAcross)
+#pragma unroll
+        for (int j = 0; j < W::LW; ++j) c_at[j] &= kNowhere - 1;
+    }
+    const uint64_t rows_in = (uint64_t)(uintptr_t)g.rows_in, cols_in = (uint64_t)(uintptr_t)g.cols_in;
+    const int64_t weight = (int64_t)nxt.e * g.N * g.K;
     if constexpr (P == kWgrad) {
-      // every step its own buffers: the token rows that are left
-      rbase = static_cast<const uint8_t*>(g.rows_in) + ((nxt.lo + (int64_t)nxt.k0 * kDeep) * rld + nxt.r0) * 2;
-      cbase = static_cast<const uint8_t*>(g.cols_in) + ((nxt.lo + (int64_t)nxt.k0 * kDeep) * cld + nxt.c0) * 2;
-      const int64_t rows_left = min(nxt.hi, nxt.lo + (int64_t)(nxt.k0 + nxt.steps) * kDeep) - nxt.lo - (int64_t)nxt.k0 * kDeep;
-      rleft = (rows_left * rld - nxt.r0) * 2;
-      cleft = (rows_left * cld - nxt.c0) * 2;
+      const int row = nxt.lo + nxt.k0 * kDeep;
+      left = min(nxt.hi - row, nxt.steps * kDeep);
+      r_from = rows_in + ((int64_t)row * rld + nxt.r0) * 2;
+      c_from = cols_in + ((int64_t)row * cld + nxt.c0) * 2;
     } else {
       // rows past the segment's end are past the buffer: they bring zeros, and their results are never stored
-      rb = buffer_of(static_cast<const uint8_t*>(g.rows_in) + nxt.r0 * rld * 2, (nxt.r1 - nxt.r0) * rld * 2);
-      cbase = static_cast<const uint8_t*>(g.cols_in) + (int64_t)nxt.e * g.N * g.K * 2;
+      r_size = (uint32_t)((nxt.r1 - nxt.r0) * rld * 2);
+      set_buffer(rb, rows_in + (int64_t)nxt.r0 * rld * 2, r_size);
       if constexpr (P == kForward) {
-        cb = buffer_of(cbase, (int64_t)g.N * g.K * 2);
-        half1 = pair ? outs + nxt.c0 : nxt.c0 + kHalf;
+        c_size = (uint32_t)((g.N - nxt.c0) * cld * 2);
+        set_buffer(cb, cols_in + (weight + (int64_t)nxt.c0 * cld) * 2, c_size);
       } else {
-        cleft = ((int64_t)g.N * g.K - (int64_t)nxt.k0 * kDeep * cld - nxt.c0) * 2;
-        cbase += ((int64_t)nxt.k0 * kDeep * cld + nxt.c0) * 2;
+        left = min(deep - nxt.k0 * kDeep, nxt.steps * kDeep);
+        c_from = cols_in + (weight + (int64_t)nxt.k0 * kDeep * cld + nxt.c0) * 2;
       }
     }
   };
-  uint32_t mask = 0, base_k = 0;
-  // What the loads of step lk share.  Sides across the sum: the buffer moves along.
-  auto begin_step = [&]() {
-    const int k = nxt.k0 + lk;
-    if constexpr (!kRowsAcross) {
-      mask = lk >= nxt.steps ? kNowhere : (int64_t)(k + 1) * kDeep > deep ? late : 0u;
-      base_k = (uint32_t)__builtin_amdgcn_readfirstlane(k * kStepBytes);
-    } else {
-      rb = buffer_of(rbase, rleft);
-      rbase += kDeep * rld * 2;
-      rleft -= kDeep * rld * 2;
-    }
+  bool more = true;
+  auto advance = [&]() {  // to the next step, or the next item's first
+    ++lk;
     if constexpr (kColsAcross) {
-      cb = buffer_of(cbase, lk >= nxt.steps ? 0 : cleft);
-      cbase += kDeep * cld * 2;
-      cleft -= kDeep * cld * 2;
+      c_from += (int64_t)kDeep * cld * 2;
+      if constexpr (kRowsAcross) r_from += (int64_t)kDeep * rld * 2;
+      left -= kDeep;
     }
-  };
-  const uint32_t rows0 = lds_addr_of(s_rows);
-  constexpr int kLoads = W::LT + W::LW;
-  auto load = [&](int copy, int i0, int i1) {  // loads [i0, i1) of step lk
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      if (i < i0 || i >= i1) continue;
-      const uint32_t stage = rows0 + copy * W::kStage;
-      if (i < W::LT) {
-        const uint32_t lds = stage + wave * (W::kT / kWaves) + i * 1024;
-        if constexpr (kRowsAcross) load16_to_lds(rb, lds, r_at[i], 0);
-        else load16_to_lds(rb, lds, (r_at[0] + (uint32_t)((wave * (BM / kWaves) + i * 8) * rld * 2)) | mask, base_k);
-      } else {
-        const int j = i - W::LT, h = j / (W::LW / 2);
-        if constexpr (kColsAcross) {
-          load16_to_lds(cb, stage + W::kT + h * kHalf * kStepBytes + wave * (kHalf * kStepBytes / kWaves) +
-                                j % (W::LW / 2) * 1024,
-                        c_at[j], 0);
-        } else {
-          const int r = wave * (kHalf / kWaves) + j % (W::LW / 2) * 8;
-          const int row = (h ? half1 : nxt.c0) + r;
-          load16_to_lds(cb, stage + W::kT + (h * kHalf + r) * kStepBytes, (c_at[0] + (uint32_t)(row * cld * 2)) | mask,
-                        base_k);
-        }
+    if (lk >= nxt.steps && lk >= W::kLeast) {
+      lk = 0;
+      const int then = item_no(turn_no + slots);
+      more = then < total;
+      if (more) {  // (else the stream loads its last tile again)
+        turn_no += slots;
+        id = then;
       }
+      aim();
     }
+    set_step();
+  };
+  constexpr int kLoads = W::LT + W::LW;
+  constexpr int kRowBytes = W::kT / kWaves, kColBytes = kHalf * kStepBytes / kWaves;  // of a wave's loads
+  auto load_rows = [&](uint32_t stage, int i) {  // loads i and i + 1 of the rows
+    load16_pair_to_lds<1024>(rb, stage + wave * kRowBytes + i * 1024, r_at[i], r_at[i + 1], kRowsAcross ? 0 : base);
+  };
+  auto load_cols = [&](uint32_t stage, int h) {  // the loads of half h of the columns
+    load16_pair_to_lds<1024>(cb, stage + W::kT + h * kHalf * kStepBytes + wave * kColBytes, c_at[2 * h], c_at[2 * h + 1],
+                             kColsAcross ? 0 : base);
+  };
+  auto load_step = [&](uint32_t stage) {
+#pragma unroll
+    for (int i = 0; i < W::LT; i += 2) load_rows(stage, i);
+    load_cols(stage, 0);
+    load_cols(stage, 1);
   };
 
   // ---- the products
   f32x4 acc[NT][MT] = {};
   float bacc[P == kWgrad ? MT : 1] = {};  // wgrad: the sums of dy alone, this lane's places
-  const uint32_t off0 = col * kStepBytes + ((quad ^ (col & 7)) * 16);
-  const uint32_t off1 = col * kStepBytes + (((quad + 4) ^ (col & 7)) * 16);
-  auto along_frag = [&](uint32_t rows) {
-    typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
-    Frag f;
-    f.lo = *(lds_bf16x8*)(uintptr_t)(rows + off0);
-    f.hi = *(lds_bf16x8*)(uintptr_t)(rows + off1);
-    return f;
-  };
-  // tile `t` of 16 columns of a side across the sum, `width` columns wide
-  auto across_frag = [&](uint32_t side, int width, int t) {
+  // Addresses of a lane in a step's copy.  Along the sum: chunk quad, and chunk
+  // quad + 4, of row col of a wave's first tile.  Across: for each of a wave's
+  // tiles (their chunks differ in the bits that are exchanged).
+  typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
+  auto along_at = [&](int h) { return col * kStepBytes + (((quad + 4 * h) ^ (col & 7)) * 16); };
+  auto across_at = [&](int width, int t) {
     const int f = ((col >> 2) | quad << 2) & (width / 16 - 1);
-    const uint32_t at = side + (quad * 8 + (col >> 2)) * width * 2 + ((t ^ f) * 32) + (col & 3) * 8;
+    return (quad * 8 + (col >> 2)) * width * 2 + ((t ^ f) * 32) + (col & 3) * 8;
+  };
+  uint32_t r_lds[kRowsAcross ? MT : 2], c_lds[kColsAcross ? HT : 2];
+  if constexpr (kRowsAcross) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) r_lds[m] = across_at(BM, wm * MT + m);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) r_lds[h] = along_at(h) + wm * MT * 16 * kStepBytes;
+  }
+  if constexpr (kColsAcross) {
+#pragma unroll
+    for (int n = 0; n < HT; ++n) c_lds[n] = W::kT + across_at(kHalf, wn * HT + n);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) c_lds[h] = W::kT + along_at(h) + wn * HT * 16 * kStepBytes;
+  }
+  auto across_frag = [&](uint32_t at, int width) {
     s16x4 v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -337,176 +389,310 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
     r.hi = __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[2], v[3], 0, 1, 2, 3, 4, 5, 6, 7));
     return r;
   };
+  auto along_frag = [&](uint32_t lo, uint32_t hi) {
+    Frag f;
+    f.lo = *(lds_bf16x8*)(uintptr_t)lo;
+    f.hi = *(lds_bf16x8*)(uintptr_t)hi;
+    return f;
+  };
   auto col_frag = [&](uint32_t stage, int n) {
-    const uint32_t half = stage + W::kT + n / HT * kHalf * kStepBytes;
-    const int t = wn * HT + n % HT;
-    if constexpr (kColsAcross) return across_frag(half, kHalf, t);
-    else return along_frag(half + t * 16 * kStepBytes);
+    const uint32_t h = n / HT * kHalf * kStepBytes;
+    if constexpr (kColsAcross) return across_frag(stage + c_lds[n % HT] + h, kHalf);
+    else return along_frag(stage + c_lds[0] + (h + n % HT * 16 * kStepBytes), stage + c_lds[1] + (h + n % HT * 16 * kStepBytes));
   };
   auto row_frag = [&](uint32_t stage, int m) {
-    if constexpr (kRowsAcross) return across_frag(stage, BM, wm * MT + m);
-    else return along_frag(stage + (wm * MT + m) * 16 * kStepBytes);
+    if constexpr (kRowsAcross) return across_frag(stage + r_lds[m], BM);
+    else return along_frag(stage + r_lds[0] + m * 16 * kStepBytes, stage + r_lds[1] + m * 16 * kStepBytes);
   };
 
   Item cur;
   int kb = 0;
-  bool more = true, sums = false;
+  bool sums = false;
   Frag t[MT], w[4];
   // A step has two barriers.  Before the first, ahead of column tile kOpen,
   // every wave has read the step's rows and the first half of its columns: the
-  // loads of the step S ahead into those places start behind it (X), two with
-  // each column tile's products.  Before the second, ahead of tile NT - 2, the
-  // second half is read too, and its loads follow (Y).  Each load has S - 1/2
-  // steps until it is waited for: X of the next step at the second barrier, Y
-  // of this step at the first, with (S - 1) * kLoads newer loads on the way.
-  constexpr int kX = W::LT + W::LW / 2, kOpen = HT - 2;
-  static_assert(2 * (NT - 2 - kOpen) >= kX && W::LW / 2 <= 4, "the loads are out before the next barrier");
-  // The products of column tiles [N0, N1) of the step in `stage`, and loads
-  // [i0, i1) into it.  The fragments of the tile two ahead are read meanwhile,
-  // those of the next step from its copy; and each row tile's of the next step
-  // once its last product has started.  The scheduling barriers keep this order.
-  auto multiply = [&](uint32_t stage, uint32_t next, int N0, int N1, int copy, int i0, int i1) {
+  // loads of the step S ahead into those places start behind it (X).  Before
+  // the second, ahead of tile NT - 2, the second half is read too, and its
+  // loads follow (Y).  Each load has S - 1/2 steps until it is waited for: X of
+  // the next step at the second barrier, Y of this step at the first, with
+  // (S - 1) * kLoads newer loads on the way.
+  constexpr int kOpen = HT - 2;
+  // The products of column tiles n and n + 1.  The fragments of the two tiles
+  // after them are read meanwhile, those of the next step from its copy.  The
+  // row tiles go one after another through both column tiles, so that in a
+  // step's last pair each can be read anew for the next step as soon as its
+  // four products have started.  What else the step has to do (`more_work`, the
+  // loads) stands between the products, or the matrix cores would wait for it.
+  auto multiply = [&](uint32_t stage, uint32_t next, int n, auto more_work) {
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (n < N0 || n >= N1) continue;
-      __builtin_amdgcn_sched_barrier(0);
-      load(copy, i0 + 2 * (n - N0), i0 + 2 * (n - N0) + 2 < i1 ? i0 + 2 * (n - N0) + 2 : i1);
-      w[(n + 2) & 3] = n + 2 < NT ? col_frag(stage, n + 2) : col_frag(next, n + 2 - NT);
+    for (int i = 0; i < 2; ++i)
+      w[(n + 2 + i) & 3] = n + 2 < NT ? col_frag(stage, n + 2 + i) : col_frag(next, n + 2 + i - NT);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) acc[n][m] = mfma_bf16(w[n & 3].lo, t[m].lo, acc[n][m]);
+    for (int m = 0; m < MT; ++m) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        acc[n][m] = mfma_bf16(w[n & 3].hi, t[m].hi, acc[n][m]);
-        if (n == NT - 1) {
-          if constexpr (P == kWgrad)
-            if (sums) {
-              bacc[m] = add_places(t[m].lo, bacc[m]);
-              bacc[m] = add_places(t[m].hi, bacc[m]);
-            }
-          t[m] = row_frag(next, m);
-        }
+      for (int i = 0; i < 2; ++i) acc[n + i][m] = mfma_bf16(w[(n + i) & 3].lo, t[m].lo, acc[n + i][m]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) acc[n + i][m] = mfma_bf16(w[(n + i) & 3].hi, t[m].hi, acc[n + i][m]);
+      more_work(m);
+      if (n == NT - 2) {
+        if constexpr (P == kWgrad)
+          if (sums) {
+            bacc[m] = add_places(t[m].lo, bacc[m]);
+            bacc[m] = add_places(t[m].hi, bacc[m]);
+          }
+        t[m] = row_frag(next, m);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
   };
+  auto nothing = [](int) {};
+  constexpr int kXLoads = W::LT / 2 + 1;  // pairs of loads of X: rows, first half of the columns
+  auto load_x = [&](uint32_t stage, int i) {
+    if (i < W::LT / 2) load_rows(stage, 2 * i);
+    else if (i < kXLoads) load_cols(stage, 0);
+  };
+  // One step of the current tile in copy `stage`, the next one in `next`.  A
+  // tile's first step finds its loads landed, and the results of the tile
+  // before still on their way out: it waits for neither.
+  auto step = [&](uint32_t stage, uint32_t next, bool first, bool live) {
+    if (live && kOpen > 0) multiply(stage, next, 0, nothing);
+    if (!first) wait_vmcnt<(W::S - 1) * kLoads>();
+    step_barrier();
+    if (live) {
+      constexpr int kPairs = (NT - 2 - kOpen) / 2, kEach = (kXLoads + kPairs - 1) / kPairs;
+#pragma unroll
+      for (int q = 0; q < kPairs; ++q)
+        multiply(stage, next, kOpen + 2 * q, [&](int m) {
+          if (m < kEach) load_x(stage, q * kEach + m);
+        });
+    } else {
+#pragma unroll
+      for (int i = 0; i < kXLoads; ++i) load_x(stage, i);
+    }
+    if (!first) wait_vmcnt<(W::S - 1) * kLoads>();
+    step_barrier();
+    if (live) {
+      multiply(stage, next, NT - 2, [&](int m) {
+        if (m == 0) load_cols(stage, 1);
+        if (m == 1) advance();
+      });
+    } else {
+      load_cols(stage, 1);
+      advance();
+    }
+  };
 
-  // Lane (col, quad) holds columns 4 quad .. + 3 of each column tile of row col
-  // of each row tile.
+  // A tile's results.  Lane (col, quad) holds columns 4 quad .. + 3 of each
+  // column tile of row col of each row tile; of two neighbouring tiles in bf16
+  // the lanes exchange halves, so that each moves 8 adjacent values.  Rows past
+  // the tile's end are past the buffers, columns past the row's get an offset
+  // that is.
+  // The call's pointers are read from the arguments anew: held through the
+  // steps they would take more scalar registers than there are.
+  typedef const __attribute__((address_space(4))) LinearArgs* ConstArgs;
   auto finish = [&]() {
-    const int held = (int)(cur.r1 - cur.r0);
-    if constexpr (P == kWgrad)
-      if (sums)
+    ConstArgs f = (ConstArgs)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(f));
+    const int64_t held = cur.r1 - cur.r0;
+    const int lr = wm * MT * 16 + col;
+    auto rows_of = [&](const void* p, int64_t row, int ld, int size) {
+      return buffer_at(static_cast<const uint8_t*>(p) + row * ld * size, held * ld * size);
+    };
+    // column of the first of a lane's 4 (8) results of column tile n (and n + 1)
+    auto column4 = [&](int n) { return (wn * HT + n % HT) * 16 + 4 * quad; };
+    auto column8 = [&](int n) { return (wn * HT + n % HT) * 16 + 16 * (quad & 1) + 8 * (quad >> 1); };
+    auto offset = [&](int m, int ld, int c, int end, int size) {
+      return (uint32_t)(((lr + m * 16) * ld + c) * size) | (c < end ? 0u : kNowhere);
+    };
+    auto put8 = [&](__amdgpu_buffer_rsrc_t to, uint32_t at, f32x4 a, f32x4 b) {
+      const u32x2 x = narrow4(a), y = narrow4(b);
+      const u32x2 d0 = swap_rows16(x[0], y[0]), d1 = swap_rows16(x[1], y[1]);
+      __builtin_amdgcn_raw_buffer_store_b128(u32x4{d0[0], d1[0], d0[1], d1[1]}, to, at, 0, 0);
+    };
+    auto get8 = [&](u32x4 v, f32x4& a, f32x4& b) {
+      const u32x2 d0 = swap_rows16(v[0], v[2]), d1 = swap_rows16(v[1], v[3]);
+      a = widen4(d0[0], d1[0]);
+      b = widen4(d0[1], d1[1]);
+    };
+    auto put4 = [&](__amdgpu_buffer_rsrc_t to, uint32_t at, f32x4 v) {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), to, at, 0, 0);
+    };
+    if constexpr (P == kWgrad) {
+      if (sums) {
+        float* to = shape.splits > 1 ? f->partial + (int64_t)shape.splits * f->E * f->N * f->K +
+                                           (int64_t)cur.split * f->E * f->N
+                                     : f->dbias;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           bacc[m] += __shfl_xor(bacc[m], 16, kWave);
           bacc[m] += __shfl_xor(bacc[m], 32, kWave);
+          if (wn == 0 && quad == 0 && lr + m * 16 < held) to[(int64_t)cur.e * f->N + cur.r0 + lr + m * 16] = bacc[m];
         }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int lr = (wm * MT + m) * 16 + col;
-      if (lr >= held) continue;
-      const int64_t r = cur.r0 + lr;
-      if (P == kWgrad && sums && wn == 0) {
-        float* to = shape.splits > 1 ? g.partial + (int64_t)shape.splits * g.E * g.N * g.K +
-                                           (int64_t)cur.split * g.E * g.N
-                                     : g.dbias;
-        if (quad == 0) to[(int64_t)cur.e * g.N + r] = bacc[m];
       }
-      if (shape.splits > 1) {
-        // [split][row][weight row or column]
-        const int64_t wide = P == kForward ? g.N : g.K;
-        const int64_t row = P == kWgrad ? (int64_t)cur.e * g.N + r : r;
-        const int64_t many = P == kWgrad ? (int64_t)g.E * g.N : g.rows;
-        float* to = g.partial + (cur.split * many + row) * wide;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int i = (n < HT ? 0 : kHalf) + (wn * HT + n % HT) * 16 + 4 * quad;
-          const int c = pair ? (n < HT ? cur.c0 + i : outs + cur.c0 + i - kHalf) : cur.c0 + i;
-          const bool in = pair ? cur.c0 + (wn * HT + n % HT) * 16 + 4 * quad < outs : c < outs;
-          if (in) *reinterpret_cast<f32x4*>(to + c) = acc[n][m];
-        }
-        continue;
-      }
-      if (pair) {
-#pragma unroll
-        for (int n = 0; n < HT; ++n) {
-          const int c = cur.c0 + (wn * HT + n) * 16 + 4 * quad;
-          if (c < outs) finish_swiglu(g, cur.e, r, c, acc[n][m], acc[HT + n][m]);
-        }
-        continue;
-      }
+    }
+    if (shape.splits > 1) {
+      // float32 [split][row][weight row or column]
+      const int wide = P == kForward ? f->N : f->K;
+      const int64_t row = P == kWgrad ? (int64_t)cur.e * f->N + cur.r0 : cur.r0;
+      const int64_t many = P == kWgrad ? (int64_t)f->E * f->N : f->rows;
+      const auto to = rows_of(f->partial, cur.split * many + row, wide, 4);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int c = cur.c0 + (n < HT ? 0 : kHalf) + (wn * HT + n % HT) * 16 + 4 * quad;
-        if (c >= outs) continue;
-        if constexpr (P == kForward) finish_linear<ACT>(g, cur.e, r, c, acc[n][m]);
-        if constexpr (P == kDgrad) finish_dgrad<ACT>(g, r, c, acc[n][m]);
-        if constexpr (P == kWgrad) finish_wgrad(g, ((int64_t)cur.e * g.N + r) * g.K + c, acc[n][m]);
+        int c = cur.c0 + column4(n), end = outs;
+        if (n >= HT) c += pair ? outs : kHalf, end = pair ? wide : outs;
+        if (pair && cur.c0 + column4(n) >= outs) end = 0;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) put4(to, offset(m, wide, c, end, 4), acc[n][m]);
+      }
+      return;
+    }
+    if constexpr (P == kForward) {
+      const auto to = rows_of(f->out, cur.r0, outs, f->out_f32 ? 4 : 2);
+      const auto res = rows_of(f->residual, cur.r0, outs, 2);
+      const auto pre = rows_of(f->pre_out, cur.r0, f->N, 2);
+      const auto bias = buffer_at(f->bias + (int64_t)cur.e * f->N, f->bias ? (int64_t)f->N * 4 : 0);
+      auto bias4 = [&](int c) {
+        return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(bias, c * 4, 0, 0));
+      };
+      constexpr int kLast = pair ? HT : NT;
+      const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int n = 0; n < kLast; n += 2) {
+        const int c = cur.c0 + (n < HT ? 0 : kHalf), c4 = c + column4(n), c8 = c + column8(n);
+        f32x4 add[2] = {none, none}, add_up[2] = {none, none};
+        if (f->bias) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            add[i] = bias4(c4 + i * 16);
+            if constexpr (pair) add_up[i] = bias4(c4 + i * 16 + outs);
+          }
+        }
+        u32x4 v[MT];
+        if (f->residual) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m) v[m] = __builtin_amdgcn_raw_buffer_load_b128(res, offset(m, outs, c8, outs, 2), 0, 0);
+        } else {
+#pragma unroll
+          for (int m = 0; m < MT; ++m) v[m] = u32x4{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          f32x4 z[2], up[2], r[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            z[i] = acc[n + i][m] + add[i];
+            if constexpr (pair) up[i] = acc[HT + n + i][m] + add_up[i];
+          }
+          if (f->pre_out) {
+            const uint32_t at = offset(m, f->N, c8, outs, 2);
+            put8(pre, at, z[0], z[1]);
+            if constexpr (pair) put8(pre, at + outs * 2, up[0], up[1]);
+          }
+          get8(v[m], r[0], r[1]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            z[i] = activate4<ACT>(z[i]);
+            if constexpr (pair) z[i] *= up[i];
+            z[i] += r[i];
+          }
+          if (f->out_f32) {
+            put4(to, offset(m, outs, c4, outs, 4), z[0]);
+            put4(to, offset(m, outs, c4 + 16, outs, 4), z[1]);
+          } else {
+            put8(to, offset(m, outs, c8, outs, 2), z[0], z[1]);
+          }
+        }
+      }
+    }
+    if constexpr (P == kDgrad) {
+      const int wide = ACT == EP_ACT_SWIGLU ? 2 * outs : outs;
+      const auto to = rows_of(f->out, cur.r0, wide, 2);
+      const auto pre = rows_of(f->pre_in, cur.r0, wide, 2);
+#pragma unroll
+      for (int n = 0; n < NT; n += 2) {
+        const int c8 = cur.c0 + (n < HT ? 0 : kHalf) + column8(n);
+        u32x4 v[MT], u[MT];
+        if constexpr (ACT != EP_ACT_NONE) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const uint32_t at = offset(m, wide, c8, outs, 2);
+            v[m] = __builtin_amdgcn_raw_buffer_load_b128(pre, at, 0, 0);
+            if constexpr (ACT == EP_ACT_SWIGLU) u[m] = __builtin_amdgcn_raw_buffer_load_b128(pre, at + outs * 2, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const uint32_t at = offset(m, wide, c8, outs, 2);
+          f32x4 z[2], up[2];
+          if constexpr (ACT != EP_ACT_NONE) get8(v[m], z[0], z[1]);
+          if constexpr (ACT == EP_ACT_SWIGLU) {
+            get8(u[m], up[0], up[1]);
+            put8(to, at, slope4<ACT>(z[0]) * up[0] * acc[n][m], slope4<ACT>(z[1]) * up[1] * acc[n + 1][m]);
+            put8(to, at + outs * 2, activate4<ACT>(z[0]) * acc[n][m], activate4<ACT>(z[1]) * acc[n + 1][m]);
+          } else if constexpr (ACT != EP_ACT_NONE) {
+            put8(to, at, slope4<ACT>(z[0]) * acc[n][m], slope4<ACT>(z[1]) * acc[n + 1][m]);
+          } else {
+            put8(to, at, acc[n][m], acc[n + 1][m]);
+          }
+        }
+      }
+    }
+    if constexpr (P == kWgrad) {
+      const auto to = rows_of(f->out, (int64_t)cur.e * f->N + cur.r0, outs, f->out_f32 ? 4 : 2);
+#pragma unroll
+      for (int n = 0; n < NT; n += 2) {
+        const int c = cur.c0 + (n < HT ? 0 : kHalf), c4 = c + column4(n), c8 = c + column8(n);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if (f->out_f32) {
+            put4(to, offset(m, outs, c4, outs, 4), acc[n][m]);
+            put4(to, offset(m, outs, c4 + 16, outs, 4), acc[n + 1][m]);
+          } else {
+            put8(to, offset(m, outs, c8, outs, 2), acc[n][m], acc[n + 1][m]);
+          }
+        }
       }
     }
   };
 
+  const uint32_t rows0 = lds_addr_of(s_rows), rows_end = rows0 + W::S * W::kStage;
   aim();
+  set_step();
   cur = nxt;
-  for (; lk < W::S; ++lk) {
-    begin_step();
-    load(lk, 0, kLoads);
+  for (int i = 0; i < W::S; ++i) {
+    load_step(rows0 + i * W::kStage);
+    advance();
   }
-  step_barrier<0>();
-  bool fresh = true;  // the current step is a tile's first
-  bool live = false;  // waves past the tile's last row only load
-  for (int copy = 0;; copy = copy + 1 == W::S ? 0 : copy + 1) {
-    // step kb of the current tile
-    const uint32_t stage = rows0 + copy * W::kStage;
-    const uint32_t next = rows0 + (copy + 1 == W::S ? 0 : copy + 1) * W::kStage;
-    if (fresh) {
-      live = wm * MT * 16 < (int)(cur.r1 - cur.r0);
-      if constexpr (P == kWgrad) sums = g.dbias && cur.c0 == 0;
-      // (every wave: fragments held past a tile's results would cost their registers there)
+  wait_vmcnt<0>();
+  step_barrier();
+  uint32_t stage = rows0;
+  auto after = [&](uint32_t copy) { return copy + W::kStage == rows_end ? rows0 : copy + W::kStage; };
+  for (;;) {
+    const bool live = wm * MT * 16 < cur.r1 - cur.r0;  // waves past the tile's last row only load
+    if constexpr (P == kWgrad) sums = g.dbias && cur.c0 == 0;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) t[m] = row_frag(stage, m);
-      w[0] = col_frag(stage, 0);
-      w[1] = col_frag(stage, 1);
+    for (int m = 0; m < MT; ++m) t[m] = row_frag(stage, m);
+    w[0] = col_frag(stage, 0);
+    w[1] = col_frag(stage, 1);
+    const int steps = max(cur.steps, W::kLeast);
+    for (int kb = 0; kb < steps; ++kb) {
+      const uint32_t next = after(stage);
+      step(stage, next, kb == 0, live);
+      stage = next;
     }
-    if (live) multiply(stage, next, 0, kOpen, copy, 0, 0);
-    // A tile's first step finds its loads landed (below), and the results of
-    // the tile before still on their way out.
-    if (fresh) step_barrier<63>();
-    else step_barrier<(W::S - 1) * kLoads>();
-    if (lk >= nxt.steps && lk >= W::S) {
-      lk = 0;
-      const int then = item_no(turn_no + slots);
-      more = then < total;
-      if (more) {  // (else the stream loads its last tile again)
-        turn_no += slots;
-        id = then;
-      }
-      aim();
-    }
-    begin_step();
-    if (live) multiply(stage, next, kOpen, NT - 2, copy, 0, kX);
-    else load(copy, 0, kX);
-    if (fresh) step_barrier<63>();
-    else step_barrier<(W::S - 1) * kLoads>();
-    if (live) multiply(stage, next, NT - 2, NT, copy, kX, kLoads);
-    else load(copy, kX, kLoads);
-    ++lk;
-    ++kb;
-    fresh = kb >= cur.steps && kb >= W::S;
-    if (fresh) {
-      wait_vmcnt<0>();  // before the stores: the next tile's first step waits for none of them
-      if (live) finish();
-      if (!more) break;
+    wait_vmcnt<0>();  // before the stores: the next tile's first step waits for none of them
+    if (live) finish();
+    if (!more) break;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) acc[n][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if constexpr (P == kWgrad)
+      for (int m = 0; m < MT; ++m) acc[n][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (P == kWgrad)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) bacc[m] = 0.0f;
-      cur = nxt;
-      kb = 0;
-    }
+      for (int m = 0; m < MT; ++m) bacc[m] = 0.0f;
+    cur = nxt;
   }
   wait_vmcnt<0>();  // no load may write this workgroup's LDS after its end
 }
