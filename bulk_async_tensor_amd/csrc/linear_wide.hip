@@ -137,6 +137,14 @@ __device__ __forceinline__ float add_places(bf16x8 f, float v) {
   return v;
 }
 
+// Rows of each of the n tiles that r rows are cut into: as even as 16 allows, so
+// that workgroups beside each other take the same time and find each other's
+// operands in their XCD's L2 (49152 rows of 64 experts, 700 to 840 each, gate
+// and up product EVEN_US us for 3050 with tiles of 256 rows and a rest).
+__device__ __forceinline__ int even_rows(int r, int n) {
+  return ((r + n * 16 - 1) / (n * 16)) * 16;
+}
+
 // Whether step k of an item is the sum's last, and not full.
 __device__ __forceinline__ bool late_step(const Item& t, int k, int deep) {
   return k < t.steps && (t.k0 + k + 1) * kDeep > deep;
@@ -262,8 +270,9 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
       const uint32_t tile = p / (uint32_t)units;
       nxt.c0 = (int)(p - tile * units) * kCols;
       nxt.e = (int)(tile / (uint32_t)un);
-      nxt.r0 = (int)(tile - nxt.e * un) * BM;
-      nxt.r1 = min(nxt.r0 + BM, g.N);
+      const int per = even_rows(g.N, un);
+      nxt.r0 = (int)(tile - nxt.e * un) * per;
+      nxt.r1 = min(nxt.r0 + per, g.N);
       const Segment s = linear_segment(g, nxt.e);
       nxt.lo = s.lo, nxt.hi = s.hi;
       all = (nxt.hi - nxt.lo + kDeep - 1) / kDeep;
@@ -278,8 +287,9 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
       const Segment s = linear_segment(g, e);
       nxt.e = e;
       nxt.c0 = (int)unit * per_unit;
-      nxt.r0 = s.lo + (int)(local - unit * mine) * BM;
-      nxt.r1 = min(nxt.r0 + BM, s.hi);
+      const int per = even_rows(s.hi - s.lo, mine);
+      nxt.r0 = s.lo + (int)(local - unit * mine) * per;
+      nxt.r1 = min(nxt.r0 + per, s.hi);
       all = (deep + kDeep - 1) / kDeep;
     }
     nxt.k0 = 0, nxt.steps = all;
@@ -366,10 +376,10 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   uint32_t r_lds[kRowsAcross ? MT : 2], c_lds[kColsAcross ? HT : 2];
   if constexpr (kRowsAcross) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) r_lds[m] = across_at(BM, wm * MT + m);
+    for (int m = 0; m < MT; ++m) r_lds[m] = across_at(BM, m * W::WM + wm);
   } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) r_lds[h] = along_at(h) + wm * MT * 16 * kStepBytes;
+    for (int h = 0; h < 2; ++h) r_lds[h] = along_at(h) + wm * 16 * kStepBytes;
   }
   if constexpr (kColsAcross) {
 #pragma unroll
@@ -402,7 +412,7 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   };
   auto row_frag = [&](uint32_t stage, int m) {
     if constexpr (kRowsAcross) return across_frag(stage + r_lds[m], BM);
-    else return along_frag(stage + r_lds[0] + m * 16 * kStepBytes, stage + r_lds[1] + m * 16 * kStepBytes);
+    else return along_frag(stage + r_lds[0] + m * W::WM * 16 * kStepBytes, stage + r_lds[1] + m * W::WM * 16 * kStepBytes);
   };
 
   Item cur;
@@ -423,6 +433,8 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   // step's last pair each can be read anew for the next step as soon as its
   // four products have started.  What else the step has to do (`more_work`, the
   // loads) stands between the products, or the matrix cores would wait for it.
+  // `held` row tiles of the wave's MT have rows.
+  int held = 0;
   auto multiply = [&](uint32_t stage, uint32_t next, int n, auto more_work) {
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -430,20 +442,22 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
       w[(n + 2 + i) & 3] = n + 2 < NT ? col_frag(stage, n + 2 + i) : col_frag(next, n + 2 + i - NT);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
+      if (m < held) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) acc[n + i][m] = mfma_bf16(w[(n + i) & 3].lo, t[m].lo, acc[n + i][m]);
+        for (int i = 0; i < 2; ++i) acc[n + i][m] = mfma_bf16(w[(n + i) & 3].lo, t[m].lo, acc[n + i][m]);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) acc[n + i][m] = mfma_bf16(w[(n + i) & 3].hi, t[m].hi, acc[n + i][m]);
-      more_work(m);
-      if (n == NT - 2) {
-        if constexpr (P == kWgrad)
-          if (sums) {
-            bacc[m] = add_places(t[m].lo, bacc[m]);
-            bacc[m] = add_places(t[m].hi, bacc[m]);
-          }
-        t[m] = row_frag(next, m);
-        __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < 2; ++i) acc[n + i][m] = mfma_bf16(w[(n + i) & 3].hi, t[m].hi, acc[n + i][m]);
+        if (n == NT - 2) {
+          if constexpr (P == kWgrad)
+            if (sums) {
+              bacc[m] = add_places(t[m].lo, bacc[m]);
+              bacc[m] = add_places(t[m].hi, bacc[m]);
+            }
+          t[m] = row_frag(next, m);
+        }
       }
+      more_work(m);
+      __builtin_amdgcn_sched_barrier(0);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -456,32 +470,22 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   // One step of the current tile in copy `stage`, the next one in `next`.  A
   // tile's first step finds its loads landed, and the results of the tile
   // before still on their way out: it waits for neither.
-  auto step = [&](uint32_t stage, uint32_t next, bool first, bool live) {
-    if (live && kOpen > 0) multiply(stage, next, 0, nothing);
+  auto step = [&](uint32_t stage, uint32_t next, bool first) {
+    if constexpr (kOpen > 0) multiply(stage, next, 0, nothing);
     if (!first) wait_vmcnt<(W::S - 1) * kLoads>();
     step_barrier();
-    if (live) {
-      constexpr int kPairs = (NT - 2 - kOpen) / 2, kEach = (kXLoads + kPairs - 1) / kPairs;
+    constexpr int kPairs = (NT - 2 - kOpen) / 2, kEach = (kXLoads + kPairs - 1) / kPairs;
 #pragma unroll
-      for (int q = 0; q < kPairs; ++q)
-        multiply(stage, next, kOpen + 2 * q, [&](int m) {
-          if (m < kEach) load_x(stage, q * kEach + m);
-        });
-    } else {
-#pragma unroll
-      for (int i = 0; i < kXLoads; ++i) load_x(stage, i);
-    }
-    if (!first) wait_vmcnt<(W::S - 1) * kLoads>();
-    step_barrier();
-    if (live) {
-      multiply(stage, next, NT - 2, [&](int m) {
-        if (m == 0) load_cols(stage, 1);
-        if (m == 1) advance();
+    for (int q = 0; q < kPairs; ++q)
+      multiply(stage, next, kOpen + 2 * q, [&](int m) {
+        if (m < kEach) load_x(stage, q * kEach + m);
       });
-    } else {
-      load_cols(stage, 1);
-      advance();
-    }
+    if (!first) wait_vmcnt<(W::S - 1) * kLoads>();
+    step_barrier();
+    multiply(stage, next, NT - 2, [&](int m) {
+      if (m == 0) load_cols(stage, 1);
+      if (m == 1) advance();
+    });
   };
 
   // A tile's results.  Lane (col, quad) holds columns 4 quad .. + 3 of each
@@ -496,7 +500,7 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
     ConstArgs f = (ConstArgs)__builtin_amdgcn_kernarg_segment_ptr();
     asm volatile("" : "+s"(f));
     const int64_t held = cur.r1 - cur.r0;
-    const int lr = wm * MT * 16 + col;
+    const int lr = wm * 16 + col;
     auto rows_of = [&](const void* p, int64_t row, int ld, int size) {
       return buffer_at(static_cast<const uint8_t*>(p) + row * ld * size, held * ld * size);
     };
@@ -504,7 +508,7 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
     auto column4 = [&](int n) { return (wn * HT + n % HT) * 16 + 4 * quad; };
     auto column8 = [&](int n) { return (wn * HT + n % HT) * 16 + 16 * (quad & 1) + 8 * (quad >> 1); };
     auto offset = [&](int m, int ld, int c, int end, int size) {
-      return (uint32_t)(((lr + m * 16) * ld + c) * size) | (c < end ? 0u : kNowhere);
+      return (uint32_t)(((lr + m * (W::WM * 16)) * ld + c) * size) | (c < end ? 0u : kNowhere);
     };
     auto put8 = [&](__amdgpu_buffer_rsrc_t to, uint32_t at, f32x4 a, f32x4 b) {
       const u32x2 x = narrow4(a), y = narrow4(b);
@@ -528,7 +532,8 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
         for (int m = 0; m < MT; ++m) {
           bacc[m] += __shfl_xor(bacc[m], 16, kWave);
           bacc[m] += __shfl_xor(bacc[m], 32, kWave);
-          if (wn == 0 && quad == 0 && lr + m * 16 < held) to[(int64_t)cur.e * f->N + cur.r0 + lr + m * 16] = bacc[m];
+          if (wn == 0 && quad == 0 && lr + m * (W::WM * 16) < held)
+            to[(int64_t)cur.e * f->N + cur.r0 + lr + m * (W::WM * 16)] = bacc[m];
         }
       }
     }
@@ -670,7 +675,8 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   uint32_t stage = rows0;
   auto after = [&](uint32_t copy) { return copy + W::kStage == rows_end ? rows0 : copy + W::kStage; };
   for (;;) {
-    const bool live = wm * MT * 16 < cur.r1 - cur.r0;  // waves past the tile's last row only load
+    // of the tile's row tiles, every WM-th is the wave's
+    held = min(max(((cur.r1 - cur.r0 + 15) / 16 - wm + W::WM - 1) / W::WM, 0), MT);
     if constexpr (P == kWgrad) sums = g.dbias && cur.c0 == 0;
 #pragma unroll
     for (int m = 0; m < MT; ++m) t[m] = row_frag(stage, m);
@@ -679,11 +685,11 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
     const int steps = max(cur.steps, W::kLeast);
     for (int kb = 0; kb < steps; ++kb) {
       const uint32_t next = after(stage);
-      step(stage, next, kb == 0, live);
+      step(stage, next, kb == 0);
       stage = next;
     }
     wait_vmcnt<0>();  // before the stores: the next tile's first step waits for none of them
-    if (live) finish();
+    if (held > 0) finish();
     if (!more) break;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
