@@ -119,14 +119,7 @@ struct Item {
 };
 
 __device__ __forceinline__ Segment linear_segment(const LinearArgs& g, int e) {
-  if (!g.offsets) return Segment{0, (int)g.rows};
-  // (scalar loads: a vector load would wait for every load in flight)
-  typedef const __attribute__((address_space(4))) int32_t* scalar_i32;
-  const scalar_i32 at = (scalar_i32)(uintptr_t)(g.offsets + e);
-  Segment s;
-  s.lo = min(max(at[0], 0), (int)g.rows);
-  s.hi = min(max(at[1], s.lo), (int)g.rows);
-  return s;
+  return g.offsets ? segment_of(g.offsets, (int)g.rows, e) : Segment{0, (int)g.rows};
 }
 
 // The sum of eight bf16 values, added to v pair by pair in float32.
@@ -160,7 +153,8 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   constexpr int HT = W::HT, NT = W::NT, MT = W::MT;
   constexpr bool kRowsAcross = P == kWgrad, kColsAcross = P != kForward;
   __shared__ __attribute__((aligned(1024))) uint8_t s_rows[W::S * W::kStage];
-  __shared__ int32_t s_first[kMaxExperts + 1];
+  __shared__ int32_t s_first[P == kWgrad ? 1 : kMaxExperts + 1];
+  __shared__ Segment s_seg[kMaxExperts];
   const int lane = lane_id(), wave = wave_in_group();
   const int col = lane & 15, quad = lane >> 4;
   const int wn = wave % W::WN, wm = wave / W::WN;
@@ -173,16 +167,16 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   // ---- the items of this workgroup
   const int un = (g.N + BM - 1) / BM;  // wgrad: tiles along the weight rows
   int tiles;
-  if constexpr (P == kWgrad) {
-    tiles = g.E * un;
-  } else {
+  for (int e = threadIdx.x; e < g.E; e += kWaves * kWave) s_seg[e] = linear_segment(g, e);
+  if constexpr (P != kWgrad) {
     if (wave == 0) {
       if (g.offsets) first_tiles<BM>(g.offsets, g.E, (int)g.rows, lane, s_first);
       else if (lane < 2) s_first[lane] = lane ? (int32_t)((g.rows + BM - 1) / BM) : 0;
     }
-    __syncthreads();
-    tiles = __builtin_amdgcn_readfirstlane(s_first[g.E]);
   }
+  __syncthreads();
+  if constexpr (P == kWgrad) tiles = g.E * un;
+  else tiles = __builtin_amdgcn_readfirstlane(s_first[g.E]);
   // (as many as the host counts where offsets ascend; no more where they do not)
   const int products = min(tiles, kMostItems / (units * shape.splits)) * units, total = products * shape.splits;
   const int slots = gridDim.x / kXcds;
@@ -273,8 +267,8 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
       const int per = even_rows(g.N, un);
       nxt.r0 = (int)(tile - nxt.e * un) * per;
       nxt.r1 = min(nxt.r0 + per, g.N);
-      const Segment s = linear_segment(g, nxt.e);
-      nxt.lo = s.lo, nxt.hi = s.hi;
+      nxt.lo = __builtin_amdgcn_readfirstlane(s_seg[nxt.e].lo);
+      nxt.hi = __builtin_amdgcn_readfirstlane(s_seg[nxt.e].hi);
       all = (nxt.hi - nxt.lo + kDeep - 1) / kDeep;
     } else {
       // two rounds of 64 and 16 comparisons find the expert
@@ -284,12 +278,12 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
       const int before = __builtin_amdgcn_readfirstlane(s_first[e]);
       const int mine = __builtin_amdgcn_readfirstlane(s_first[e + 1]) - before;
       const uint32_t local = p - (uint32_t)before * units, unit = local / (uint32_t)mine;
-      const Segment s = linear_segment(g, e);
+      const int lo = __builtin_amdgcn_readfirstlane(s_seg[e].lo), hi = __builtin_amdgcn_readfirstlane(s_seg[e].hi);
       nxt.e = e;
       nxt.c0 = (int)unit * per_unit;
-      const int per = even_rows(s.hi - s.lo, mine);
-      nxt.r0 = s.lo + (int)(local - unit * mine) * per;
-      nxt.r1 = min(nxt.r0 + per, s.hi);
+      const int per = even_rows(hi - lo, mine);
+      nxt.r0 = lo + (int)(local - unit * mine) * per;
+      nxt.r1 = min(nxt.r0 + per, hi);
       all = (deep + kDeep - 1) / kDeep;
     }
     nxt.k0 = 0, nxt.steps = all;
@@ -467,12 +461,17 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
     if (i < W::LT / 2) load_rows(stage, 2 * i);
     else if (i < kXLoads) load_cols(stage, 0);
   };
-  // One step of the current tile in copy `stage`, the next one in `next`.  A
-  // tile's first step finds its loads landed, and the results of the tile
-  // before still on their way out: it waits for neither.
-  auto step = [&](uint32_t stage, uint32_t next, bool first) {
+  // The fewest stores that finish() issues.  They are younger than the loads
+  // that a tile's first S steps wait for, which need not wait for them too.
+  constexpr int kStores = P == kForward && ACT == EP_ACT_SWIGLU ? NT * MT / 4 : NT * MT / 2;
+  constexpr int kNewer = (W::S - 1) * kLoads;
+  static_assert(kNewer + kStores <= 63, "vmcnt is a 6-bit field");
+  bool stored = false;  // the tile before left results
+  // Step kb of the current tile in copy `stage`, the next one in `next`.
+  auto step = [&](uint32_t stage, uint32_t next, int kb) {
     if constexpr (kOpen > 0) multiply(stage, next, 0, nothing);
-    if (!first) wait_vmcnt<(W::S - 1) * kLoads>();
+    if (stored && kb < W::S) wait_vmcnt<kNewer + kStores>();
+    else wait_vmcnt<kNewer>();
     step_barrier();
     constexpr int kPairs = (NT - 2 - kOpen) / 2, kEach = (kXLoads + kPairs - 1) / kPairs;
 #pragma unroll
@@ -480,7 +479,8 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
       multiply(stage, next, kOpen + 2 * q, [&](int m) {
         if (m < kEach) load_x(stage, q * kEach + m);
       });
-    if (!first) wait_vmcnt<(W::S - 1) * kLoads>();
+    if (stored && kb < W::S - 1) wait_vmcnt<kNewer + kStores>();
+    else wait_vmcnt<kNewer>();
     step_barrier();
     multiply(stage, next, NT - 2, [&](int m) {
       if (m == 0) load_cols(stage, 1);
@@ -685,11 +685,11 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
     const int steps = max(cur.steps, W::kLeast);
     for (int kb = 0; kb < steps; ++kb) {
       const uint32_t next = after(stage);
-      step(stage, next, kb == 0);
+      step(stage, next, kb);
       stage = next;
     }
-    wait_vmcnt<0>();  // before the stores: the next tile's first step waits for none of them
     if (held > 0) finish();
+    stored = held > 0;
     if (!more) break;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
