@@ -181,15 +181,18 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   const int products = min(tiles, kMostItems / (units * shape.splits)) * units, total = products * shape.splits;
   const int slots = gridDim.x / kXcds;
   const int xcd = blockIdx.x % kXcds;
-  int turn_no = blockIdx.x / kXcds;
+  const int slot = blockIdx.x / kXcds;
+  int round = 0;
   // Forward and dgrad: a run of items for each XCD, whose tiles share weights.
-  // wgrad, where an item's cost goes by its expert's rows: runs of 32 in turn.
+  // wgrad, where an item's cost goes by its expert's rows: every XCD takes as
+  // many items as it has workgroups in turn.
   const int run = (total + kXcds - 1) / kXcds;
-  auto item_no = [&](int i) {
-    if constexpr (P == kWgrad) return ((i >> 5) * kXcds + xcd) * 32 + (i & 31);
+  auto item_no = [&](int r) {
+    if constexpr (P == kWgrad) return (r * kXcds + xcd) * slots + slot;
+    const int i = slot + r * slots;
     return i < run ? xcd * run + i : total;
   };
-  int id = item_no(turn_no);
+  int id = item_no(0);
   if (id >= total) return;
 
   // ---- the loads of the stream
@@ -329,10 +332,10 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
     }
     if (lk >= nxt.steps && lk >= W::kLeast) {
       lk = 0;
-      const int then = item_no(turn_no + slots);
+      const int then = item_no(round + 1);
       more = then < total;
       if (more) {  // (else the stream loads its last tile again)
-        turn_no += slots;
+        ++round;
         id = then;
       }
       aim();
@@ -710,33 +713,30 @@ __global__ __launch_bounds__(kWaves * kWave) __attribute__((amdgpu_waves_per_eu(
   linear_wide<P, ACT, BM>(g, shape);
 }
 
-// ---- the runs of a cut sum, added in order, and what follows the product
-constexpr int kJoinWaves = 4, kJoinCols = 4 * kWave;  // a wave takes 256 columns of a row
+// ---- the runs of a cut sum, added, and what follows the product: a workgroup
+// takes 256 columns of a row, a wave every fourth run, eight loads at a time,
+// and the waves' sums are added in their order.
+constexpr int kJoinWaves = 4, kJoinCols = 4 * kWave;
 
-__device__ __forceinline__ f32x4 join4(const float* p, int64_t stride, int splits) {
-  f32x4 v = *reinterpret_cast<const f32x4*>(p);
-  for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(p + s * stride);
+__device__ __forceinline__ f32x4 join4(const float* p, int64_t stride, int first, int splits) {
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int s = first; s < splits; s += kJoinWaves) v += *reinterpret_cast<const f32x4*>(p + s * stride);
   return v;
 }
 
 template <Product P, int ACT>
 __global__ __launch_bounds__(kJoinWaves * kWave) void join_kernel(LinearArgs g, int splits) {
-  const int lane = lane_id();
+  __shared__ f32x4 s_sum[2][kJoinWaves][kWave];
+  const int lane = lane_id(), wave = wave_in_group();
   constexpr bool pair = P == kForward && ACT == EP_ACT_SWIGLU;
   const int wide = P == kForward ? g.N : g.K, outs = pair ? wide / 2 : wide;
   const int units = (outs + kJoinCols - 1) / kJoinCols;
   const int64_t many = P == kWgrad ? (int64_t)g.E * g.N : g.rows;
   const int64_t stride = many * wide;
-  for (int64_t u = (int64_t)blockIdx.x * kJoinWaves + wave_in_group(); u < many * units;
-       u += (int64_t)gridDim.x * kJoinWaves) {
+  for (int64_t u = blockIdx.x; u < many * units; u += gridDim.x) {
     const int64_t r = u / units;
     const int c = (int)(u % units) * kJoinCols + lane * 4;
-    if (P == kWgrad && g.dbias && u % units == 0 && lane == 0) {
-      const float* p = g.partial + splits * stride + r;
-      float v = p[0];
-      for (int s = 1; s < splits; ++s) v += p[s * many];
-      g.dbias[r] = v;
-    }
     int e = 0;
     if (P != kWgrad && g.offsets) {
       if (r < linear_segment(g, 0).lo || r >= linear_segment(g, g.E - 1).hi) continue;  // rows that no expert holds
@@ -745,17 +745,32 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void join_kernel(LinearArgs g, 
         e += __builtin_popcountll(ballot(e0 + lane < g.E && g.offsets[e0 + lane + 1] <= r));
       e = min(e, g.E - 1);
     }
-    if (c >= outs) continue;
     const float* p = g.partial + r * wide + c;
-    const f32x4 v = join4(p, stride, splits);
-    if constexpr (P == kForward) {
-      if constexpr (pair) finish_swiglu(g, e, r, c, v, join4(p + outs, stride, splits));
-      else finish_linear<ACT>(g, e, r, c, v);
-    } else if constexpr (P == kDgrad) {
-      finish_dgrad<ACT>(g, r, c, v);
-    } else {
-      finish_wgrad(g, r * wide + c, v);
+    if (c < outs) {
+      s_sum[0][wave][lane] = join4(p, stride, wave, splits);
+      if constexpr (pair) s_sum[1][wave][lane] = join4(p + outs, stride, wave, splits);
     }
+    __syncthreads();
+    if (wave == 0 && c < outs) {
+      f32x4 v[2];
+#pragma unroll
+      for (int h = 0; h < (pair ? 2 : 1); ++h) {
+        v[h] = s_sum[h][0][lane];
+#pragma unroll
+        for (int w = 1; w < kJoinWaves; ++w) v[h] += s_sum[h][w][lane];
+      }
+      if constexpr (pair) finish_swiglu(g, e, r, c, v[0], v[1]);
+      else if constexpr (P == kForward) finish_linear<ACT>(g, e, r, c, v[0]);
+      else if constexpr (P == kDgrad) finish_dgrad<ACT>(g, r, c, v[0]);
+      else finish_wgrad(g, r * wide + c, v[0]);
+    }
+    if (P == kWgrad && wave == 1 && g.dbias && u % units == 0 && lane == 0) {
+      const float* q = g.partial + splits * stride + r;
+      float v = q[0];
+      for (int s = 1; s < splits; ++s) v += q[s * many];
+      g.dbias[r] = v;
+    }
+    __syncthreads();
   }
 }
 
@@ -771,8 +786,8 @@ hipError_t launch(const Budget& b, const LinearArgs& g, const LinearShape& s, hi
   if (e != hipSuccess || s.splits == 1) return e;
   const int wide = P == kForward ? (ACT == EP_ACT_SWIGLU ? g.N / 2 : g.N) : g.K;
   const int64_t units = (P == kWgrad ? (int64_t)g.E * g.N : g.rows) * ((wide + kJoinCols - 1) / kJoinCols);
-  const int64_t most = 8LL * b.device_cus, groups = (units + kJoinWaves - 1) / kJoinWaves;
-  hipLaunchKernelGGL((join_kernel<P, ACT>), dim3((uint32_t)(groups < most ? groups : most)), dim3(kJoinWaves * kWave), 0,
+  const int64_t most = 8LL * b.device_cus;
+  hipLaunchKernelGGL((join_kernel<P, ACT>), dim3((uint32_t)(units < most ? units : most)), dim3(kJoinWaves * kWave), 0,
                      stream, g, s.splits);
   return hipGetLastError();
 }
