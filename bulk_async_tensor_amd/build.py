@@ -34,7 +34,7 @@ KERNEL_SOURCES = {
     "dispatch_fp8": ["dispatch_fp8.hip", "fp8_device.hpp", "expert_internal.hpp", "ep_device.hpp", "ep_internal.hpp"],
     "grouped_fp8": ["grouped_fp8.hip", "grouped_wide.hip", "grouped_swiglu.hip", "grouped_tiles.hpp", "fp8_device.hpp",
                     "expert_shapes.hpp", "expert_internal.hpp", "ep_device.hpp", "ep_internal.hpp"],
-    "route": ["route.hip", "layer_internal.hpp", "ep_device.hpp", "ep_internal.hpp"],
+    "route": ["route.hip", "route_shapes.hpp", "layer_internal.hpp", "ep_device.hpp", "ep_internal.hpp"],
     "linear": ["linear_wide.hip", "linear_shapes.hpp", "linear_epilogue.hpp", "layer_internal.hpp", "grouped_tiles.hpp",
                "fp8_device.hpp", "expert_internal.hpp", "ep_device.hpp", "ep_internal.hpp"],
     "backward": ["backward.hip", "expert_shapes.hpp", "row_io.hpp", "expert_internal.hpp", "ep_device.hpp",

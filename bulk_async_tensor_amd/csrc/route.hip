@@ -1,17 +1,36 @@
 // ep_route and ep_route_backward: the router's choice of experts for each
 // token, its weights, and the weights' gradient to the logits.
+//
+// ep_route.  The choice has to be that of exact scores, but float32 is enough
+// to make nearly all of it: a token's experts are ranked by float32 keys, and
+// where two neighbours of the ranking (or the groups at the edge) are closer
+// than the keys can be wrong, and not equal by having the same logit and bias,
+// the token is done again in float64 by the whole wave (route_exact).
+//
+// 16 lanes take a token (64 where there are more than 512 experts, more than
+// 15 are chosen, or few tokens are there), a lane NV neighbouring experts.  A
+// key is the 31 high bits of an integer that orders as the score does, its
+// lowest bits replaced by the expert's place in the lane, so that keys differ
+// within a lane and the largest names its expert.  Choosing one: each lane
+// finds its largest key below the last one it gave (key - last wraps to the top
+// of the unsigned range exactly for smaller keys, so that is one subtraction
+// and half a maximum a key); four exchanges give the token's largest value, a ballot
+// the first lane that holds it (of equal values the lowest expert).
+//
+// T 16384, E 256, groups: ROUTE_NUMBERS
 #include <math.h>
 
 #include "ep.h"
 #include "ep_device.hpp"
 #include "layer_internal.hpp"
+#include "route_shapes.hpp"
 
 namespace ep {
 
 namespace {
 
 constexpr int kRouteWaves = 4;
-constexpr int kPerLane = kMaxExperts / kWave;
+constexpr int64_t kRouteGroups = 1 << 20;  // workgroups of a launch: a grid has fewer than 2^32 lanes
 
 __device__ __forceinline__ float logit_at(const void* logits, int bf16, int64_t i) {
   return bf16 ? __uint_as_float((uint32_t) static_cast<const uint16_t*>(logits)[i] << 16)
@@ -50,8 +69,10 @@ __device__ __forceinline__ double sigmoid64(double l) {
   return (l < 0.0 ? e : 1.0) / (1.0 + e);
 }
 
-// One token by one wave, scores in float64.  s_c: E doubles of LDS.
-__device__ void route_exact(const RouteArgs& a, int64_t t, int lane, double* s_c) {
+// One token by one wave, scores in float64, kPerLane experts a lane.  s_c: E
+// doubles of LDS.
+template <int kPerLane>
+__device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t t, int lane, double* s_c) {
   const int E = a.E;
   double l[kPerLane], c[kPerLane];
   double top = -INFINITY, total = 0.0;
@@ -182,11 +203,264 @@ __device__ void route_exact(const RouteArgs& a, int64_t t, int lane, double* s_c
   }
 }
 
+// ---- float32
+
+// The exchange of step d within 16 lanes, after which each lane has the value
+// of another that held a different half (d = 0, 1: lanes 1 and 2 away; 2, 3:
+// the mirrored lane of 8 and of 16).
+template <int D>
+__device__ __forceinline__ int exchange16(int v) {
+  constexpr int ctrl = D == 0 ? 0xB1 : D == 1 ? 0x4E : D == 2 ? 0x141 : 0x140;
+  return __builtin_amdgcn_mov_dpp(v, ctrl, 0xF, 0xF, true);
+}
+template <int L, class Op>
+__device__ __forceinline__ int all_lanes(int v, Op op) {
+  v = op(v, exchange16<0>(v));
+  v = op(v, exchange16<1>(v));
+  v = op(v, exchange16<2>(v));
+  v = op(v, exchange16<3>(v));
+  if constexpr (L == 64) {
+    const int a = op(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16));
+    const int b = op(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48));
+    v = op(a, b);
+  }
+  return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  return (uint32_t)all_lanes<L>((int)v, [](int a, int b) { return (int)max((uint32_t)a, (uint32_t)b); });
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+  return __int_as_float(
+      all_lanes<L>(__float_as_int(v), [](int a, int b) { return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b))); }));
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  return __int_as_float(
+      all_lanes<L>(__float_as_int(v), [](int a, int b) { return __float_as_int(__int_as_float(a) + __int_as_float(b)); }));
+}
+// The bits of a ballot that belong to the caller's token, its first lane lowest.
+template <int L>
+__device__ __forceinline__ uint64_t token_bits(uint64_t ballot_bits, int lane) {
+  return L == 64 ? ballot_bits : (ballot_bits >> (lane & ~(L - 1))) & ((1ull << (L & 63)) - 1);
+}
+
+// 31 bits that order as v does; zero is below all of them.  No NaN, no -0.
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const int b = __float_as_int(v);
+  return ((uint32_t)b ^ ((uint32_t)(b >> 31) | 0x80000000u)) >> 1;
+}
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+
+template <int L, int NV, bool BF16>
+struct RouteShape {
+  static constexpr int kTokens = kWave / L;             // of a wave
+  static constexpr int kScores = L * NV + kMaxGroups;   // floats of LDS for a token: scores, a place between groups
+  static constexpr int kFloats = kTokens * (kScores + kMaxGroups);
+  static constexpr int kLds = kFloats * 4 > L * NV * 8 ? kFloats * 4 : L * NV * 8;  // (and the exact path's scores)
+  static constexpr int kExact = (L * NV + kWave - 1) / kWave;
+};
+
+template <int L, int NV, bool BF16>
 __global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(RouteArgs a) {
-  __shared__ double s_c[kRouteWaves][kMaxExperts];
-  const int wave = wave_in_group();
-  const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
-  if (t < a.T) route_exact(a, t, lane_id(), s_c[wave]);
+  using S = RouteShape<L, NV, BF16>;
+  __shared__ __attribute__((aligned(16))) uint8_t s_all[kRouteWaves][S::kLds];
+  const int lane = lane_id(), wave = wave_in_group();
+  const int sub = lane & (L - 1), token = lane / L;
+  const int E = a.E;
+  const bool scores = a.bias || a.groups > 1;  // compared by score; else by logit
+  const bool vectors = E % (BF16 ? 8 : 4) == 0 && ((uintptr_t)a.logits & 15) == 0;
+  const bool sums = !a.sigmoid && (scores || !a.renorm);  // the softmax's sum is needed
+  float* const s_c = reinterpret_cast<float*>(s_all[wave]) + token * (S::kScores + kMaxGroups);
+  float* const s_rank = s_c + S::kScores;
+
+  const int64_t step = (int64_t)gridDim.x * kRouteWaves * S::kTokens;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * S::kTokens; t0 < a.T; t0 += step) {
+    const int64_t t = t0 + token;
+    const bool held = t < a.T;
+    const int64_t row = (held ? t : t0) * E;
+    // ---- the lane's logits; an absent one counts as -infinity
+    float l[NV];
+    const int e0 = sub * NV;
+    if (vectors) {
+      constexpr int kPer = BF16 ? 8 : 4;
+#pragma unroll
+      for (int i = 0; i < NV; i += kPer) {
+        u32x4 v = {0u, 0u, 0u, 0u};
+        const bool in = e0 + i < E;
+        if (NV < kPer) {
+          // (four bf16 values a lane)
+          uint2 h = make_uint2(0u, 0u);
+          if (in) h = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + row + e0 + i);
+          v[0] = h.x, v[1] = h.y;
+        } else if (in) {
+          v = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.logits) + (row + e0 + i) * (BF16 ? 2 : 4));
+        }
+#pragma unroll
+        for (int q = 0; q < (NV < kPer ? NV : kPer); ++q) {
+          const float x = BF16 ? (q & 1 ? bf16_hi(v[q / 2]) : bf16_lo(v[q / 2])) : __uint_as_float(v[q & 3]);
+          l[i + q] = in ? x : -INFINITY;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) l[i] = e0 + i < E ? logit_at(a.logits, BF16, row + e0 + i) : -INFINITY;
+    }
+    // ---- scores and keys
+    bool again = false;  // float32 does not decide this token
+    float top = 0.0f, inv = 0.0f;
+    if (sums) {
+      top = l[0];
+#pragma unroll
+      for (int i = 1; i < NV; ++i) top = fmaxf(top, l[i]);
+      top = lanes_max<L>(top);
+      float total = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) total += exp_fast(l[i] - top);  // (a NaN, +infinity, or nothing else than -infinity: NaN)
+      total = lanes_sum<L>(total);
+      again = total != total;
+      inv = 1.0f / total;
+    }
+    // What the scores may be off by, twice.  Sigmoid: exp's argument loses 1.5 |l|
+    // half steps, of which its slope leaves 0.34, and four are added by exp, sum
+    // and reciprocal: 2^-22.  Softmax: the sum's roundings, NV and a few half
+    // steps, relative to scores of at most 1 / total, and 2^-24 by exp.
+    const float score_error = !scores ? 0.0f : a.sigmoid ? 0x1p-20f : inv * (NV + 10) * 0x1p-23f + 0x1p-22f;
+    uint32_t key[NV];
+    float probe = 0.0f;  // NaN if any is
+    float c[NV];
+    if (scores) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        c[i] = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + exp_fast(-l[i])) : exp_fast(l[i] - top) * inv;
+        if (a.bias && e0 + i < E) c[i] += a.bias[e0 + i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) c[i] = l[i] + 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (e0 + i < E) probe += c[i];
+      key[i] = e0 + i < E ? (key_of(c[i]) & ~(uint32_t)(NV - 1)) | (uint32_t)(NV - 1 - i) : 0u;
+    }
+    probe = lanes_sum<L>(probe);
+    again |= probe != probe;
+    // ---- the best groups
+    if (a.groups > 1) {
+      const int per = E / a.groups;
+      const uint32_t over = ((1u << 20) + per - 1) / per;  // e / per = e * over >> 20 for e < 1024
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const uint32_t e = e0 + i;
+        if ((int)e < E) s_c[e + (e * over >> 20)] = c[i];  // (a place between the groups: other banks)
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      for (int g = sub; g < a.groups; g += L) {
+        float v1 = -INFINITY, v2 = -INFINITY;
+        const float* p = s_c + g * (per + 1);
+        for (int i = 0; i < per; ++i) {
+          const float v = p[i];
+          v2 = fmaxf(v2, fminf(v1, v));
+          v1 = fmaxf(v1, v);
+        }
+        s_rank[g] = a.group_best == 2 ? v1 + v2 : v1;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      uint64_t kept = 0;
+      float worst = INFINITY, next = -INFINITY;  // of the groups kept, and the best of the others
+      for (int g0 = 0; g0 < a.groups; g0 += L) {
+        const int g = g0 + sub;
+        const float mine = g < a.groups ? s_rank[g] : -INFINITY;
+        int before = g < a.groups ? 0 : kMaxGroups;
+        for (int o = 0; o < a.groups; ++o) {
+          const float r = s_rank[o];
+          before += r > mine || (r == mine && o < g);
+        }
+        const bool keep = before < a.top_groups;
+        if (keep) worst = fminf(worst, mine);
+        else next = fmaxf(next, mine);
+        kept |= token_bits<L>(ballot(keep), lane) << g0;
+      }
+      worst = -lanes_max<L>(-worst);
+      next = lanes_max<L>(next);
+      // (sums of two: twice the scores' error, and their own rounding)
+      again |= a.top_groups < a.groups && !(worst - next > 2.0f * score_error + 0x1p-21f * fmaxf(fabsf(worst), fabsf(next)));
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const uint32_t e = e0 + i;
+        if (!(kept >> (e * over >> 20 & 63) & 1)) key[i] = 0u;
+      }
+    }
+    // ---- the choice: slot j in lane j, and the best that is left in lane k
+    uint32_t last = 1u << 31;
+    int32_t* const s_slot = reinterpret_cast<int32_t*>(s_rank);
+    for (int j = 0; j <= a.k; ++j) {
+      uint32_t most = key[0] - last;
+#pragma unroll
+      for (int i = 1; i < NV; ++i) most = max(most, key[i] - last);
+      const uint32_t best = most >> 31 ? most + last : 0u;  // (none left: zero)
+      const uint32_t value = best & ~(uint32_t)(NV - 1), all = lanes_max<L>(value);
+      const uint64_t who = token_bits<L>(ballot(value == all), lane);
+      if (sub == (L == 64 ? __builtin_ctzll(who) : __builtin_ctz((uint32_t)who))) {
+        last = best;
+        s_slot[j] = all != 0u ? e0 + (NV - 1) - (int)(best & (NV - 1)) : -1;
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int mine = sub <= a.k ? s_slot[sub] : -1;
+    // ---- its weights, and whether the order is certain
+    const bool here = sub < a.k;
+    const float lj = mine >= 0 ? logit_at(a.logits, BF16, row + mine) : -INFINITY;
+    const float bj = mine >= 0 && a.bias ? a.bias[mine] : 0.0f;
+    float sj = 0.0f;
+    {
+      float cj = lj;
+      if (scores) {
+        cj = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + exp_fast(-lj)) : exp_fast(lj - top) * inv;
+        cj += bj;
+      }
+      const int up = sub + 1 < L ? lane + 1 : lane;
+      const float cn = __shfl(cj, up, kWave), ln = __shfl(lj, up, kWave), bn = __shfl(bj, up, kWave);
+      const int en = __shfl(mine, up, kWave);
+      const float scale = fmaxf(fabsf(cj), fabsf(cn));
+      // a key's cell is 2 NV steps of float32, the sums' roundings two
+      const float margin = scale * (2.0f * NV + 2.0f) * 0x1p-23f + score_error;
+      const bool clear = !here || en < 0 || (lj == ln && bj == bn) || (cn == -INFINITY && cj > cn) || cj - cn > margin;
+      again |= token_bits<L>(ballot(!clear), lane) != 0;
+    }
+    const float most = lanes_max<L>(here ? lj : -INFINITY);
+    again |= !(fabsf(most) < INFINITY);
+    if (a.renorm) {
+      if (a.sigmoid) {
+        const float shift = fminf(most, 0.0f);
+        sj = lj > 0.0f ? expf(-shift) / (1.0f + expf(-lj)) : expf(lj - shift) / (1.0f + expf(lj));
+      } else {
+        sj = expf(lj - most);
+      }
+      if (!here) sj = 0.0f;
+      sj /= lanes_sum<L>(sj);
+    } else if (a.sigmoid) {
+      const float x = expf(-fabsf(lj));
+      sj = (lj < 0.0f ? x : 1.0f) / (1.0f + x);
+    } else {
+      sj = expf(lj - top) * inv;
+    }
+    if (held && here && !again) {
+      a.idx[t * a.k + sub] = mine;
+      a.w[t * a.k + sub] = sj * a.scale;
+    }
+    // ---- the tokens that are left
+    uint64_t left = ballot(held && sub == 0 && again);
+    while (left) {
+      const int at = __builtin_ctzll(left);
+      left &= left - 1;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      route_exact<S::kExact>(a, t0 + at / L, lane, reinterpret_cast<double*>(s_all[wave]));
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -200,10 +474,7 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
-__global__ __launch_bounds__(kRouteWaves * kWave) void route_backward_kernel(RouteBackwardArgs a) {
-  const int lane = lane_id();
-  const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave_in_group();
-  if (t >= a.T) return;
+__device__ __forceinline__ void route_back(const RouteBackwardArgs& a, int64_t t, int lane) {
   const int E = a.E;
   // lane j: slot j
   const int e = lane < a.k ? a.idx[t * a.k + lane] : -1;
@@ -267,19 +538,47 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_backward_kernel(Rou
   }
 }
 
+__global__ __launch_bounds__(kRouteWaves * kWave) void route_backward_kernel(RouteBackwardArgs a) {
+  const int64_t step = (int64_t)gridDim.x * kRouteWaves;
+  for (int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave_in_group(); t < a.T; t += step) route_back(a, t, lane_id());
+}
+
 }  // namespace
 
-hipError_t launch_route(const Budget& b, const RouteArgs& a, hipStream_t stream) {
-  (void)b;
-  hipLaunchKernelGGL(route_kernel, dim3((a.T + kRouteWaves - 1) / kRouteWaves), dim3(kRouteWaves * kWave), 0, stream,
-                     a);
+namespace {
+
+template <int L, int NV>
+hipError_t launch_shape(const RouteArgs& a, hipStream_t stream) {
+  const int64_t groups = ((int64_t)a.T + kRouteWaves * (kWave / L) - 1) / (kRouteWaves * (kWave / L));
+  const dim3 grid((uint32_t)(groups < kRouteGroups ? groups : kRouteGroups)), block(kRouteWaves * kWave);
+  if (a.bf16) hipLaunchKernelGGL((route_kernel<L, NV, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((route_kernel<L, NV, false>), grid, block, 0, stream, a);
   return hipGetLastError();
 }
 
-hipError_t launch_route_backward(const Budget& b, const RouteBackwardArgs& a, hipStream_t stream) {
-  (void)b;
-  hipLaunchKernelGGL(route_backward_kernel, dim3((a.T + kRouteWaves - 1) / kRouteWaves), dim3(kRouteWaves * kWave), 0,
-                     stream, a);
+}  // namespace
+
+hipError_t launch_route(const Budget& b, const RouteArgs& a, hipStream_t stream) {
+  const RouteLanes r = route_lanes(a.T, a.E, a.k, b.device_cus);
+  if (r.lanes == 16) {
+    switch (r.each) {
+      case 4: return launch_shape<16, 4>(a, stream);
+      case 8: return launch_shape<16, 8>(a, stream);
+      case 16: return launch_shape<16, 16>(a, stream);
+      default: return launch_shape<16, 32>(a, stream);
+    }
+  }
+  switch (r.each) {
+    case 4: return launch_shape<64, 4>(a, stream);
+    case 8: return launch_shape<64, 8>(a, stream);
+    default: return launch_shape<64, 16>(a, stream);
+  }
+}
+
+hipError_t launch_route_backward(const Budget&, const RouteBackwardArgs& a, hipStream_t stream) {
+  const int64_t groups = ((int64_t)a.T + kRouteWaves - 1) / kRouteWaves;
+  hipLaunchKernelGGL(route_backward_kernel, dim3((uint32_t)(groups < kRouteGroups ? groups : kRouteGroups)),
+                     dim3(kRouteWaves * kWave), 0, stream, a);
   return hipGetLastError();
 }
 
