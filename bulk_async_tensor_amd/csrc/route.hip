@@ -30,7 +30,7 @@ namespace ep {
 namespace {
 
 constexpr int kRouteWaves = 4;
-constexpr int64_t kRouteGroups = 1 << 20;  // workgroups of a launch: a grid has fewer than 2^32 lanes
+constexpr int64_t kRouteGroups = 1 << 22;  // workgroups of a launch: a grid has fewer than 2^32 lanes
 
 __device__ __forceinline__ float logit_at(const void* logits, int bf16, int64_t i) {
   return bf16 ? __uint_as_float((uint32_t) static_cast<const uint16_t*>(logits)[i] << 16)
@@ -45,165 +45,6 @@ __device__ __forceinline__ int64_t order_of(double v) {
   const int64_t b = __double_as_longlong(v + 0.0);
   return b < 0 ? b ^ INT64_MAX : b;
 }
-
-// The larger key of two lanes, of equal ones the lower index: over the wave.
-__device__ __forceinline__ void wave_best(int64_t& key, int& at) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const int64_t k = __shfl_xor(key, d, kWave);
-    const int i = __shfl_xor(at, d, kWave);
-    if (k > key || (k == key && i < at)) {
-      key = k;
-      at = i;
-    }
-  }
-}
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d, kWave);
-  return v;
-}
-
-__device__ __forceinline__ double sigmoid64(double l) {
-  const double e = exp(-fabs(l));
-  return (l < 0.0 ? e : 1.0) / (1.0 + e);
-}
-
-// One token by one wave, scores in float64, kPerLane experts a lane.  s_c: E
-// doubles of LDS.
-template <int kPerLane>
-__device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t t, int lane, double* s_c) {
-  const int E = a.E;
-  double l[kPerLane], c[kPerLane];
-  double top = -INFINITY, total = 0.0;
-#pragma unroll
-  for (int i = 0; i < kPerLane; ++i) {
-    const int e = i * kWave + lane;
-    l[i] = e < E ? (double)logit_at(a.logits, a.bf16, t * E + e) : -INFINITY;
-    top = l[i] > top || l[i] != l[i] ? l[i] : top;
-  }
-  if (!a.sigmoid) {
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-      const double o = __shfl_xor(top, d, kWave);
-      top = o > top || o != o ? o : top;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kPerLane; ++i) {
-    c[i] = 0.0;
-    if (i * kWave >= E) continue;
-    if (a.sigmoid) c[i] = sigmoid64(l[i]);
-    else if (top != -INFINITY) c[i] = exp(l[i] - top);
-    if (i * kWave + lane >= E) c[i] = 0.0;
-    total += c[i];
-  }
-  if (a.sigmoid) total = 1.0;
-  else total = wave_sum(total);
-  // (a row of -infinity alone: scores 0)
-  const bool none = !a.sigmoid && top == -INFINITY;
-  int64_t key[kPerLane];
-#pragma unroll
-  for (int i = 0; i < kPerLane; ++i) {
-    const int e = i * kWave + lane;
-    key[i] = kGone;
-    if (e >= E) continue;
-    c[i] = none ? 0.0 : c[i] / total;
-    if (a.bias) c[i] += (double)a.bias[e];
-    key[i] = order_of(a.bias ? c[i] : l[i]);
-    if (a.groups > 1) s_c[e] = c[i];
-  }
-  if (a.groups > 1) {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    const int per = E / a.groups;
-    int64_t rank = kGone;
-    if (lane < a.groups) {
-      int64_t k1 = kGone, k2 = kGone;
-      double v1 = 0.0, v2 = 0.0;
-      for (int i = 0; i < per; ++i) {
-        const double v = s_c[lane * per + i];
-        const int64_t k = order_of(v);
-        if (k > k1) {
-          k2 = k1, v2 = v1;
-          k1 = k, v1 = v;
-        } else if (k > k2) {
-          k2 = k, v2 = v;
-        }
-      }
-      rank = order_of(a.group_best == 2 ? v1 + v2 : v1);
-    }
-    uint64_t kept = 0;
-    for (int i = 0; i < a.top_groups; ++i) {
-      int64_t best = rank;
-      int at = lane;
-      wave_best(best, at);
-      kept |= 1ull << at;
-      if (lane == at) rank = kGone;
-    }
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      const int e = i * kWave + lane;
-      if (e < E && !(kept >> (e / per) & 1)) key[i] = kGone;
-    }
-  }
-  int mine = 0;        // lane j: the expert of slot j
-  double logit = 0.0;  // and its logit
-  for (int j = 0; j < a.k; ++j) {
-    int64_t best = kGone;
-    int at = INT32_MAX;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i * kWave + lane;
-      }
-    wave_best(best, at);
-    double v = 0.0;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i)
-      if (i * kWave + lane == at) {
-        key[i] = kGone;
-        v = l[i];
-      }
-    v = __shfl(v, at & (kWave - 1), kWave);
-    if (lane == j) {
-      mine = at;
-      logit = v;
-    }
-  }
-  // ---- the weights
-  const bool here = lane < a.k;
-  double w;
-  if (a.renorm) {
-    // sigmoid: both the score and the sum times exp(-shift), shift the largest
-    // chosen logit where that is negative
-    double shift = here ? logit : -INFINITY;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-      const double o = __shfl_xor(shift, d, kWave);
-      shift = o > shift || o != o ? o : shift;
-    }
-    const bool empty = shift == -INFINITY;
-    if (a.sigmoid) {
-      if (shift > 0.0) shift = 0.0;
-      w = logit > 0.0 ? 1.0 / (1.0 + exp(-logit)) * exp(-shift) : exp(logit - shift) / (1.0 + exp(logit));
-    } else {
-      w = exp(logit - shift);
-    }
-    if (!here || empty) w = 0.0;
-    const double sum = wave_sum(w);
-    w = empty ? 0.0 : w / sum;
-    if (total != total) w = total;
-  } else {
-    w = a.sigmoid ? sigmoid64(logit) : none ? 0.0 : exp(logit - top) / total;
-  }
-  if (here) {
-    a.idx[t * a.k + lane] = mine;
-    a.w[t * a.k + lane] = (float)w * a.scale;
-  }
-}
-
-// ---- float32
 
 // The exchange of step d within 16 lanes, after which each lane has the value
 // of another that held a different half (d = 0, 1: lanes 1 and 2 away; 2, 3:
@@ -246,6 +87,144 @@ __device__ __forceinline__ uint64_t token_bits(uint64_t ballot_bits, int lane) {
   return L == 64 ? ballot_bits : (ballot_bits >> (lane & ~(L - 1))) & ((1ull << (L & 63)) - 1);
 }
 
+// The wave's largest key, and of lanes that hold it the lowest index.
+__device__ __forceinline__ void wave_best(int64_t& key, int& at) {
+  const int hi = all_lanes<kWave>((int)(key >> 32), [](int a, int b) { return max(a, b); });
+  const uint32_t low = (int)(key >> 32) == hi ? (uint32_t)key : 0u;
+  const uint32_t lo = lanes_max<kWave>(low);
+  const bool mine = (int)(key >> 32) == hi && (uint32_t)key == lo;
+  at = all_lanes<kWave>(mine ? at : INT32_MAX, [](int a, int b) { return min(a, b); });
+  key = (int64_t)(((uint64_t)(uint32_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d, kWave);
+  return v;
+}
+// The largest, a NaN above all.
+__device__ __forceinline__ double wave_top(double v) {
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const double o = __shfl_xor(v, d, kWave);
+    v = o > v || o != o ? o : v;
+  }
+  return v;
+}
+
+__device__ __forceinline__ double sigmoid64(double l) {
+  const double e = exp(-fabs(l));
+  return (l < 0.0 ? e : 1.0) / (1.0 + e);
+}
+
+// One token by one wave, scores in float64.  s_c: E doubles of LDS, the lane's
+// experts e = lane, lane + 64, ...: held there and not in registers, which the
+// path that nearly every token takes would lack.
+__device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t t, int lane, double* s_c) {
+  const int E = a.E;
+  const int64_t row = t * E;
+  int64_t* const s_key = reinterpret_cast<int64_t*>(s_c);
+  double top = -INFINITY, total = 0.0;
+  if (!a.sigmoid) {
+#pragma unroll 1
+    for (int e = lane; e < E; e += kWave) {
+      const double l = (double)logit_at(a.logits, a.bf16, row + e);
+      top = l > top || l != l ? l : top;
+    }
+    top = wave_top(top);
+  }
+  // (a softmax's row of -infinity alone: scores 0)
+  const bool none = !a.sigmoid && top == -INFINITY;
+#pragma unroll 1
+  for (int e = lane; e < E; e += kWave) {
+    const double l = (double)logit_at(a.logits, a.bf16, row + e);
+    const double x = a.sigmoid ? sigmoid64(l) : none ? 0.0 : exp(l - top);
+    s_c[e] = x;
+    total += x;
+  }
+  total = a.sigmoid || none ? 1.0 : wave_sum(total);
+#pragma unroll 1
+  for (int e = lane; e < E; e += kWave) s_c[e] = s_c[e] / total + (a.bias ? (double)a.bias[e] : 0.0);
+  uint64_t kept = ~0ull;
+  const int per = E / a.groups;
+  if (a.groups > 1) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    int64_t rank = kGone;
+    if (lane < a.groups) {
+      int64_t k1 = kGone, k2 = kGone;
+      double v1 = 0.0, v2 = 0.0;
+      for (int i = 0; i < per; ++i) {
+        const double v = s_c[lane * per + i];
+        const int64_t k = order_of(v);
+        if (k > k1) {
+          k2 = k1, v2 = v1;
+          k1 = k, v1 = v;
+        } else if (k > k2) {
+          k2 = k, v2 = v;
+        }
+      }
+      rank = order_of(a.group_best == 2 ? v1 + v2 : v1);
+    }
+    kept = 0;
+    for (int i = 0; i < a.top_groups; ++i) {
+      int64_t best = rank;
+      int at = lane;
+      wave_best(best, at);
+      kept |= 1ull << at;
+      if (lane == at) rank = kGone;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+#pragma unroll 1
+  for (int e = lane; e < E; e += kWave)
+    s_key[e] = kept >> (a.groups > 1 ? e / per : 0) & 1
+                   ? order_of(a.bias ? s_c[e] : (double)logit_at(a.logits, a.bf16, row + e))
+                   : kGone;
+  int mine = 0;  // lane j: the expert of slot j
+  for (int j = 0; j < a.k; ++j) {
+    int64_t best = kGone;
+    int at = INT32_MAX;
+#pragma unroll 1
+    for (int e = lane; e < E; e += kWave) {
+      const int64_t k = s_key[e];
+      if (k > best) {
+        best = k;
+        at = e;
+      }
+    }
+    wave_best(best, at);
+    if (lane == (at & (kWave - 1))) s_key[at] = kGone;
+    if (lane == j) mine = at;
+  }
+  // ---- the weights
+  const bool here = lane < a.k;
+  const double logit = here ? (double)logit_at(a.logits, a.bf16, row + mine) : 0.0;
+  double w;
+  if (a.renorm) {
+    // sigmoid: both the score and the sum times exp(-shift), shift the largest
+    // chosen logit where that is negative
+    double shift = wave_top(here ? logit : -INFINITY);
+    const bool empty = shift == -INFINITY;
+    if (a.sigmoid) {
+      if (shift > 0.0) shift = 0.0;
+      w = logit > 0.0 ? 1.0 / (1.0 + exp(-logit)) * exp(-shift) : exp(logit - shift) / (1.0 + exp(logit));
+    } else {
+      w = exp(logit - shift);
+    }
+    if (!here || empty) w = 0.0;
+    const double sum = wave_sum(w);
+    w = empty ? 0.0 : w / sum;
+    if (total != total) w = total;
+  } else {
+    w = a.sigmoid ? sigmoid64(logit) : none ? 0.0 : exp(logit - top) / total;
+  }
+  if (here) {
+    a.idx[t * a.k + lane] = mine;
+    a.w[t * a.k + lane] = (float)w * a.scale;
+  }
+}
+
+// ---- float32
+
 // 31 bits that order as v does; zero is below all of them.  No NaN, no -0.
 __device__ __forceinline__ uint32_t key_of(float v) {
   const int b = __float_as_int(v);
@@ -259,11 +238,10 @@ struct RouteShape {
   static constexpr int kScores = L * NV + kMaxGroups;   // floats of LDS for a token: scores, a place between groups
   static constexpr int kFloats = kTokens * (kScores + kMaxGroups);
   static constexpr int kLds = kFloats * 4 > L * NV * 8 ? kFloats * 4 : L * NV * 8;  // (and the exact path's scores)
-  static constexpr int kExact = (L * NV + kWave - 1) / kWave;
 };
 
 template <int L, int NV, bool BF16>
-__global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(RouteArgs a) {
+__global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(RouteArgs a, int first) {
   using S = RouteShape<L, NV, BF16>;
   __shared__ __attribute__((aligned(16))) uint8_t s_all[kRouteWaves][S::kLds];
   const int lane = lane_id(), wave = wave_in_group();
@@ -275,128 +253,142 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(RouteArgs a)
   float* const s_c = reinterpret_cast<float*>(s_all[wave]) + token * (S::kScores + kMaxGroups);
   float* const s_rank = s_c + S::kScores;
 
-  const int64_t step = (int64_t)gridDim.x * kRouteWaves * S::kTokens;
-  for (int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * S::kTokens; t0 < a.T; t0 += step) {
-    const int64_t t = t0 + token;
-    const bool held = t < a.T;
-    const int64_t row = (held ? t : t0) * E;
-    // ---- the lane's logits; an absent one counts as -infinity
-    float l[NV];
-    const int e0 = sub * NV;
-    if (vectors) {
-      constexpr int kPer = BF16 ? 8 : 4;
+  const int64_t t0 = first + ((int64_t)blockIdx.x * kRouteWaves + wave) * S::kTokens;
+  if (t0 >= a.T) return;
+  const int64_t t = t0 + token;
+  const bool held = t < a.T;
+  const int64_t row = (held ? t : t0) * E;
+  // ---- the lane's logits; an absent one counts as -infinity
+  float l[NV];
+  const int e0 = sub * NV;
+  if (vectors) {
+    constexpr int kPer = BF16 ? 8 : 4;
 #pragma unroll
-      for (int i = 0; i < NV; i += kPer) {
-        u32x4 v = {0u, 0u, 0u, 0u};
-        const bool in = e0 + i < E;
-        if (NV < kPer) {
-          // (four bf16 values a lane)
-          uint2 h = make_uint2(0u, 0u);
-          if (in) h = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + row + e0 + i);
-          v[0] = h.x, v[1] = h.y;
-        } else if (in) {
-          v = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.logits) + (row + e0 + i) * (BF16 ? 2 : 4));
-        }
-#pragma unroll
-        for (int q = 0; q < (NV < kPer ? NV : kPer); ++q) {
-          const float x = BF16 ? (q & 1 ? bf16_hi(v[q / 2]) : bf16_lo(v[q / 2])) : __uint_as_float(v[q & 3]);
-          l[i + q] = in ? x : -INFINITY;
-        }
+    for (int i = 0; i < NV; i += kPer) {
+      u32x4 v = {0u, 0u, 0u, 0u};
+      const bool in = e0 + i < E;
+      if (NV < kPer) {
+        // (four bf16 values a lane)
+        uint2 h = make_uint2(0u, 0u);
+        if (in) h = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + row + e0 + i);
+        v[0] = h.x, v[1] = h.y;
+      } else if (in) {
+        v = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.logits) + (row + e0 + i) * (BF16 ? 2 : 4));
       }
-    } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) l[i] = e0 + i < E ? logit_at(a.logits, BF16, row + e0 + i) : -INFINITY;
-    }
-    // ---- scores and keys
-    bool again = false;  // float32 does not decide this token
-    float top = 0.0f, inv = 0.0f;
-    if (sums) {
-      top = l[0];
-#pragma unroll
-      for (int i = 1; i < NV; ++i) top = fmaxf(top, l[i]);
-      top = lanes_max<L>(top);
-      float total = 0.0f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) total += exp_fast(l[i] - top);  // (a NaN, +infinity, or nothing else than -infinity: NaN)
-      total = lanes_sum<L>(total);
-      again = total != total;
-      inv = 1.0f / total;
-    }
-    // What the scores may be off by, twice.  Sigmoid: exp's argument loses 1.5 |l|
-    // half steps, of which its slope leaves 0.34, and four are added by exp, sum
-    // and reciprocal: 2^-22.  Softmax: the sum's roundings, NV and a few half
-    // steps, relative to scores of at most 1 / total, and 2^-24 by exp.
-    const float score_error = !scores ? 0.0f : a.sigmoid ? 0x1p-20f : inv * (NV + 10) * 0x1p-23f + 0x1p-22f;
-    uint32_t key[NV];
-    float probe = 0.0f;  // NaN if any is
-    float c[NV];
-    if (scores) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        c[i] = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + exp_fast(-l[i])) : exp_fast(l[i] - top) * inv;
-        if (a.bias && e0 + i < E) c[i] += a.bias[e0 + i];
+      for (int q = 0; q < (NV < kPer ? NV : kPer); ++q) {
+        const float x = BF16 ? (q & 1 ? bf16_hi(v[q / 2]) : bf16_lo(v[q / 2])) : __uint_as_float(v[q & 3]);
+        l[i + q] = in ? x : -INFINITY;
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) c[i] = l[i] + 0.0f;
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) l[i] = e0 + i < E ? logit_at(a.logits, BF16, row + e0 + i) : -INFINITY;
+  }
+  // ---- scores and keys
+  bool again = false;  // float32 does not decide this token
+  float top = 0.0f, inv = 0.0f;
+  if (sums) {
+    top = l[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) top = fmaxf(top, l[i]);
+    top = lanes_max<L>(top);
+    float total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) total += exp_fast(l[i] - top);  // (a NaN, +infinity, or nothing else than -infinity: NaN)
+    total = lanes_sum<L>(total);
+    again = total != total;
+    inv = 1.0f / total;
+  }
+  // What the scores may be off by, twice.  Sigmoid: exp's argument loses 1.5 |l|
+  // half steps, of which its slope leaves 0.34, and four are added by exp, sum
+  // and reciprocal: 2^-22.  Softmax: the sum's roundings, NV and a few half
+  // steps, relative to scores of at most 1 / total, and 2^-24 by exp.
+  const float score_error = !scores ? 0.0f : a.sigmoid ? 0x1p-20f : inv * (NV + 10) * 0x1p-23f + 0x1p-22f;
+  uint32_t key[NV];
+  float probe = 0.0f;  // NaN if any is
+  float c[NV];
+  if (scores) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (e0 + i < E) probe += c[i];
-      key[i] = e0 + i < E ? (key_of(c[i]) & ~(uint32_t)(NV - 1)) | (uint32_t)(NV - 1 - i) : 0u;
+      c[i] = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + exp_fast(-l[i])) : exp_fast(l[i] - top) * inv;
     }
-    probe = lanes_sum<L>(probe);
-    again |= probe != probe;
-    // ---- the best groups
-    if (a.groups > 1) {
-      const int per = E / a.groups;
-      const uint32_t over = ((1u << 20) + per - 1) / per;  // e / per = e * over >> 20 for e < 1024
+    if (a.bias) {
+      if (E % 4 == 0 && ((uintptr_t)a.bias & 15) == 0) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const uint32_t e = e0 + i;
-        if ((int)e < E) s_c[e + (e * over >> 20)] = c[i];  // (a place between the groups: other banks)
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      for (int g = sub; g < a.groups; g += L) {
-        float v1 = -INFINITY, v2 = -INFINITY;
-        const float* p = s_c + g * (per + 1);
-        for (int i = 0; i < per; ++i) {
-          const float v = p[i];
-          v2 = fmaxf(v2, fminf(v1, v));
-          v1 = fmaxf(v1, v);
+        for (int i = 0; i < NV; i += 4) {
+          float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (e0 + i < E) b = *reinterpret_cast<const float4*>(a.bias + e0 + i);
+          c[i] += b.x, c[i + 1] += b.y, c[i + 2] += b.z, c[i + 3] += b.w;
         }
-        s_rank[g] = a.group_best == 2 ? v1 + v2 : v1;
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      uint64_t kept = 0;
-      float worst = INFINITY, next = -INFINITY;  // of the groups kept, and the best of the others
-      for (int g0 = 0; g0 < a.groups; g0 += L) {
-        const int g = g0 + sub;
-        const float mine = g < a.groups ? s_rank[g] : -INFINITY;
-        int before = g < a.groups ? 0 : kMaxGroups;
-        for (int o = 0; o < a.groups; ++o) {
-          const float r = s_rank[o];
-          before += r > mine || (r == mine && o < g);
-        }
-        const bool keep = before < a.top_groups;
-        if (keep) worst = fminf(worst, mine);
-        else next = fmaxf(next, mine);
-        kept |= token_bits<L>(ballot(keep), lane) << g0;
-      }
-      worst = -lanes_max<L>(-worst);
-      next = lanes_max<L>(next);
-      // (sums of two: twice the scores' error, and their own rounding)
-      again |= a.top_groups < a.groups && !(worst - next > 2.0f * score_error + 0x1p-21f * fmaxf(fabsf(worst), fabsf(next)));
+      } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const uint32_t e = e0 + i;
-        if (!(kept >> (e * over >> 20 & 63) & 1)) key[i] = 0u;
+        for (int i = 0; i < NV; ++i)
+          if (e0 + i < E) c[i] += a.bias[e0 + i];
       }
     }
-    // ---- the choice: slot j in lane j, and the best that is left in lane k
-    uint32_t last = 1u << 31;
-    int32_t* const s_slot = reinterpret_cast<int32_t*>(s_rank);
-    for (int j = 0; j <= a.k; ++j) {
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) c[i] = l[i] + 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (e0 + i < E) probe += c[i];
+    key[i] = e0 + i < E ? (key_of(c[i]) & ~(uint32_t)(NV - 1)) | (uint32_t)(NV - 1 - i) : 0u;
+  }
+  probe = lanes_sum<L>(probe);
+  again |= probe != probe;
+  // ---- the best groups
+  if (a.groups > 1) {
+    const int per = E / a.groups;
+    const uint32_t over = ((1u << 20) + per - 1) / per;  // e / per = e * over >> 20 for e < 1024
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t e = e0 + i;
+      if ((int)e < E) s_c[e + (e * over >> 20)] = c[i];  // (a place between the groups: other banks)
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    for (int g = sub; g < a.groups; g += L) {
+      float v1 = -INFINITY, v2 = -INFINITY;
+      const float* p = s_c + g * (per + 1);
+      for (int i = 0; i < per; ++i) {
+        const float v = p[i];
+        v2 = fmaxf(v2, fminf(v1, v));
+        v1 = fmaxf(v1, v);
+      }
+      s_rank[g] = a.group_best == 2 ? v1 + v2 : v1;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    uint64_t kept = 0;
+    float worst = INFINITY, next = -INFINITY;  // of the groups kept, and the best of the others
+    for (int g0 = 0; g0 < a.groups; g0 += L) {
+      const int g = g0 + sub;
+      const float mine = g < a.groups ? s_rank[g] : -INFINITY;
+      int before = g < a.groups ? 0 : kMaxGroups;
+      for (int o = 0; o < a.groups; ++o) {
+        const float r = s_rank[o];
+        before += r > mine || (r == mine && o < g);
+      }
+      const bool keep = before < a.top_groups;
+      if (keep) worst = fminf(worst, mine);
+      else next = fmaxf(next, mine);
+      kept |= token_bits<L>(ballot(keep), lane) << g0;
+    }
+    worst = -lanes_max<L>(-worst);
+    next = lanes_max<L>(next);
+    // (sums of two: twice the scores' error, and their own rounding)
+    again |= a.top_groups < a.groups && !(worst - next > 2.0f * score_error + 0x1p-21f * fmaxf(fabsf(worst), fabsf(next)));
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t e = e0 + i;
+      if (!(kept >> (e * over >> 20 & 63) & 1)) key[i] = 0u;
+    }
+  }
+  // ---- the choice: slot j in lane j, and the best that is left in lane k
+  uint32_t last = 1u << 31;
+  int32_t* const s_slot = reinterpret_cast<int32_t*>(s_rank);
+  auto choose = [&](int j0, int j1) {
+    for (int j = j0; j < j1; ++j) {
       uint32_t most = key[0] - last;
 #pragma unroll
       for (int i = 1; i < NV; ++i) most = max(most, key[i] - last);
@@ -409,57 +401,83 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(RouteArgs a)
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    const int mine = sub <= a.k ? s_slot[sub] : -1;
-    // ---- its weights, and whether the order is certain
-    const bool here = sub < a.k;
-    const float lj = mine >= 0 ? logit_at(a.logits, BF16, row + mine) : -INFINITY;
-    const float bj = mine >= 0 && a.bias ? a.bias[mine] : 0.0f;
-    float sj = 0.0f;
-    {
-      float cj = lj;
-      if (scores) {
-        cj = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + exp_fast(-lj)) : exp_fast(lj - top) * inv;
-        cj += bj;
-      }
-      const int up = sub + 1 < L ? lane + 1 : lane;
-      const float cn = __shfl(cj, up, kWave), ln = __shfl(lj, up, kWave), bn = __shfl(bj, up, kWave);
-      const int en = __shfl(mine, up, kWave);
-      const float scale = fmaxf(fabsf(cj), fabsf(cn));
-      // a key's cell is 2 NV steps of float32, the sums' roundings two
-      const float margin = scale * (2.0f * NV + 2.0f) * 0x1p-23f + score_error;
-      const bool clear = !here || en < 0 || (lj == ln && bj == bn) || (cn == -INFINITY && cj > cn) || cj - cn > margin;
-      again |= token_bits<L>(ballot(!clear), lane) != 0;
+  };
+  int mine = -1;
+  float lj = -INFINITY, bj = 0.0f;
+  // The lane's slot of `slots`; bit j: slot j is certainly before slot j + 1,
+  // and, from the choice's last slot on, before all that follow.  (Equal ones
+  // are in their order, but what follows them may lie in their cell above them.)
+  auto certain = [&](int slots) -> uint64_t {
+    mine = sub < slots ? s_slot[sub] : -1;
+    lj = mine >= 0 ? logit_at(a.logits, BF16, row + mine) : -INFINITY;
+    bj = mine >= 0 && a.bias ? a.bias[mine] : 0.0f;
+    float cj = lj;
+    if (scores) {
+      cj = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + exp_fast(-lj)) : exp_fast(lj - top) * inv;
+      cj += bj;
     }
-    const float most = lanes_max<L>(here ? lj : -INFINITY);
-    again |= !(fabsf(most) < INFINITY);
-    if (a.renorm) {
-      if (a.sigmoid) {
-        const float shift = fminf(most, 0.0f);
-        sj = lj > 0.0f ? expf(-shift) / (1.0f + expf(-lj)) : expf(lj - shift) / (1.0f + expf(lj));
-      } else {
-        sj = expf(lj - most);
-      }
-      if (!here) sj = 0.0f;
-      sj /= lanes_sum<L>(sj);
-    } else if (a.sigmoid) {
-      const float x = expf(-fabsf(lj));
-      sj = (lj < 0.0f ? x : 1.0f) / (1.0f + x);
+    const int up = sub + 1 < L ? lane + 1 : lane;
+    const float cn = __shfl(cj, up, kWave), ln = __shfl(lj, up, kWave), bn = __shfl(bj, up, kWave);
+    const int en = __shfl(mine, up, kWave);
+    // a key's cell is 2 NV steps of float32, the sums' roundings two
+    const float margin = fmaxf(fabsf(cj), fabsf(cn)) * (2.0f * NV + 2.0f) * 0x1p-23f + score_error;
+    const bool clear = en < 0 || (sub < a.k - 1 && lj == ln && bj == bn) || (cn == -INFINITY && cj > cn) || cj - cn > margin;
+    return token_bits<L>(ballot(clear), lane);
+  };
+  choose(0, a.k + 1);
+  const uint64_t inside = (1ull << a.k) - 1;
+  uint64_t sure = certain(a.k + 1);
+  int place = sub;  // of the lane's slot in the choice
+  // (the keys hold a bf16 logit whole: their order is the choice)
+  if (BF16 && !scores) sure = inside;
+  again |= (scores && !a.sigmoid) && (sure & inside) != inside;
+  if (ballot((sure & inside) != inside && !again)) {
+    // A few more, up to a certain gap: what lies before it holds the choice, and is ranked in float64.
+    const int slots = min(L, a.k + 1 + 4);
+    choose(a.k + 1, slots);
+    sure = certain(slots) >> (a.k - 1);
+    const int before = a.k + (sure ? __builtin_ctzll(sure) : L);
+    again |= before >= slots;
+    const double x = !scores ? (double)lj : sigmoid64((double)lj) + (double)bj;
+    const bool in = sub < before;
+    place = in ? 0 : L;
+    for (int i = 0; i < slots; ++i) {
+      const double o = __shfl(x, (lane & ~(L - 1)) + i, kWave);
+      const int e = __shfl(mine, (lane & ~(L - 1)) + i, kWave);
+      if (in && i < before) place += o > x || (o == x && e < mine);
+    }
+  }
+  // ---- its weights
+  const bool here = place < a.k;
+  const float most = lanes_max<L>(here ? lj : -INFINITY);
+  again |= !(fabsf(most) < INFINITY);
+  float sj;
+  if (a.renorm) {
+    if (a.sigmoid) {
+      const float shift = fminf(most, 0.0f);
+      sj = lj > 0.0f ? expf(-shift) / (1.0f + expf(-lj)) : expf(lj - shift) / (1.0f + expf(lj));
     } else {
-      sj = expf(lj - top) * inv;
+      sj = expf(lj - most);
     }
-    if (held && here && !again) {
-      a.idx[t * a.k + sub] = mine;
-      a.w[t * a.k + sub] = sj * a.scale;
-    }
-    // ---- the tokens that are left
-    uint64_t left = ballot(held && sub == 0 && again);
-    while (left) {
-      const int at = __builtin_ctzll(left);
-      left &= left - 1;
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      route_exact<S::kExact>(a, t0 + at / L, lane, reinterpret_cast<double*>(s_all[wave]));
-    }
+    if (!here) sj = 0.0f;
+    sj /= lanes_sum<L>(sj);
+  } else if (a.sigmoid) {
+    const float x = expf(-fabsf(lj));
+    sj = (lj < 0.0f ? x : 1.0f) / (1.0f + x);
+  } else {
+    sj = expf(lj - top) * inv;
+  }
+  if (held && here && !again) {
+    a.idx[t * a.k + place] = mine;
+    a.w[t * a.k + place] = sj * a.scale;
+  }
+  // ---- the tokens that are left
+  uint64_t left = ballot(held && sub == 0 && again);
+  while (left) {
+    const int at = __builtin_ctzll(left);
+    left &= left - 1;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    route_exact(a, t0 + at / L, lane, reinterpret_cast<double*>(s_all[wave]));
   }
 }
 
@@ -549,11 +567,16 @@ namespace {
 
 template <int L, int NV>
 hipError_t launch_shape(const RouteArgs& a, hipStream_t stream) {
-  const int64_t groups = ((int64_t)a.T + kRouteWaves * (kWave / L) - 1) / (kRouteWaves * (kWave / L));
-  const dim3 grid((uint32_t)(groups < kRouteGroups ? groups : kRouteGroups)), block(kRouteWaves * kWave);
-  if (a.bf16) hipLaunchKernelGGL((route_kernel<L, NV, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((route_kernel<L, NV, false>), grid, block, 0, stream, a);
-  return hipGetLastError();
+  constexpr int kEach = kRouteWaves * (kWave / L);  // tokens of a workgroup
+  for (int64_t first = 0; first < a.T; first += kRouteGroups * kEach) {
+    const int64_t groups = (a.T - first + kEach - 1) / kEach;
+    const dim3 grid((uint32_t)(groups < kRouteGroups ? groups : kRouteGroups)), block(kRouteWaves * kWave);
+    if (a.bf16) hipLaunchKernelGGL((route_kernel<L, NV, true>), grid, block, 0, stream, a, (int)first);
+    else hipLaunchKernelGGL((route_kernel<L, NV, false>), grid, block, 0, stream, a, (int)first);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
