@@ -805,11 +805,11 @@ hipError_t launch_act(const Budget& b, const LinearArgs& g, const LinearShape& s
 }  // namespace
 
 size_t linear_workspace(int64_t rows, int K, int E, int N, int) {
-  const LinearShape s = linear_shape(rows, E, N, K);
+  const LinearShape s = linear_shape(rows, E, N, K, rows * N);
   return s.splits > 1 ? (size_t)s.splits * rows * N * 4 : 0;
 }
 size_t dgrad_workspace(int64_t rows, int K, int E, int N) {
-  const LinearShape s = linear_shape(rows, E, K, N);
+  const LinearShape s = linear_shape(rows, E, K, N, rows * K);
   return s.splits > 1 ? (size_t)s.splits * rows * K * 4 : 0;
 }
 size_t wgrad_workspace(int64_t rows, int K, int E, int N) {
@@ -818,10 +818,10 @@ size_t wgrad_workspace(int64_t rows, int K, int E, int N) {
 }
 
 hipError_t launch_linear(const Budget& b, const LinearArgs& g, hipStream_t stream) {
-  return launch_act<kForward>(b, g, linear_shape(g.rows, g.E, g.N, g.K), stream);
+  return launch_act<kForward>(b, g, linear_shape(g.rows, g.E, g.N, g.K, g.rows * g.N), stream);
 }
 hipError_t launch_dgrad(const Budget& b, const LinearArgs& g, hipStream_t stream) {
-  return launch_act<kDgrad>(b, g, linear_shape(g.rows, g.E, g.K, g.N), stream);
+  return launch_act<kDgrad>(b, g, linear_shape(g.rows, g.E, g.K, g.N, g.rows * g.K), stream);
 }
 hipError_t launch_wgrad(const Budget& b, const LinearArgs& g, hipStream_t stream) {
   return launch<kWgrad, EP_ACT_NONE>(b, g, wgrad_shape(g.rows, g.E, g.N, g.K), stream);
