@@ -183,12 +183,16 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   const int xcd = blockIdx.x % kXcds;
   const int slot = blockIdx.x / kXcds;
   int round = 0;
-  // Forward and dgrad: a run of items for each XCD, whose tiles share weights.
-  // wgrad, where an item's cost goes by its expert's rows: every XCD takes as
-  // many items as it has workgroups in turn.
+  // Tiles of 256 rows: every XCD takes as many items as it has workgroups in
+  // turn, so that what neighbouring items share passes by all of them within a
+  // round (and wgrad's items, whose cost goes by their expert's rows, are spread
+  // evenly).  Tiles of 128, which mostly read weights: a run of items for each
+  // XCD.  us, in turn / runs: gate and up product of 49152 rows 2615 / 2695, the
+  // down product's gradient 1500 / 1535, a decode batch's down product (128)
+  // 1244 / 1222.
   const int run = (total + kXcds - 1) / kXcds;
   auto item_no = [&](int r) {
-    if constexpr (P == kWgrad) return (r * kXcds + xcd) * slots + slot;
+    if constexpr (P == kWgrad || BM == 256) return (r * kXcds + xcd) * slots + slot;
     const int i = slot + r * slots;
     return i < run ? xcd * run + i : total;
   };
@@ -566,6 +570,17 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
       };
       constexpr int kLast = pair ? HT : NT;
       const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
+      // (a pair's values are asked for before the results of the pair before it
+      // are stored: what is loaded behind stores waits for them)
+      u32x4 v[2][MT];
+      auto ask = [&](int n) {
+        const int c8 = cur.c0 + (n < HT ? 0 : kHalf) + column8(n);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          v[n / 2 % 2][m] = f->residual ? __builtin_amdgcn_raw_buffer_load_b128(res, offset(m, outs, c8, outs, 2), 0, 0)
+                                        : u32x4{0u, 0u, 0u, 0u};
+      };
+      ask(0);
 #pragma unroll
       for (int n = 0; n < kLast; n += 2) {
         const int c = cur.c0 + (n < HT ? 0 : kHalf), c4 = c + column4(n), c8 = c + column8(n);
@@ -577,14 +592,7 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
             if constexpr (pair) add_up[i] = bias4(c4 + i * 16 + outs);
           }
         }
-        u32x4 v[MT];
-        if (f->residual) {
-#pragma unroll
-          for (int m = 0; m < MT; ++m) v[m] = __builtin_amdgcn_raw_buffer_load_b128(res, offset(m, outs, c8, outs, 2), 0, 0);
-        } else {
-#pragma unroll
-          for (int m = 0; m < MT; ++m) v[m] = u32x4{0u, 0u, 0u, 0u};
-        }
+        if (n + 2 < kLast) ask(n + 2);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           f32x4 z[2], up[2], r[2];
@@ -598,7 +606,7 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
             put8(pre, at, z[0], z[1]);
             if constexpr (pair) put8(pre, at + outs * 2, up[0], up[1]);
           }
-          get8(v[m], r[0], r[1]);
+          get8(v[n / 2 % 2][m], r[0], r[1]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             z[i] = activate4<ACT>(z[i]);
@@ -618,25 +626,32 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
       const int wide = ACT == EP_ACT_SWIGLU ? 2 * outs : outs;
       const auto to = rows_of(f->out, cur.r0, wide, 2);
       const auto pre = rows_of(f->pre_in, cur.r0, wide, 2);
+      // (a pair's values are asked for before the results of the pair before it
+      // are stored: what is loaded behind stores waits for them)
+      u32x4 v[2][MT], u[2][MT];
+      auto ask = [&](int n) {
+        const int c8 = cur.c0 + (n < HT ? 0 : kHalf) + column8(n);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const uint32_t at = offset(m, wide, c8, outs, 2);
+          v[n / 2 % 2][m] = __builtin_amdgcn_raw_buffer_load_b128(pre, at, 0, 0);
+          if constexpr (ACT == EP_ACT_SWIGLU) u[n / 2 % 2][m] = __builtin_amdgcn_raw_buffer_load_b128(pre, at + outs * 2, 0, 0);
+        }
+      };
+      if constexpr (ACT != EP_ACT_NONE) ask(0);
 #pragma unroll
       for (int n = 0; n < NT; n += 2) {
         const int c8 = cur.c0 + (n < HT ? 0 : kHalf) + column8(n);
-        u32x4 v[MT], u[MT];
-        if constexpr (ACT != EP_ACT_NONE) {
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const uint32_t at = offset(m, wide, c8, outs, 2);
-            v[m] = __builtin_amdgcn_raw_buffer_load_b128(pre, at, 0, 0);
-            if constexpr (ACT == EP_ACT_SWIGLU) u[m] = __builtin_amdgcn_raw_buffer_load_b128(pre, at + outs * 2, 0, 0);
-          }
-        }
+        if constexpr (ACT != EP_ACT_NONE)
+          if (n + 2 < NT) ask(n + 2);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const uint32_t at = offset(m, wide, c8, outs, 2);
           f32x4 z[2], up[2];
-          if constexpr (ACT != EP_ACT_NONE) get8(v[m], z[0], z[1]);
+          if constexpr (ACT != EP_ACT_NONE) get8(v[n / 2 % 2][m], z[0], z[1]);
           if constexpr (ACT == EP_ACT_SWIGLU) {
-            get8(u[m], up[0], up[1]);
+            get8(u[n / 2 % 2][m], up[0], up[1]);
             put8(to, at, slope4<ACT>(z[0]) * up[0] * acc[n][m], slope4<ACT>(z[1]) * up[1] * acc[n + 1][m]);
             put8(to, at + outs * 2, activate4<ACT>(z[0]) * acc[n][m], activate4<ACT>(z[1]) * acc[n + 1][m]);
           } else if constexpr (ACT != EP_ACT_NONE) {
@@ -645,6 +660,7 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
             put8(to, at, acc[n][m], acc[n + 1][m]);
           }
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     if constexpr (P == kWgrad) {
