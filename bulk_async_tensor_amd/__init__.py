@@ -81,7 +81,7 @@ _SIGNATURES = {
                           _p, _p]),
     "ep_route_backward": (_c_int, [_p, _c_int, _c_int, _c_int, _c_int, _p, _c_int, _c_int, _c_f32, _p, _p, _c_int,
                                    _p]),
-    "ep_grouped_linear_workspace_bytes": (_c_sz, [_c_i64, _c_int, _c_int, _c_int, _c_int]),
+    "ep_grouped_linear_workspace_bytes": (_c_sz, [_c_i64, _c_int, _c_int, _c_int]),
     "ep_grouped_linear": (_c_int, [_p, _c_i64, _c_int, _p, _c_int, _p, _p, _c_int, _c_int, _p, _p, _c_int, _p, _p,
                                    _c_sz, _p]),
     "ep_grouped_linear_dgrad_workspace_bytes": (_c_sz, [_c_i64, _c_int, _c_int, _c_int]),
@@ -693,8 +693,8 @@ def _weight_of(th, what, name, w, offsets, devices):
     return E, N, K, offsets.data_ptr()
 
 
-def ep_grouped_linear_workspace_bytes(rows, K, E, N, act="none"):
-    return lib().ep_grouped_linear_workspace_bytes(int(rows), int(K), int(E), int(N), _one_of(_ACTS, act, "act"))
+def ep_grouped_linear_workspace_bytes(rows, K, E, N):
+    return lib().ep_grouped_linear_workspace_bytes(int(rows), int(K), int(E), int(N))
 
 
 def ep_grouped_linear_dgrad_workspace_bytes(rows, K, E, N):
@@ -763,7 +763,7 @@ def ep_grouped_linear(a, offsets, b, y, bias=None, act="none", residual=None, pr
         if pre.shape != (rows, N):
             raise ValueError(f"{what}: pre must be [{rows}, {N}]")
         pp = pre.data_ptr()
-    _with_workspace(th, what, _lib.ep_grouped_linear_workspace_bytes(rows, K, E, N, code), workspace, a, devices, stream,
+    _with_workspace(th, what, _lib.ep_grouped_linear_workspace_bytes(rows, K, E, N), workspace, a, devices, stream,
                     (a.data_ptr(), rows, K, off, E, b.data_ptr(), bp, N, code, rp, y.data_ptr(), kind, pp))
     return y
 

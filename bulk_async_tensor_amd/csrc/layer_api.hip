@@ -51,7 +51,9 @@ int check_product(const char* what, int64_t rows, int N, int K, int E, const voi
   return EP_OK;
 }
 
-int check_workspace(const char* what, size_t need, const void* workspace, size_t bytes) {
+int check_needs(const char* what, const ep::LinearNeeds& needs, const void* workspace, size_t bytes) {
+  if (!needs.fits) return fail(EP_ERR_INVALID_ARG, "%s: more than 2^30 tiles of results", what);
+  const size_t need = needs.workspace;
   if (need == 0) return EP_OK;
   if (!workspace || bytes < need)
     return fail(EP_ERR_WORKSPACE, "%s: a workspace of %zu bytes is needed, %zu given", what, need,
@@ -121,14 +123,14 @@ int ep_route_backward(const void* logits, int logits_type, int T, int E, int sco
   return run("ep_route_backward launch", a, ep::launch_route_backward, stream);
 }
 
-size_t ep_grouped_linear_workspace_bytes(int64_t rows, int K, int E, int N, int act) {
-  return sizes_fit(rows, K, E, N) ? ep::linear_workspace(rows, K, E, N, act) : 0;
+size_t ep_grouped_linear_workspace_bytes(int64_t rows, int K, int E, int N) {
+  return sizes_fit(rows, K, E, N) ? ep::linear_needs(rows, K, E, N).workspace : 0;
 }
 size_t ep_grouped_linear_dgrad_workspace_bytes(int64_t rows, int K, int E, int N) {
-  return sizes_fit(rows, K, E, N) ? ep::dgrad_workspace(rows, K, E, N) : 0;
+  return sizes_fit(rows, K, E, N) ? ep::dgrad_needs(rows, K, E, N).workspace : 0;
 }
 size_t ep_grouped_linear_wgrad_workspace_bytes(int64_t rows, int K, int E, int N) {
-  return sizes_fit(rows, K, E, N) ? ep::wgrad_workspace(rows, K, E, N) : 0;
+  return sizes_fit(rows, K, E, N) ? ep::wgrad_needs(rows, K, E, N).workspace : 0;
 }
 
 int ep_grouped_linear(const void* a, int64_t rows, int K, const int32_t* offsets, int E, const void* b,
@@ -145,7 +147,7 @@ int ep_grouped_linear(const void* a, int64_t rows, int K, const int32_t* offsets
     return fail(EP_ERR_ALIGNMENT, "%s: a tensor not 16-byte aligned", what);
   if (!aligned(bias, 4)) return fail(EP_ERR_ALIGNMENT, "%s: bias not 4-byte aligned", what);
   if (rows == 0) return EP_OK;
-  rc = check_workspace(what, ep::linear_workspace(rows, K, E, N, act), workspace, workspace_bytes);
+  rc = check_needs(what, ep::linear_needs(rows, K, E, N), workspace, workspace_bytes);
   if (rc) return rc;
   ep::LinearArgs g = {};
   g.rows_in = a, g.cols_in = b, g.rows = rows, g.N = N, g.K = K, g.offsets = offsets, g.E = E, g.act = act;
@@ -166,7 +168,7 @@ int ep_grouped_linear_dgrad(const void* dy, int64_t rows, int N, const int32_t* 
   if (!aligned(dy, 16) || !aligned(b, 16) || !aligned(pre, 16) || !aligned(dx, 16))
     return fail(EP_ERR_ALIGNMENT, "%s: a tensor not 16-byte aligned", what);
   if (rows == 0) return EP_OK;
-  rc = check_workspace(what, ep::dgrad_workspace(rows, K, E, N), workspace, workspace_bytes);
+  rc = check_needs(what, ep::dgrad_needs(rows, K, E, N), workspace, workspace_bytes);
   if (rc) return rc;
   ep::LinearArgs g = {};
   g.rows_in = dy, g.cols_in = b, g.rows = rows, g.N = N, g.K = K, g.offsets = offsets, g.E = E, g.act = act;
@@ -185,7 +187,7 @@ int ep_grouped_linear_wgrad(const void* dy, const void* a, int64_t rows, int N, 
   if (!aligned(dy, 16) || !aligned(a, 16) || !aligned(db, 16))
     return fail(EP_ERR_ALIGNMENT, "%s: a tensor not 16-byte aligned", what);
   if (!aligned(dbias, 4)) return fail(EP_ERR_ALIGNMENT, "%s: dbias not 4-byte aligned", what);
-  rc = check_workspace(what, ep::wgrad_workspace(rows, K, E, N), workspace, workspace_bytes);
+  rc = check_needs(what, ep::wgrad_needs(rows, K, E, N), workspace, workspace_bytes);
   if (rc) return rc;
   ep::LinearArgs g = {};
   g.rows_in = dy, g.cols_in = a, g.rows = rows, g.N = N, g.K = K, g.offsets = offsets, g.E = E;

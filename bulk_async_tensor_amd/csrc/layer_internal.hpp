@@ -33,9 +33,7 @@ struct RouteBackwardArgs {
 };
 hipError_t launch_route_backward(const Budget& b, const RouteBackwardArgs& a, hipStream_t stream);
 
-// ---- linear.hip: one product of the three, as it is cut into tiles.  A tile
-// is some rows of the "row side" (token rows; wgrad: weight rows n) times some
-// of the "column side", along which results lie in memory.
+// ---- linear_wide.hip: one product of the three
 struct LinearArgs {
   const void* rows_in;  // a or dy, [rows, ...]
   const void* cols_in;  // b, or wgrad's a
@@ -53,9 +51,13 @@ struct LinearArgs {
   float* dbias;
   float* partial;  // the workspace
 };
-size_t linear_workspace(int64_t rows, int K, int E, int N, int act);
-size_t dgrad_workspace(int64_t rows, int K, int E, int N);
-size_t wgrad_workspace(int64_t rows, int K, int E, int N);
+struct LinearNeeds {
+  size_t workspace;
+  bool fits;  // no more tiles than a launch counts
+};
+LinearNeeds linear_needs(int64_t rows, int K, int E, int N);
+LinearNeeds dgrad_needs(int64_t rows, int K, int E, int N);
+LinearNeeds wgrad_needs(int64_t rows, int K, int E, int N);
 hipError_t launch_linear(const Budget& b, const LinearArgs& g, hipStream_t stream);
 hipError_t launch_dgrad(const Budget& b, const LinearArgs& g, hipStream_t stream);
 hipError_t launch_wgrad(const Budget& b, const LinearArgs& g, hipStream_t stream);

@@ -8,6 +8,7 @@ namespace ep {
 
 constexpr int kLinearCols = 256, kLinearDeep = 64;  // a tile's columns, and places along the sum in a step
 constexpr int kLinearCus = 256;                     // compute units that a call's work is cut for
+constexpr int kLinearMostItems = 1 << 30;           // items of a call
 constexpr int kLinearMostSplits = 64;
 constexpr int64_t kLinearMostPartial = (int64_t)64 << 20;  // bytes of results of cut sums
 

@@ -55,7 +55,7 @@ constexpr int kHalf = kCols / 2;    // the first and the second of them (swiglu:
 constexpr int kDeep = kLinearDeep;  // places along the sum in a step
 constexpr int kStepBytes = 2 * kDeep;
 constexpr uint32_t kNowhere = 0x80000000u;  // past every buffer
-constexpr int kMostItems = 1 << 30;         // items of a call
+constexpr int kMostItems = kLinearMostItems;
 
 template <int BM>
 struct Wide {
@@ -133,9 +133,9 @@ __device__ __forceinline__ float add_places(bf16x8 f, float v) {
 // Rows of each of the n tiles that r rows are cut into: as even as 16 allows, so
 // that workgroups beside each other take the same time and find each other's
 // operands in their XCD's L2 (49152 rows of 64 experts, 700 to 840 each, gate
-// and up product EVEN_US us for 3050 with tiles of 256 rows and a rest).
+// and up product 2680 us for 3050 with tiles of 256 rows and a rest).
 __device__ __forceinline__ int even_rows(int r, int n) {
-  return ((r + n * 16 - 1) / (n * 16)) * 16;
+  return (int)(((uint32_t)r + (uint32_t)n * 16 - 1) / ((uint32_t)n * 16) * 16);
 }
 
 // Whether step k of an item is the sum's last, and not full.
@@ -792,7 +792,6 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void join_kernel(LinearArgs g, 
 
 template <Product P, int ACT>
 hipError_t launch(const Budget& b, const LinearArgs& g, const LinearShape& s, hipStream_t stream) {
-  if (s.items > kMostItems) return hipErrorInvalidValue;
   const int grid = stay_grid(b, s.items);
   if (s.rows == 256)
     hipLaunchKernelGGL((linear_wide_kernel<P, ACT, 256>), dim3(grid), dim3(kWaves * kWave), 0, stream, g, s);
@@ -820,17 +819,17 @@ hipError_t launch_act(const Budget& b, const LinearArgs& g, const LinearShape& s
 
 }  // namespace
 
-size_t linear_workspace(int64_t rows, int K, int E, int N, int) {
+LinearNeeds linear_needs(int64_t rows, int K, int E, int N) {
   const LinearShape s = linear_shape(rows, E, N, K, rows * N);
-  return s.splits > 1 ? (size_t)s.splits * rows * N * 4 : 0;
+  return {s.splits > 1 ? (size_t)s.splits * rows * N * 4 : 0, s.items <= kMostItems};
 }
-size_t dgrad_workspace(int64_t rows, int K, int E, int N) {
+LinearNeeds dgrad_needs(int64_t rows, int K, int E, int N) {
   const LinearShape s = linear_shape(rows, E, K, N, rows * K);
-  return s.splits > 1 ? (size_t)s.splits * rows * K * 4 : 0;
+  return {s.splits > 1 ? (size_t)s.splits * rows * K * 4 : 0, s.items <= kMostItems};
 }
-size_t wgrad_workspace(int64_t rows, int K, int E, int N) {
+LinearNeeds wgrad_needs(int64_t rows, int K, int E, int N) {
   const LinearShape s = wgrad_shape(rows, E, N, K);
-  return s.splits > 1 ? (size_t)s.splits * E * N * (K + 1LL) * 4 : 0;
+  return {s.splits > 1 ? (size_t)s.splits * E * N * (K + 1LL) * 4 : 0, s.items <= kMostItems};
 }
 
 hipError_t launch_linear(const Budget& b, const LinearArgs& g, hipStream_t stream) {

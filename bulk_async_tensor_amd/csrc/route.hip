@@ -125,7 +125,7 @@ __device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t t, int l
   int64_t* const s_key = reinterpret_cast<int64_t*>(s_c);
   double top = -INFINITY, total = 0.0;
   if (!a.sigmoid) {
-#pragma unroll 1
+#pragma unroll 4
     for (int e = lane; e < E; e += kWave) {
       const double l = (double)logit_at(a.logits, a.bf16, row + e);
       top = l > top || l != l ? l : top;
@@ -134,7 +134,7 @@ __device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t t, int l
   }
   // (a softmax's row of -infinity alone: scores 0)
   const bool none = !a.sigmoid && top == -INFINITY;
-#pragma unroll 1
+#pragma unroll 4
   for (int e = lane; e < E; e += kWave) {
     const double l = (double)logit_at(a.logits, a.bf16, row + e);
     const double x = a.sigmoid ? sigmoid64(l) : none ? 0.0 : exp(l - top);
@@ -142,7 +142,7 @@ __device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t t, int l
     total += x;
   }
   total = a.sigmoid || none ? 1.0 : wave_sum(total);
-#pragma unroll 1
+#pragma unroll 4
   for (int e = lane; e < E; e += kWave) s_c[e] = s_c[e] / total + (a.bias ? (double)a.bias[e] : 0.0);
   uint64_t kept = ~0ull;
   const int per = E / a.groups;
@@ -174,7 +174,7 @@ __device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t t, int l
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
-#pragma unroll 1
+#pragma unroll 4
   for (int e = lane; e < E; e += kWave)
     s_key[e] = kept >> (a.groups > 1 ? e / per : 0) & 1
                    ? order_of(a.bias ? s_c[e] : (double)logit_at(a.logits, a.bf16, row + e))
@@ -183,7 +183,7 @@ __device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t t, int l
   for (int j = 0; j < a.k; ++j) {
     int64_t best = kGone;
     int at = INT32_MAX;
-#pragma unroll 1
+#pragma unroll 4
     for (int e = lane; e < E; e += kWave) {
       const int64_t k = s_key[e];
       if (k > best) {
@@ -300,11 +300,12 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(RouteArgs a,
     again = total != total;
     inv = 1.0f / total;
   }
-  // What the scores may be off by, twice.  Sigmoid: exp's argument loses 1.5 |l|
-  // half steps, of which its slope leaves 0.34, and four are added by exp, sum
-  // and reciprocal: 2^-22.  Softmax: the sum's roundings, NV and a few half
-  // steps, relative to scores of at most 1 / total, and 2^-24 by exp.
-  const float score_error = !scores ? 0.0f : a.sigmoid ? 0x1p-20f : inv * (NV + 10) * 0x1p-23f + 0x1p-22f;
+  // What the scores may be off by, twice.  Sigmoid, in half steps of 1: exp's
+  // argument loses 1.22 |l|, exp itself 2, of which the sigmoid's slope leaves
+  // 0.27 and 0.5, and the sum and the reciprocal add 3: 3.8, twice 2^-21.
+  // Softmax: the sum's roundings, NV and a few half steps, relative to scores of
+  // at most 1 / total, and 2^-24 by exp.
+  const float score_error = !scores ? 0.0f : a.sigmoid ? 0x1p-21f : inv * (NV + 10) * 0x1p-23f + 0x1p-22f;
   uint32_t key[NV];
   float probe = 0.0f;  // NaN if any is
   float c[NV];

@@ -135,14 +135,15 @@ int ep_route_backward(const void* logits, int logits_type, int T, int E, int sco
  *   pre       bf16 [rows, N] or NULL
  *   workspace ep_grouped_linear_workspace_bytes(...) bytes, 16-byte aligned,
  *             or NULL where that is 0 (it is where there are rows enough for
- *             every compute unit; else sums along K are split and joined).
- *             Its contents need not be kept or cleared.
+ *             every compute unit; else sums along K are cut and joined).  At
+ *             most 64 MiB, and its contents need not be kept or cleared.
  * a, b, residual, y and pre are 16-byte aligned, bias 4-byte.  Limits: 1 <= E <=
  * EP_MAX_EXPERTS, 0 <= rows <= EP_MAX_ENTRIES, N and K <= EP_LINEAR_MAX_SIDE,
- * N * K <= EP_LINEAR_MAX_WEIGHT.  rows == 0 enqueues nothing.  Equal calls give
- * equal bits.
+ * N * K <= EP_LINEAR_MAX_WEIGHT, and 2^30 tiles of 128 x 256 results.  rows ==
+ * 0 enqueues nothing.  Sums are taken in an order that the sizes fix: equal
+ * calls give equal bits.
  */
-size_t ep_grouped_linear_workspace_bytes(int64_t rows, int K, int E, int N, int act);
+size_t ep_grouped_linear_workspace_bytes(int64_t rows, int K, int E, int N);
 int ep_grouped_linear(const void* a, int64_t rows, int K, const int32_t* offsets, int E, const void* b,
                       const float* bias, int N, int act, const void* residual, void* y, int y_type, void* pre,
                       void* workspace, size_t workspace_bytes, void* stream);

@@ -1,0 +1,216 @@
+"""The router and the bf16 products at the ends of their ranges: workgroups that
+go through many tiles, sums of few steps, buffers past 4 GiB, launches in more
+than one piece, and workspaces of the caller's."""
+
+import math
+
+import pytest
+import torch
+
+import bulk_async_tensor_amd as ep
+
+import layer_ref as ref
+from gpu_helpers import DEV
+from test_gpu_layer import BF16, F32, check_dgrad, check_linear, check_wgrad, gen, same, within
+
+pytestmark = pytest.mark.gpu
+
+
+def offsets_of(counts):
+    return torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), dtype=torch.int32, device=DEV)
+
+
+@pytest.fixture(scope="module")
+def eight_cus():
+    stream = ep.ep_stream_create_cu_masked(ep.cu_mask_words(range(8)))
+    yield stream
+    torch.cuda.synchronize()
+    ep.ep_stream_destroy(stream)
+
+
+# Sums of one to six steps (three copies or two in LDS, one step more in a tile at least), tiles of 128 rows and of
+# 256, and items that eight workgroups share in many rounds: rows of each expert, K, N.
+STREAMS = [([500, 0, 130, 257, 64, 1], 64, 600), ([300, 700], 72, 2056), ([129] * 9, 128, 520), ([256] * 5, 200, 1000),
+           ([4000, 5000], 64, 1288), ([3000] * 4, 192, 1040), ([2000, 0, 2500, 1], 264, 1544), ([9000], 384, 776)]
+
+
+@pytest.mark.parametrize("counts, K, N", STREAMS)
+def test_streams_of_tiles(counts, K, N, eight_cus):
+    """On a stream of eight compute units each workgroup goes through many tiles: the same bits as on all."""
+    offsets, rows, E = offsets_of(counts), sum(counts), len(counts)
+    a, d, b = ref.rows(rows, K, 1, DEV), ref.rows(rows, N, 2, DEV), ref.weights(E, N, K, 3, DEV)
+    pre, bias = ref.rows(rows, 2 * K, 4, DEV), torch.randn(E, N, generator=gen(5), device=DEV)
+    want = (check_linear(a, offsets, b, "gelu", bias=bias), check_dgrad(d, offsets, b, "swiglu", pre),
+            *check_wgrad(d, a, offsets, E))
+    torch.cuda.synchronize()
+    y = torch.full((rows, N), 77.0, dtype=BF16, device=DEV)
+    dx = torch.full((rows, 2 * K), 77.0, dtype=BF16, device=DEV)
+    db, dbias = torch.full((E, N, K), 77.0, device=DEV), torch.full((E, N), 77.0, device=DEV)
+    torch.cuda.synchronize()
+    ep.ep_grouped_linear(a, offsets, b, y, bias=bias, act="gelu", stream=eight_cus)
+    ep.ep_grouped_linear_dgrad(d, offsets, b, dx, act="swiglu", pre=pre, stream=eight_cus)
+    ep.ep_grouped_linear_wgrad(d, a, offsets, db, dbias, stream=eight_cus)
+    eight_cus.synchronize()
+    for got, w in zip((y, dx, db, dbias), want):
+        same(got, w)
+
+
+def test_rows_past_4_gib():
+    """Token rows and results whose byte offsets pass 32 bits; the last expert holds the last rows."""
+    rows, wide = 300000, 8192
+    tail = 777
+    offsets = torch.tensor([0, 5, 5, rows - tail, rows], dtype=torch.int32, device=DEV)
+    a = torch.zeros(rows, wide, dtype=BF16, device=DEV)
+    a[:5] = ref.rows(5, wide, 1, DEV)
+    a[-tail:] = ref.rows(tail, wide, 2, DEV)
+    narrow = ref.rows(rows, 64, 3, DEV)
+    b = ref.weights(4, 64, wide, 4, DEV)
+    y = torch.zeros(rows, 64, dtype=BF16, device=DEV)
+    ep.ep_grouped_linear(a, offsets, b, y)
+    for e, lo in ((0, 0), (3, rows - tail)):
+        hi = lo + (5 if e == 0 else tail)
+        want, err, _, _ = ref.linear(a[lo:hi], None, b[e : e + 1], None, "none", None, BF16)
+        within(y[lo:hi], want, err, "y")
+    db = torch.full((4, 64, wide), 7.0, device=DEV)
+    ep.ep_grouped_linear_wgrad(narrow, a, offsets, db)
+    want, err, _, _ = ref.wgrad(narrow[-tail:], a[-tail:], None, 1, F32)
+    within(db[3], want[0], err[0], "db")
+    assert bool((db[1] == 0).all())
+    dx = torch.empty(rows, wide, dtype=BF16, device=DEV)
+    ep.ep_grouped_linear_dgrad(narrow, offsets, b, dx)
+    want, err = ref.dgrad(narrow[-tail:], None, b[3:], "none", None)
+    within(dx[-tail:], want, err, "dx")
+    want, err = ref.dgrad(narrow[5:50], None, b[2:3], "none", None)
+    within(dx[5:50], want, err, "dx")
+
+
+def test_weights_past_4_gib():
+    """A weight and a float32 gradient of 5 GB, experts at both ends."""
+    E, N, K = 300, 2048, 2048
+    rows = 200
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    offsets[1:-1] = 90
+    offsets[-1] = rows
+    big = torch.zeros(E + 350, N, K, dtype=BF16, device=DEV)
+    b = big[350:]
+    b[0], b[-1] = ref.weights(1, N, K, 1, DEV)[0], ref.weights(1, N, K, 2, DEV)[0]
+    a, d = ref.rows(rows, K, 3, DEV), ref.rows(rows, N, 4, DEV)
+    y, dx = torch.zeros(rows, N, dtype=BF16, device=DEV), torch.zeros(rows, K, dtype=BF16, device=DEV)
+    # all experts of the larger tensor: the last one lies past 4 GiB
+    off_big = torch.zeros(E + 351, dtype=torch.int32, device=DEV)
+    off_big[351:-1] = 90
+    off_big[-1] = rows
+    ep.ep_grouped_linear(a, off_big, big, y)
+    ep.ep_grouped_linear_dgrad(d, off_big, big, dx)
+    for e, r in ((0, slice(0, 90)), (-1, slice(90, rows))):
+        w = b[e].unsqueeze(0)
+        want, err, _, _ = ref.linear(a[r], None, w, None, "none", None, BF16)
+        within(y[r], want, err, "y")
+        want, err = ref.dgrad(d[r], None, w, "none", None)
+        within(dx[r], want, err, "dx")
+    del big, b
+    db = torch.full((E, N, K), 7.0, device=DEV)
+    ep.ep_grouped_linear_wgrad(d, a, offsets, db)
+    for e, r in ((0, slice(0, 90)), (-1, slice(90, rows))):
+        want, err, _, _ = ref.wgrad(d[r], a[r], None, 1, F32)
+        within(db[e], want[0], err[0], "db")
+    assert float(db[1:-1].abs().max()) == 0.0
+
+
+def test_longest_sides():
+    """A weight's sides at their limit, and sums over very many places."""
+    side = 1 << 20
+    a, b = ref.rows(3, side, 1, DEV), ref.weights(1, 8, side, 2, DEV)
+    check_linear(a, None, b, dtype=F32)
+    d = ref.rows(3, 8, 3, DEV)
+    check_dgrad(d, None, b)
+    check_wgrad(d, a, None, 1)
+    w = ref.weights(1, side, 16, 4, DEV)
+    x = ref.rows(2, 16, 5, DEV)
+    check_linear(x, None, w, "swiglu")
+    check_dgrad(ref.rows(2, side, 6, DEV), None, w)
+
+
+@pytest.mark.parametrize("op", ["linear", "dgrad", "wgrad"])
+def test_workspace_of_the_caller(op):
+    """What a workspace holds does not matter; one that is too small is refused; a larger one may be any size."""
+    rows, K, N = 200, 4096, 264
+    a, d, b = ref.rows(rows, K, 1, DEV), ref.rows(rows, N, 2, DEV), ref.weights(1, N, K, 3, DEV)
+    if op == "wgrad":
+        rows = 8192
+        a, d = ref.rows(rows, 264, 1, DEV), ref.rows(rows, 128, 2, DEV)
+        need = ep.ep_grouped_linear_wgrad_workspace_bytes(rows, 264, 1, 128)
+    elif op == "dgrad":
+        d, b = ref.rows(rows, K, 2, DEV), ref.weights(1, K, N, 3, DEV)
+        need = ep.ep_grouped_linear_dgrad_workspace_bytes(rows, N, 1, K)
+    else:
+        need = ep.ep_grouped_linear_workspace_bytes(rows, K, 1, N)
+    assert need > 0
+
+    def call(workspace):
+        if op == "linear":
+            return check_linear(a, None, b, workspace=workspace)
+        if op == "dgrad":
+            return check_dgrad(d, None, b, workspace=workspace)
+        return check_wgrad(d, a, None, 1, workspace=workspace)[0]
+
+    want = call(None)
+    for size in (need, need + 4096):
+        ws = torch.full((size // 4,), math.nan, device=DEV)
+        same(call(ws), want)
+        same(call(ws), want)
+    with pytest.raises(ep.EpError, match="workspace"):
+        call(torch.zeros(need - 16, dtype=torch.uint8, device=DEV))
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured calls on one workspace, replayed one after the other on a stream."""
+    need = ep.ep_grouped_linear_workspace_bytes(64, 4096, 1, 128)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    xs = [ref.rows(64, 4096, i, DEV) for i in (1, 2)]
+    b = ref.weights(1, 128, 4096, 3, DEV)
+    ys = [torch.zeros(64, 128, device=DEV) for _ in xs]
+    side = torch.cuda.Stream()
+    graphs = []
+    with torch.cuda.stream(side):
+        for x, y in zip(xs, ys):
+            ep.ep_grouped_linear(x, None, b, y, workspace=ws)
+            side.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                ep.ep_grouped_linear(x, None, b, y, workspace=ws)
+            graphs.append(g)
+    for seed in (5, 6, 7):
+        for i, x in enumerate(xs):
+            x.copy_(ref.rows(64, 4096, seed + 10 * i, DEV))
+        torch.cuda.synchronize()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(xs, ys):
+            want, err, _, _ = ref.linear(x, None, b, None, "none", None, F32)
+            within(y, want, err, "y")
+
+
+def test_route_of_very_many_tokens():
+    """More tokens than one launch takes, and logits past 4 GiB."""
+    T, E = (1 << 26) + 1000, 4
+    l = torch.randint(-8, 8, (T, E), generator=gen(1), device=DEV, dtype=torch.int8).float()
+    idx, w = torch.full((T, 1), -9, dtype=torch.int32, device=DEV), torch.full((T, 1), -9.0, device=DEV)
+    ep.ep_route(l, idx, w, score="sigmoid", renormalize=False)
+    assert torch.equal(idx[:, 0].long(), l.argmax(1))  # (of equal ones the lowest: torch's on these sizes too)
+    want = torch.sigmoid(l.double().amax(1))
+    assert float(((w[:, 0].double() - want) / want).abs().max()) < 8 * ref.U32 * 8
+    del l, idx, w, want
+    T, E = 5_000_000, 256
+    l = torch.randn(T, E, generator=gen(2), device=DEV)
+    idx, w = torch.full((T, 2), -9, dtype=torch.int32, device=DEV), torch.full((T, 2), -9.0, device=DEV)
+    ep.ep_route(l, idx, w, score="softmax")
+    for r in (slice(0, 500), slice(T - 500, T)):
+        assert torch.equal(idx[r].cpu(), ref.route(l[r], 2, "softmax")[0])
+    dl = torch.full((T, E), 7.0, dtype=BF16, device=DEV)
+    ep.ep_route_backward(l, idx, w, dl)
+    r = slice(T - 500, T)
+    want = ref.route_backward(l[r], idx[r], w[r], "softmax")
+    assert float((dl[r].cpu().double() - want).abs().max()) <= ref.UBF16
+    assert bool((w.sum(1) - 1).abs().max() < 4 * ref.U32)

@@ -102,6 +102,7 @@ LINEAR = [("a", A16), ("rows", 4096), ("K", 256), ("off", A4), ("E", 4), ("b", A
     (dict(b=None), -1), (dict(y=None), -1), (dict(a=A16 + 8), -2), (dict(b=A16 + 8), -2), (dict(y=A16 + 8), -2),
     (dict(res=A16 + 8), -2), (dict(pre=A4), -2), (dict(bias=A2), -2), (dict(rows=0), 0),
     (dict(rows=0, a=None, b=None, y=None, bias=None, res=None, pre=None, ws=None, bytes=0), 0),
+    (dict(rows=2143289343, E=1, N=1 << 20, K=1000), -1),
 ])
 def test_linear_arguments(lib, over, code):
     refused(lib, "ep_grouped_linear", LINEAR, over, code)
@@ -134,20 +135,18 @@ def test_wgrad_arguments(lib, over, code):
 
 def test_workspace_is_checked(lib):
     """Wherever a call needs a workspace, it is refused without one, with one that is too small, and unaligned."""
-    cases = [("ep_grouped_linear", LINEAR, lib.ep_grouped_linear_workspace_bytes(128, 7168, 1, 256, 0)),
+    cases = [("ep_grouped_linear", LINEAR, lib.ep_grouped_linear_workspace_bytes(128, 7168, 1, 256)),
              ("ep_grouped_linear_dgrad", DGRAD, lib.ep_grouped_linear_dgrad_workspace_bytes(128, 256, 1, 7168)),
              ("ep_grouped_linear_wgrad", WGRAD, lib.ep_grouped_linear_wgrad_workspace_bytes(8192, 1024, 1, 256))]
     sizes = {"ep_grouped_linear": dict(rows=128, K=7168, E=1, off=None, N=256),
              "ep_grouped_linear_dgrad": dict(rows=128, K=256, E=1, off=None, N=7168),
              "ep_grouped_linear_wgrad": dict(rows=8192, K=1024, E=1, off=None, N=256)}
     for name, args, need in cases:
-        if not need:
-            continue
-        assert need % 16 == 0
+        assert 0 < need <= (64 << 20) + (1 << 20) and need % 16 == 0
         for over, code in ((dict(ws=None, bytes=0), -4), (dict(ws=None), -4), (dict(bytes=need - 1), -4),
                            (dict(ws=A4, bytes=need), -2)):
             refused(lib, name, args, {**sizes[name], **over}, code)
-    assert lib.ep_grouped_linear_workspace_bytes(-1, 64, 1, 64, 0) == 0
+    assert lib.ep_grouped_linear_workspace_bytes(-1, 64, 1, 64) == 0
     assert lib.ep_grouped_linear_dgrad_workspace_bytes(8, 0, 1, 64) == 0
     assert lib.ep_grouped_linear_wgrad_workspace_bytes(8, 64, 0, 64) == 0
 
