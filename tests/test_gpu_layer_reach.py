@@ -31,7 +31,8 @@ def eight_cus():
 # Sums of one to six steps (three copies or two in LDS, one step more in a tile at least), tiles of 128 rows and of
 # 256, and items that eight workgroups share in many rounds: rows of each expert, K, N.
 STREAMS = [([500, 0, 130, 257, 64, 1], 64, 600), ([300, 700], 72, 2056), ([129] * 9, 128, 520), ([256] * 5, 200, 1000),
-           ([4000, 5000], 64, 1288), ([3000] * 4, 192, 1040), ([2000, 0, 2500, 1], 264, 1544), ([9000], 384, 776)]
+           ([4000, 5000], 64, 1288), ([3000] * 4, 192, 1040), ([2000, 0, 2500, 1], 264, 1544), ([9000], 384, 776),
+           ([4000, 5000], 1288, 64), ([3000] * 4, 1040, 192), ([500, 0, 700, 10], 1032, 4104)]
 
 
 @pytest.mark.parametrize("counts, K, N", STREAMS)
