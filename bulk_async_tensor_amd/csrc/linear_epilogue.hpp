@@ -1,6 +1,5 @@
 // What follows the experts' bf16 products: bias, activation and residual, and
-// the activation's derivative on the way back, for four neighbouring results
-// of a row.
+// the activation's derivative on the way back.
 #pragma once
 
 #include "ep_device.hpp"

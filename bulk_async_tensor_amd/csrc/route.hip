@@ -2,10 +2,13 @@
 // token, its weights, and the weights' gradient to the logits.
 //
 // ep_route.  The choice has to be that of exact scores, but float32 is enough
-// to make nearly all of it: a token's experts are ranked by float32 keys, and
-// where two neighbours of the ranking (or the groups at the edge) are closer
-// than the keys can be wrong, and not equal by having the same logit and bias,
-// the token is done again in float64 by the whole wave (route_exact).
+// to make nearly all of it: a token's experts are ranked by float32 keys.  Where
+// two neighbours of the choice are closer than the keys can be wrong, and not
+// equal by having the same logit and bias, a few more experts are taken, up to a
+// certain gap, and what lies before it is ranked in float64.  Where that does
+// not do either (groups as close at the edge, softmax scores with a bias, a NaN,
+// no gap near), the token is done again in float64 by the whole wave
+// (route_exact).
 //
 // 16 lanes take a token (64 where there are more than 512 experts, more than
 // 15 are chosen, or few tokens are there), a lane NV neighbouring experts.  A
@@ -14,10 +17,15 @@
 // within a lane and the largest names its expert.  Choosing one: each lane
 // finds its largest key below the last one it gave (key - last wraps to the top
 // of the unsigned range exactly for smaller keys, so that is one subtraction
-// and half a maximum a key); four exchanges give the token's largest value, a ballot
-// the first lane that holds it (of equal values the lowest expert).
+// and half a maximum a key); four exchanges give the token's largest value, a
+// ballot the first lane that holds it (of equal values the lowest expert).
 //
-// T 16384, E 256, groups: ROUTE_NUMBERS
+// us, kernel alone: 128 tokens of 256 experts in 8 groups, k 8 6.5; 16384 of
+// them 17.7 (without groups 10.6), 17.8 MB or 1.0 TB/s: 12 are the scores,
+// groups and nine rounds of choosing, the rest a token or two that float64
+// decides, one load and one exchange after another; 16384 tokens of 64 experts
+// in bf16, k 6, 5.5.  The gradient: 4096 tokens of 256 experts 7.6, 8191 of 60
+// 6.9, load latency.
 #include <math.h>
 
 #include "ep.h"

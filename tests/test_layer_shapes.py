@@ -81,7 +81,8 @@ def test_kernels_are_those_that_are_reached(shapes):
     """The library holds the kernels that some call reaches, and no other."""
     names = subprocess.run(["nm", "-C", LIB_PATH], capture_output=True, text=True, check=True).stdout
     built = {(int(a), int(b), t == "true") for a, b, t in re.findall(r"__device_stub__route_kernel<(\d+), (\d+), (\w+)>", names)}
-    asked = ["route %d %d %d 256" % (T, E, k) for T in (1, 100000) for E in (4, 64, 128, 256, 512, 1024) for k in (1, 20) if k <= E]
+    asked = ["route %d %d %d 256" % (T, E, k) for T in (1, 100000) for E in (4, 64, 128, 256, 512, 1024) for k in (1, 20)
+             if k <= E]
     assert built == {(*r, t) for r in shapes(asked) for t in (False, True)}
     # forward and dgrad with every activation, wgrad without, each with both tile heights
     wide = set(re.findall(r"__device_stub__linear_wide_kernel<\S*?(\d), (\d), (\d+)>", names))
