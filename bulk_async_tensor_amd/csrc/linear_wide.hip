@@ -42,8 +42,8 @@
 // up to the number of copies and one.
 //
 // Few tiles: the sum is cut into `splits` runs of steps, each an item of its
-// own whose float32 results go to the workspace; join_kernel adds them in
-// ascending order and does what follows the product.
+// own whose float32 results go to the workspace; join_kernel adds them in a
+// fixed order and does what follows the product.
 #include "ep.h"
 #include "ep_device.hpp"
 #include "fp8_device.hpp"
@@ -95,11 +95,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p, int64
 // below wait for the ones that are due.  They have no result registers, and the
 // next instruction may change the address registers.  The s_nop covers M0 and
 // buffer registers that a vector instruction has just written (5 wait states).
-__device__ __forceinline__ void load16_to_lds(const u32x4& buf, uint32_t lds, uint32_t offset, uint32_t base) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(offset),
-               "s"(buf), "s"(base)
-               : "memory");
-}
 template <int kNext>
 __device__ __forceinline__ void load16_pair_to_lds(const u32x4& buf, uint32_t lds, uint32_t offset0, uint32_t offset1,
                                                    uint32_t base) {
@@ -299,7 +294,8 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
       const int lo = __builtin_amdgcn_readfirstlane(s_seg[e].lo), hi = __builtin_amdgcn_readfirstlane(s_seg[e].hi);
       nxt.e = e;
       nxt.c0 = (int)unit * per_unit;
-      const int per = even_rows(hi - lo, mine);
+      // (never more than a tile holds, were the count of tiles cut short)
+      const int per = min(even_rows(hi - lo, mine), BM);
       nxt.r0 = lo + (int)(local - unit * mine) * per;
       nxt.r1 = min(nxt.r0 + per, hi);
       all = (deep + kDeep - 1) / kDeep;
@@ -428,7 +424,6 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   };
 
   Item cur;
-  int kb = 0;
   bool sums = false;
   Frag t[MT], w[4];
   // A step has two barriers.  Before the first, ahead of column tile kOpen,
