@@ -11,7 +11,7 @@ import bulk_async_tensor_amd as ep
 
 import layer_ref as ref
 from gpu_helpers import DEV
-from test_gpu_layer import BF16, F32, check_dgrad, check_linear, check_wgrad, gen, same, within
+from test_gpu_layer import (BF16, F32, check_dgrad, check_linear, check_route, check_wgrad, gen, logits_of, same, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -215,3 +215,101 @@ def test_route_of_very_many_tokens():
     want = ref.route_backward(l[r], idx[r], w[r], "softmax")
     assert float((dl[r].cpu().double() - want).abs().max()) <= ref.UBF16
     assert bool((w.sum(1) - 1).abs().max() < 4 * ref.U32)
+
+
+# ------------------------------------------------------------------ enough tokens for 16 lanes each
+MANY = 2100  # (2048 and fewer take 64 lanes on 256 compute units)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("E, k, groups, top, best", [(128, 8, 32, 9, 2), (100, 15, 1, 1, 1), (256, 8, 8, 4, 2),
+                                                     (255, 6, 5, 2, 2), (512, 8, 64, 5, 1), (300, 15, 3, 2, 2),
+                                                     (257, 1, 1, 1, 1), (500, 4, 50, 50, 2)])
+def test_route_many_tokens(E, k, groups, top, best, dtype, kind):
+    l = logits_of(MANY, E, E, dtype)
+    bias = torch.randint(-30, 31, (E,), generator=gen(E), device=DEV) * 0.001
+    more = dict(groups=groups, top_groups=top, group_best=best)
+    check_route(l, k, kind, renormalize=True, scale=2.5, bias=bias, **more)
+    check_route(l, k, kind, renormalize=False, **more)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [128, 256, 512])
+def test_route_many_tokens_close(E, kind):
+    """Near ties, ties, masks and NaN beside ordinary tokens in one wave."""
+    k, inf, nan = 8, math.inf, math.nan
+    l = logits_of(MANY, E, 1)
+    some = torch.arange(0, MANY, 3, device=DEV)
+    l[some] = 2.0 + l[some] * 1e-6
+    l[1::7] = torch.randint(0, 4, (len(range(1, MANY, 7)), E), generator=gen(2), device=DEV).float()
+    l[5], l[50, 1:], l[51, ::2], l[52] = -inf, -inf, -inf, torch.finfo(F32).min
+    l[100, 3:], l[101, 7], l[102, 0], l[102, E - 1], l[103] = torch.finfo(F32).min, nan, inf, nan, nan
+    l[104] = -200.0 - torch.arange(E, device=DEV) * 0.01
+    l[105, 5], l[105, 6] = inf, inf
+    near = torch.randn(E, generator=gen(3), device=DEV) * 1e-7
+    odd = near.clone()
+    odd[5], odd[6], odd[7] = -inf, torch.finfo(F32).min, nan
+    for over in (dict(), dict(bias=near), dict(bias=odd), dict(groups=8, top_groups=3, group_best=2),
+                 dict(bias=near, groups=8, top_groups=3, group_best=2), dict(bias=odd, groups=4, top_groups=2, group_best=2)):
+        for renorm in (False, True):
+            idx, _ = check_route(l, k, kind, renormalize=renorm, **over)
+            assert bool((idx.sort(1).values.diff(dim=1) > 0).all()) and bool((idx >= 0).all()) and bool((idx < E).all())
+
+
+# ------------------------------------------------------------------ what follows a product
+@pytest.mark.parametrize("act", ["none", "silu", "gelu", "swiglu"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows, E, K, N", [(300, 3, 128, 400), (40, 2, 2048, 272)])
+def test_every_epilogue(rows, E, K, N, dtype, act):
+    """Bias, residual and pre in all combinations, on whole sums and on cut ones."""
+    first = rows // E + 1
+    offsets = offsets_of([first] + [0] * (E - 2) + [rows - first])
+    a, b = ref.rows(rows, K, 1, DEV), ref.weights(E, N, K, 2, DEV)
+    bias = torch.randn(E, N, generator=gen(3), device=DEV)
+    res = ref.rows(rows, N // 2 if act == "swiglu" else N, 4, DEV)
+    for use in range(8):
+        check_linear(a, offsets, b, act, dtype, bias=bias if use & 1 else None, residual=res if use & 2 else None,
+                     pre=bool(use & 4) or None)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "swiglu"])
+def test_activations_over_their_range(act):
+    """Values and slopes from far below zero to far above, relative to the value.
+
+    The sum is zero, so z is the bias itself.  The argument's rounding moves exp
+    by |z| and erfc by z^2 half steps at most; the fit, its ten additions, the
+    exponential, the reciprocal and the products add no more than 18, and 24 are
+    allowed.  Below -88.7 the exponential overflows and the result is 0, where it
+    is 88.8 e^-88.8 = 2e-37 < 2^-120 in magnitude (times the up product)."""
+    n = 4096
+    z = torch.linspace(-120, 120, n, device=DEV)
+    z[:1000] = torch.linspace(-6, 6, 1000, device=DEV)
+    g, u = z.double(), torch.ones(n, dtype=torch.float64, device=DEV)
+    if act == "swiglu":
+        z = torch.cat([z, z.flip(0)])
+        g, u = z.double().chunk(2)
+    a, b = torch.zeros(3, 8, dtype=BF16, device=DEV), torch.zeros(1, len(z), 8, dtype=BF16, device=DEV)
+    y = torch.full((3, n), 77.0, device=DEV)
+    ep.ep_grouped_linear(a, None, b, y, bias=z.view(1, -1), act=act)
+    want = ref.act(act, g) * u
+    within(y, want.expand(3, n), ((g * g + g.abs() + 24) * ref.U32 * want.abs() + 2.0 ** -120 * u.abs()).expand(3, n), "y")
+    pre, dy = z.to(BF16).expand(3, -1).contiguous(), ref.rows(3, 8, 5, DEV)
+    ones = torch.ones(1, 8, n, dtype=BF16, device=DEV)
+    dx = torch.full(pre.shape, 77.0, dtype=BF16, device=DEV)
+    ep.ep_grouped_linear_dgrad(dy, None, ones, dx, act=act, pre=pre)
+    want, e = ref.dgrad(dy, None, ones, act, pre)
+    within(dx, want, e + 2.0 ** -120 * 128 * 64, "dx")  # (|u| <= 120, |d| <= 64)
+
+
+def test_rows_before_the_first_segment():
+    """Offsets that start past zero: the rows before them are not touched either, whole sums or cut ones."""
+    offsets = torch.tensor([5, 20, 20, 33], dtype=torch.int32, device=DEV)
+    for K, N in ((64, 264), (4096, 136)):
+        a, d, b = ref.rows(40, K, 1, DEV), ref.rows(40, N, 2, DEV), ref.weights(3, N, K, 3, DEV)
+        for t in (a, d):
+            t[:5], t[33:] = math.nan, math.nan
+        check_linear(a, offsets, b, "silu", pre=True, bias=torch.randn(3, N, generator=gen(4), device=DEV))
+        check_dgrad(d, offsets, b)
+        check_dgrad(a, offsets, b.transpose(1, 2).contiguous())
+        check_wgrad(d, a, offsets, 3)
