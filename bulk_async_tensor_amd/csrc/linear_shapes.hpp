@@ -6,13 +6,17 @@
 
 namespace ep {
 
-constexpr int kLinearCols = 256, kLinearDeep = 64;  // a tile's columns, and places along the sum in a step
-constexpr int kLinearCus = 256;                     // compute units that a call's work is cut for
-constexpr int kLinearMostItems = 1 << 30;           // items of a call
+constexpr int kLinearDeep = 64;            // places along the sum in a step
+constexpr int kLinearCus = 256;            // compute units that a call's work is cut for
+constexpr int kLinearMostItems = 1 << 30;  // items of a call
 constexpr int kLinearMostSplits = 64;
 constexpr int64_t kLinearMostPartial = (int64_t)64 << 20;  // bytes of results of cut sums
 
-// Steps whose tiles are in LDS or on the way.
+// A tile's columns, by its rows.
+constexpr int linear_cols(int rows) { return rows == 64 ? 128 : 256; }
+// Steps whose tiles are in LDS or on the way.  (64 rows with four or five: a
+// router's product 13.5 or 14.1 us for 13.7, wgrad of 4096 rows, N 256, K 7168
+// 41.6 or 42.2 for 38.1.)
 constexpr int linear_copies(int rows) { return rows == 256 ? 2 : 3; }
 
 // Rows of a tile, runs that a sum is cut into, and the items (tiles times
@@ -22,57 +26,74 @@ struct LinearShape {
   int64_t items;
 };
 
-// The shape is the one whose estimated time is least.  A tile's step takes
-// 0.75 us with 128 rows and 1.15 with 256 where half of the CUs or fewer work,
-// 0.95 and 1.65 where all do (wgrad, both sides turned, 0.95 and 1.2 with 128), and a
-// tile 2.5 or 4 us beside its steps.  The CUs make whole rounds of items.  A
-// cut sum costs a second kernel, 5 us, and its results their way to memory and
-// back, 2.9 bytes a picosecond.  Measured, us, by rows / runs (the rule's
-// choice first):
-//   128 rows, K 7168, N 256 (a router)      128/28 16.5  128/1 90.5  128/8 21.8
-//   4096 rows of it                         128/8 34.0   128/1 92.6  256/8 41.7
-//   97 rows, K 1200, N 336                  128/6 12.7   128/1 19.1  128/16 13.7
-//   2 rows, 5 experts, K 576, N 320         128/1 11.0   128/2 12.2
-//   416 rows, 34 experts, K 6456, N 816     128/3 101.8  128/1 130.9 128/28 116.3
-//   4096 rows, K = N = 4096                 256/1 110.8  128/1 132.1 256/2 177.2
-//   1024 rows, K = N = 4096                 128/2 52.5   128/1 55.8  256/4 57.1
-//   12078 rows, 7 experts, K 1448, N 368    128/1 28.4   256/1 40.2  128/2 59.2
-//   wgrad, 4096 rows, N 256, K 7168         128/4 36.8   128/1 65.8  128/8 49.0
-//   wgrad, 56934 rows, 9 experts, 848 x 568 256/2 122.1  128/1 141.8 256/8 157.7
-//   wgrad, 3944 rows, 2872 x 4864           256/1 101.5  128/1 130.5 256/2 154.5
+// The shape is the one whose estimated time is least: the CUs make whole rounds
+// of items, a tile takes its steps and some time beside them, and a cut sum
+// costs a second kernel, 6 us, and its results their way to memory and back, 2.6
+// bytes a picosecond.  The times are set so that over 1480 random sizes (1 to
+// 8000 rows, 1 to 64 experts, sides of 64 to 8192) the rule's choice takes 1.3 %
+// longer than the best of those tried (heights, 1 to 16 runs) on average.
+// Measured, us, by rows / runs (the rule's choice first):
+//   128 rows, K 7168, N 256 (a router)      64/28 13.4   64/14 13.9   128/28 17.3
+//   512 rows of it                          64/16 16.0   64/4 19.7    128/8 24.0
+//   32768 rows of it                        128/1 137.0  256/2 157.2  64/1 211.8
+//   64 rows, K 8192, N 4096                 64/8 22.8    64/1 59.7    128/4 36.4
+//   64 rows, K 1024, N 16384                64/1 14.3    128/1 20.6   64/2 18.3
+//   16 rows, K 4096, N 7168                 64/4 18.0    64/8 18.9    128/4 23.0
+//   1024 rows, K = N = 1024                 64/1 12.5    128/1 21.3   64/2 16.6
+//   512 rows, K = N = 8192                  256/4 84.9   128/2 86.0   64/1 114.6
+//   4096 rows, K = N = 4096                 256/1 114.6  128/1 137.8  64/1 227.5
+//   1024 rows, 256 experts, K 2048, N 7168  64/1 1230    128/1 1270   256/1 1330
+//   416 rows, 34 experts, K 6456, N 816     64/1 83.9    64/2 89.5    128/8 107.3
+//   12078 rows, 7 experts, K 1448, N 368    128/1 30.8   64/1 40.4    256/1 43.7
+//   wgrad, 1024 rows, N 256, K 8192         64/1 16.0    128/1 24.1   64/2 27.0
+//   wgrad, 8192 rows, N 64, K 4096          64/8 21.2    64/4 25.4    64/1 64.4
+//   wgrad, 512 rows, N 2048, K 4096         128/1 19.2   64/1 30.3    128/2 50.3
+//   wgrad, 56934 rows, 9 experts, 848 x 568 256/2 105.6  128/1 117.2  64/1 179.6
+//   wgrad, 3944 rows, 2872 x 4864           256/1 108.0  128/1 140.8  64/1 261.6
+constexpr int kLinearHeights[] = {64, 128, 256};
+
 struct LinearWork {
-  int64_t tiles[2];   // tiles there may be expected to be with 128 and with 256 rows,
-  int64_t most[2];    // and at most
+  int64_t tiles[3];   // tiles there may be expected to be with 64, 128 and 256 rows,
+  int64_t most[3];    // and at most
   int64_t steps;      // of a tile's sum
   int64_t results;    // float32 values of a run's results
   bool wgrad;
 };
 
-inline int64_t linear_cost_ns(const LinearWork& w, int tall, int64_t splits) {
-  const int64_t items = w.tiles[tall] * splits;
+// By height, in ns: a tile beside its steps, and a step where half of the CUs
+// or fewer work, where all do, and both for wgrad.
+constexpr int kLinearCosts[][5] = {
+    {2000, 430, 440, 460, 550}, {2500, 850, 1050, 950, 1200}, {4000, 1250, 1600, 1400, 1650}};
+
+// `steps` is that of the longest of the runs.
+inline int64_t linear_cost_ns(const LinearWork& w, int h, int splits, int steps) {
+  const int64_t items = w.tiles[h] * splits;
   const int64_t rounds = (items + kLinearCus - 1) / kLinearCus;
-  int64_t steps = (w.steps + splits - 1) / splits;
-  const int64_t least = linear_copies(tall ? 256 : 128) + 1;
-  if (steps < least) steps = least;
-  const bool all = 2 * items > kLinearCus;
-  const int64_t step = tall ? (all ? 1650 : 1150) : all ? (w.wgrad ? 1200 : 950) : w.wgrad ? 950 : 750;
-  const int64_t join = splits > 1 ? 5000 + splits * w.results * 4 / 2900 : 0;
-  return rounds * (steps * step + (tall ? 4000 : 2500)) + join;
+  const int64_t step = kLinearCosts[h][1 + (2 * items > kLinearCus) + 2 * w.wgrad];
+  const int64_t join = splits > 1 ? 6000 + splits * w.results * 4 / 2600 : 0;
+  return rounds * (steps * step + kLinearCosts[h][0]) + join;
 }
 
 inline LinearShape linear_best(const LinearWork& w) {
-  LinearShape best = {128, 1, w.most[0]};
+  LinearShape best = {};
   int64_t cost = -1;
-  for (int tall = 0; tall < 2; ++tall)
-    for (int s = 1; s <= kLinearMostSplits && s <= w.steps; ++s) {
+  const uint32_t all = w.steps > 1 ? (uint32_t)w.steps : 1;
+  for (int h = 0; h < 3; ++h) {
+    const uint32_t least = linear_copies(kLinearHeights[h]) + 1;
+    // of the numbers of runs that leave the longest the same steps the smallest
+    // costs least, and a run has `least` steps however few it is given
+    for (uint32_t s = 1; s <= kLinearMostSplits;) {
       if (s > 1 && s * w.results * 4 > kLinearMostPartial) break;
-      const int64_t c = linear_cost_ns(w, tall, s);
-      if (cost >= 0 && c >= cost) continue;
-      cost = c;
-      best.rows = tall ? 256 : 128;
-      best.splits = s;
-      best.items = w.most[tall] * s;
+      const uint32_t steps = (all + s - 1) / s;
+      const int64_t c = linear_cost_ns(w, h, s, steps > least ? steps : least);
+      if (cost < 0 || c < cost) {
+        cost = c;
+        best = {kLinearHeights[h], (int)s, w.most[h] * s};
+      }
+      if (steps <= least) break;
+      s = (all + steps - 2) / (steps - 1);
     }
+  }
   return best;
 }
 
@@ -80,12 +101,13 @@ inline LinearShape linear_best(const LinearWork& w) {
 // for all rows, whose tiles the host can count.  (An expert's last tile counts
 // as half; one that holds fewer rows than a tile has one.)
 inline LinearShape linear_shape(int64_t rows, int E, int cols, int deep, int64_t results) {
-  const int64_t units = (cols + kLinearCols - 1) / kLinearCols, held = E < rows ? E : rows;
+  const int64_t held = E < rows ? E : rows;
   LinearWork w = {};
-  for (int tall = 0; tall < 2; ++tall) {
-    const int64_t bm = tall ? 256 : 128, half = (2 * rows / bm + held) / 2;
-    w.tiles[tall] = units * (E == 1 ? (rows + bm - 1) / bm : half > held ? half : held);
-    w.most[tall] = units * (E == 1 ? (rows + bm - 1) / bm : rows / bm + held);
+  for (int h = 0; h < 3; ++h) {
+    const int64_t bm = kLinearHeights[h], bn = linear_cols((int)bm), units = (cols + bn - 1) / bn;
+    const int64_t half = (2 * rows / bm + held) / 2;
+    w.tiles[h] = units * (E == 1 ? (rows + bm - 1) / bm : half > held ? half : held);
+    w.most[h] = units * (E == 1 ? (rows + bm - 1) / bm : rows / bm + held);
   }
   w.steps = (deep + kLinearDeep - 1) / kLinearDeep;
   w.results = results;
@@ -94,11 +116,10 @@ inline LinearShape linear_shape(int64_t rows, int E, int cols, int deep, int64_t
 
 // wgrad: N x K results for each expert, sums over its rows.
 inline LinearShape wgrad_shape(int64_t rows, int E, int N, int K) {
-  const int64_t units = (K + kLinearCols - 1) / kLinearCols;
   LinearWork w = {};
-  for (int tall = 0; tall < 2; ++tall) {
-    const int64_t bm = tall ? 256 : 128;
-    w.tiles[tall] = w.most[tall] = E * ((N + bm - 1) / bm) * units;
+  for (int h = 0; h < 3; ++h) {
+    const int64_t bm = kLinearHeights[h], bn = linear_cols((int)bm);
+    w.tiles[h] = w.most[h] = E * ((N + bm - 1) / bm) * ((K + bn - 1) / bn);
   }
   w.steps = (rows / E + kLinearDeep - 1) / kLinearDeep;
   w.results = (int64_t)E * N * K;

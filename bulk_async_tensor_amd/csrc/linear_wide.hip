@@ -1,14 +1,15 @@
 // ep_grouped_linear and its gradients: a workgroup of 8 waves computes 256
-// columns x BM rows at a time from tiles that both sides' loads bring straight
-// into LDS.  (The column side is the one along which results lie in memory:
-// b's rows n in the forward product, b's columns in dgrad, a's columns in
-// wgrad; the row side the token rows, and in wgrad dy's columns n.)
+// columns x 128 or 256 rows at a time, one of 4 waves 128 x 64 where there is
+// little to do, from tiles that both sides' loads bring straight into LDS.  (The
+// column side is the one along which results lie in memory: b's rows n in the
+// forward product, b's columns in dgrad, a's columns in wgrad; the row side the
+// token rows, and in wgrad dy's columns n.)
 //
 // One step is 64 places along the sum: 64 products of 16 x 16 x 32 for each
-// of a wave's 128 x 64 results (BM = 256), 32 for 64 x 64.  The workgroups stay
-// (one per CU; its LDS is full) and run through their tiles as one stream of
-// steps, so that the next tile's loads are under way while a tile's last steps
-// and its results are done.  A step's tiles lie in one of two or three copies
+// of a wave's 128 x 64 results (256 rows), 32 for 64 x 64, 16 for 64 x 32.  The
+// workgroups stay (one per CU; its LDS is full, or half full) and run through
+// their tiles as one stream of steps, so that the next tile's loads are under
+// way while a tile's last steps and its results are done.  A step's tiles lie in one of two or three copies
 // in LDS, and each part of a copy is loaded anew as soon as every wave has read
 // it (see the two barriers of a step below).  The stream goes on loading past
 // its end (the last tile again), so that the waits can count the loads.
@@ -24,7 +25,8 @@
 // the same time on all CUs: 23000 cycles of a tile's 330000); its weights'
 // gradient 1.56 ms, 0.93 PFLOP/s (tiles of 12 steps, with 9000 cycles of 50000
 // spent on a tile's results and its first step).  A decode batch's down product
-// reads its weights at 6.1 TB/s.
+// reads its weights at 6.4 TB/s: 64 rows with 128 columns 1165 us, 128 with 256
+// 1217.
 //
 // A side that lies along the sum in memory (its rows are the tile's rows) has
 // LDS rows of 128 bytes, 8 chunks of 16; row r keeps chunk c at place
@@ -60,9 +62,6 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 enum Product { kForward, kDgrad, kWgrad };
 
-constexpr int kWaves = 8;
-constexpr int kCols = kLinearCols;  // columns per workgroup
-constexpr int kHalf = kCols / 2;    // the first and the second of them (swiglu: gate and up)
 constexpr int kDeep = kLinearDeep;  // places along the sum in a step
 constexpr int kStepBytes = 2 * kDeep;
 constexpr uint32_t kNowhere = 0x80000000u;  // past every buffer
@@ -70,16 +69,19 @@ constexpr int kMostItems = kLinearMostItems;
 
 template <int BM>
 struct Wide {
-  static constexpr int WN = BM == 256 ? 2 : 4;  // waves along the columns
-  static constexpr int WM = kWaves / WN;        // waves along the rows
-  static constexpr int HT = kHalf / 16 / WN;    // column tiles of a wave in each half
+  static constexpr int kCols = linear_cols(BM);  // columns per workgroup
+  static constexpr int kHalf = kCols / 2;        // the first and the second of them (swiglu: gate and up)
+  static constexpr int kWaves = BM == 64 ? 4 : 8;
+  static constexpr int WN = BM == 128 ? 4 : 2;   // waves along the columns
+  static constexpr int WM = kWaves / WN;         // waves along the rows
+  static constexpr int HT = kHalf / 16 / WN;     // column tiles of a wave in each half
   static constexpr int NT = 2 * HT;
   static constexpr int MT = BM / 16 / WM;  // row tiles of a wave
   static constexpr int kT = BM * kStepBytes, kStage = kT + kCols * kStepBytes;  // rows, then columns
   static constexpr int S = linear_copies(BM);  // copies: steps whose tiles are in LDS or on the way
   static constexpr int kLeast = S + 1;         // steps of a tile: the loads are S steps and one tile ahead at most
-  static constexpr int LT = BM / 64;           // load instructions of a wave a step: rows,
-  static constexpr int LW = kCols / 64;        // and columns
+  static constexpr int LT = BM / 8 / kWaves;     // load instructions of a wave a step: rows,
+  static constexpr int LW = kCols / 8 / kWaves;  // and columns
 };
 
 // A raw buffer of `bytes` at p: loads past its end bring zeros, stores go nowhere.
@@ -157,6 +159,7 @@ template <Product P, int ACT, int BM>
 __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearShape& shape) {
   using W = Wide<BM>;
   constexpr int HT = W::HT, NT = W::NT, MT = W::MT;
+  constexpr int kWaves = W::kWaves, kCols = W::kCols, kHalf = W::kHalf;
   constexpr bool kRowsAcross = P == kWgrad, kColsAcross = P != kForward;
   __shared__ __attribute__((aligned(1024))) uint8_t s_rows[W::S * W::kStage];
   __shared__ int32_t s_first[P == kWgrad ? 1 : kMaxExperts + 1];
@@ -192,10 +195,10 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   // Tiles of 256 rows: every XCD takes as many items as it has workgroups in
   // turn, so that what neighbouring items share passes by all of them within a
   // round (and wgrad's items, whose cost goes by their expert's rows, are spread
-  // evenly).  Tiles of 128, which mostly read weights: a run of items for each
-  // XCD.  us, in turn / runs: gate and up product of 49152 rows 2615 / 2695, the
-  // down product's gradient 1500 / 1535, a decode batch's down product (128)
-  // 1244 / 1222.
+  // evenly).  Lower tiles, which mostly read weights: a run of items for each XCD.
+  // us, in turn / runs: gate and up product of 49152 rows 2615 / 2695, the down
+  // product's gradient 1500 / 1535, a decode batch's down product (64) 1190 /
+  // 1165, (128) 1244 / 1222.
   const int run = (total + kXcds - 1) / kXcds;
   auto item_no = [&](int r) {
     if constexpr (P == kWgrad || BM == 256) return (r * kXcds + xcd) * slots + slot;
@@ -214,8 +217,8 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   constexpr int kRowUnits = BM / 8, kColUnits = kHalf / 8;  // 16-byte units in an LDS row across the sum
   auto across = [&](int units16, int ld, int i) -> uint32_t {  // offset of load i of a side across the sum
     const int ri = kWave / units16;  // rows of a load
-    const int r = wave * 8 + i * ri + lane / units16, u = lane % units16;
-    const int f = ((r & 3) | (wave & 3) << 2) & (units16 / 2 - 1);
+    const int r = wave * (kDeep / kWaves) + i * ri + lane / units16, u = lane % units16;
+    const int f = ((r & 3) | (r >> 3 & 3) << 2) & (units16 / 2 - 1);
     return (uint32_t)(r * ld * 2) + (((u >> 1) ^ f) * 2 + (u & 1)) * 16;
   };
   uint32_t r_at[W::LT], c_at[W::LW];
@@ -728,10 +731,10 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   wait_vmcnt<0>();  // no load may write this workgroup's LDS after its end
 }
 
-// One workgroup fills a CU's LDS: two waves per SIMD, 256 registers each.
-template <Product P, int ACT, int BM>
-__global__ __launch_bounds__(kWaves * kWave) __attribute__((amdgpu_waves_per_eu(2, 2))) void linear_wide_kernel(
-    LinearArgs g, LinearShape shape) {
+// One workgroup fills a CU's LDS: a wave or two per SIMD, 256 registers each.
+template <Product P, int ACT, int BM, int PER_SIMD = Wide<BM>::kWaves / 4>
+__global__ __launch_bounds__(Wide<BM>::kWaves * kWave) __attribute__((amdgpu_waves_per_eu(PER_SIMD, PER_SIMD))) void
+linear_wide_kernel(LinearArgs g, LinearShape shape) {
   linear_wide<P, ACT, BM>(g, shape);
 }
 
@@ -800,9 +803,11 @@ template <Product P, int ACT>
 hipError_t launch(const Budget& b, const LinearArgs& g, const LinearShape& s, hipStream_t stream) {
   const int grid = stay_grid(b, s.items);
   if (s.rows == 256)
-    hipLaunchKernelGGL((linear_wide_kernel<P, ACT, 256>), dim3(grid), dim3(kWaves * kWave), 0, stream, g, s);
+    hipLaunchKernelGGL((linear_wide_kernel<P, ACT, 256>), dim3(grid), dim3(Wide<256>::kWaves * kWave), 0, stream, g, s);
+  else if (s.rows == 128)
+    hipLaunchKernelGGL((linear_wide_kernel<P, ACT, 128>), dim3(grid), dim3(Wide<128>::kWaves * kWave), 0, stream, g, s);
   else
-    hipLaunchKernelGGL((linear_wide_kernel<P, ACT, 128>), dim3(grid), dim3(kWaves * kWave), 0, stream, g, s);
+    hipLaunchKernelGGL((linear_wide_kernel<P, ACT, 64>), dim3(grid), dim3(Wide<64>::kWaves * kWave), 0, stream, g, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || s.splits == 1) return e;
   const int wide = P == kForward ? (ACT == EP_ACT_SWIGLU ? g.N / 2 : g.N) : g.K;

@@ -11,6 +11,14 @@ UBF16 = 2.0 ** -8  # of bf16
 UNIT = {torch.float32: U32, torch.bfloat16: UBF16}
 
 
+# Rows, experts, K, N at which the products' rule takes tiles of 64, 128 and 256 rows, whole sums and cut ones, for
+# each product.
+HEIGHTS = [(1106, 1, 64, 64), (224, 20, 64, 1632), (5354, 5, 64, 2560), (5881, 9, 264, 2384), (2971, 1, 144, 3360),
+           (3834, 1, 2072, 64), (5589, 3, 264, 2656), (5492, 3, 2344, 288), (2696, 5, 3016, 144), (5493, 9, 3328, 272),
+           (5968, 3, 328, 1872), (3939, 1, 136, 1664), (5823, 3, 3608, 144), (110, 1, 1240, 64), (118, 1, 80, 1184),
+           (5470, 5, 296, 2864), (4481, 2, 280, 3040)]
+
+
 def routing(T, E, k, seed, drop=0.0, device="cpu"):
     g = torch.Generator().manual_seed(seed)
     ids = torch.rand(T, E, generator=g).argsort(1)[:, :k].to(torch.int32)

@@ -11,7 +11,8 @@ import bulk_async_tensor_amd as ep
 
 import layer_ref as ref
 from gpu_helpers import DEV
-from test_gpu_layer import (BF16, F32, check_dgrad, check_linear, check_route, check_wgrad, gen, logits_of, same, within)
+from test_gpu_layer import (BF16, F32, check_dgrad, check_linear, check_route, check_wgrad, gen, logits_of, same,
+                            within)
 
 pytestmark = pytest.mark.gpu
 
@@ -28,8 +29,8 @@ def eight_cus():
     ep.ep_stream_destroy(stream)
 
 
-# Sums of one to six steps (three copies or two in LDS, one step more in a tile at least), tiles of 128 rows and of
-# 256, and items that eight workgroups share in many rounds: rows of each expert, K, N.
+# Sums of one to six steps (three copies or two in LDS, one step more in a tile at least), tiles of 64, 128 and 256
+# rows, and items that eight workgroups share in many rounds: rows of each expert, K, N.
 STREAMS = [([500, 0, 130, 257, 64, 1], 64, 600), ([300, 700], 72, 2056), ([129] * 9, 128, 520), ([256] * 5, 200, 1000),
            ([4000, 5000], 64, 1288), ([3000] * 4, 192, 1040), ([2000, 0, 2500, 1], 264, 1544), ([9000], 384, 776),
            ([4000, 5000], 1288, 64), ([3000] * 4, 1040, 192), ([500, 0, 700, 10], 1032, 4104)]
@@ -54,6 +55,21 @@ def test_streams_of_tiles(counts, K, N, eight_cus):
     eight_cus.synchronize()
     for got, w in zip((y, dx, db, dbias), want):
         same(got, w)
+
+
+@pytest.mark.parametrize("act", ["none", "silu", "gelu", "swiglu"])
+@pytest.mark.parametrize("rows, E, K, N", ref.HEIGHTS)
+def test_every_height(rows, E, K, N, act):
+    """Tiles of 64, 128 and 256 rows, whole sums and cut ones, of each product."""
+    offsets = None if E == 1 else ep.ep_layout(ref.routing(rows, E, 1, 7, 0.02, DEV), E)["offsets"]
+    a, d, b = ref.rows(rows, K, 1, DEV), ref.rows(rows, N, 2, DEV), ref.weights(E, N, K, 3, DEV)
+    bias, swiglu = torch.randn(E, N, generator=gen(4), device=DEV), act == "swiglu"
+    check_linear(a, offsets, b, act, bias=bias, residual=ref.rows(rows, N // 2 if swiglu else N, 5, DEV), pre=True)
+    check_linear(a, offsets, b, act, F32)
+    check_dgrad(d, offsets, b, act, None if act == "none" else ref.rows(rows, 2 * K if swiglu else K, 6, DEV, 2.0))
+    if act == "none":
+        check_wgrad(d, a, offsets, E)
+        check_wgrad(d, a, offsets, E, BF16, bias=False)
 
 
 def test_rows_past_4_gib():
@@ -251,7 +267,8 @@ def test_route_many_tokens_close(E, kind):
     odd = near.clone()
     odd[5], odd[6], odd[7] = -inf, torch.finfo(F32).min, nan
     for over in (dict(), dict(bias=near), dict(bias=odd), dict(groups=8, top_groups=3, group_best=2),
-                 dict(bias=near, groups=8, top_groups=3, group_best=2), dict(bias=odd, groups=4, top_groups=2, group_best=2)):
+                 dict(bias=near, groups=8, top_groups=3, group_best=2),
+                 dict(bias=odd, groups=4, top_groups=2, group_best=2)):
         for renorm in (False, True):
             idx, _ = check_route(l, k, kind, renormalize=renorm, **over)
             assert bool((idx.sort(1).values.diff(dim=1) > 0).all()) and bool((idx >= 0).all()) and bool((idx < E).all())
@@ -260,7 +277,8 @@ def test_route_many_tokens_close(E, kind):
 # ------------------------------------------------------------------ what follows a product
 @pytest.mark.parametrize("act", ["none", "silu", "gelu", "swiglu"])
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("rows, E, K, N", [(300, 3, 128, 400), (40, 2, 2048, 272)])
+@pytest.mark.parametrize("rows, E, K, N", [(300, 3, 128, 400), (40, 2, 2048, 272), (2000, 2, 1536, 1040),
+                                           (900, 2, 4096, 1040), (3000, 3, 128, 2704), (5493, 9, 3328, 272)])
 def test_every_epilogue(rows, E, K, N, dtype, act):
     """Bias, residual and pre in all combinations, on whole sums and on cut ones."""
     first = rows // E + 1
@@ -293,7 +311,8 @@ def test_activations_over_their_range(act):
     y = torch.full((3, n), 77.0, device=DEV)
     ep.ep_grouped_linear(a, None, b, y, bias=z.view(1, -1), act=act)
     want = ref.act(act, g) * u
-    within(y, want.expand(3, n), ((g * g + g.abs() + 24) * ref.U32 * want.abs() + 2.0 ** -120 * u.abs()).expand(3, n), "y")
+    bound = (g * g + g.abs() + 24) * ref.U32 * want.abs() + 2.0 ** -120 * u.abs()
+    within(y, want.expand(3, n), bound.expand(3, n), "y")
     pre, dy = z.to(BF16).expand(3, -1).contiguous(), ref.rows(3, 8, 5, DEV)
     ones = torch.ones(1, 8, n, dtype=BF16, device=DEV)
     dx = torch.full(pre.shape, 77.0, dtype=BF16, device=DEV)
