@@ -243,9 +243,7 @@ __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp
 template <int L, int NV, bool BF16>
 struct RouteShape {
   static constexpr int kTokens = kWave / L;             // of a wave
-  // floats of LDS for a token: scores, a place between groups, and 8 that set the
-  // tokens of a wave on banks of their own
-  static constexpr int kScores = L * NV + kMaxGroups + 8;
+  static constexpr int kScores = L * NV + kMaxGroups;   // floats of LDS for a token: scores, a place between groups
   static constexpr int kFloats = kTokens * (kScores + kMaxGroups);
   static constexpr int kLds = kFloats * 4 > L * NV * 8 ? kFloats * 4 : L * NV * 8;  // (and the exact path's scores)
 };
@@ -362,7 +360,6 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(RouteArgs a,
     for (int g = sub; g < a.groups; g += L) {
       float v1 = -INFINITY, v2 = -INFINITY;
       const float* p = s_c + g * (per + 1);
-#pragma unroll 8
       for (int i = 0; i < per; ++i) {
         const float v = p[i];
         v2 = fmaxf(v2, fminf(v1, v));
