@@ -447,7 +447,8 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(RouteArgs a,
     sure = certain(slots) >> (a.k - 1);
     const int before = a.k + (sure ? __builtin_ctzll(sure) : L);
     again |= before >= slots;
-    const double x = !scores ? (double)lj : sigmoid64((double)lj) + (double)bj;
+    // (Without a bias by the logits: from about 24 on the sigmoids of neighbouring ones are equal in float64.)
+    const double x = a.bias ? sigmoid64((double)lj) + (double)bj : (double)lj;
     const bool in = sub < before;
     place = in ? 0 : L;
     for (int i = 0; i < slots; ++i) {
