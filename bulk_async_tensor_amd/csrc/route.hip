@@ -359,17 +359,27 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(RouteArgs a,
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     for (int g = sub; g < a.groups; g += L) {
       float v1 = -INFINITY, v2 = -INFINITY;
-      const float* p = s_c + g * (per + 1);
+      float* p = s_c + g * (per + 1);
       for (int i = 0; i < per; ++i) {
         const float v = p[i];
         v2 = fmaxf(v2, fminf(v1, v));
         v1 = fmaxf(v1, v);
       }
-      s_rank[g] = a.group_best == 2 ? v1 + v2 : v1;
+      const bool two = a.group_best == 2;
+      s_rank[g] = two ? v1 + v2 : v1;
+      // What the rank may be off by, in the place of the group's first score,
+      // which is not read again: the scores' errors (half of score_error each),
+      // half a step for a bias added to each at its own size, which may be far
+      // above the sum's, half a step for the sum, and as much again for the
+      // sums with this bound below.
+      p[0] = two ? score_error + (fabsf(v1) + fabsf(v2)) * 0x1p-22f : 0.5f * score_error + fabsf(v1) * 0x1p-23f;
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     uint64_t kept = 0;
-    float worst = INFINITY, next = -INFINITY;  // of the groups kept, and the best of the others
+    // The least that a kept group's rank can be, and the most that another's
+    // can.  (Of a kept +infinity and of another's -infinity that is NaN, which
+    // fminf and fmaxf pass over: nothing is above the one or below the other.)
+    float worst = INFINITY, next = -INFINITY;
     for (int g0 = 0; g0 < a.groups; g0 += L) {
       const int g = g0 + sub;
       const float mine = g < a.groups ? s_rank[g] : -INFINITY;
@@ -379,14 +389,14 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(RouteArgs a,
         before += r > mine || (r == mine && o < g);
       }
       const bool keep = before < a.top_groups;
-      if (keep) worst = fminf(worst, mine);
-      else next = fmaxf(next, mine);
+      const float off = g < a.groups ? s_c[g * (per + 1)] : 0.0f;
+      if (keep) worst = fminf(worst, mine - off);
+      else next = fmaxf(next, mine + off);
       kept |= token_bits<L>(ballot(keep), lane) << g0;
     }
     worst = -lanes_max<L>(-worst);
     next = lanes_max<L>(next);
-    // (sums of two: twice the scores' error, and their own rounding)
-    again |= a.top_groups < a.groups && !(worst - next > 2.0f * score_error + 0x1p-21f * fmaxf(fabsf(worst), fabsf(next)));
+    again |= a.top_groups < a.groups && !(worst > next);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const uint32_t e = e0 + i;

@@ -1,13 +1,14 @@
-"""ep_route where scores are closer than float32 or float64 holds, against 64 bits
-(layer_ref.py)."""
+"""ep_route where scores or group ranks are closer than float32 holds, against 64
+bits (layer_ref.py)."""
 
 import math
 
 import pytest
 import torch
 
+import layer_ref as ref
 from gpu_helpers import DEV
-from test_gpu_layer import BF16, F32, check_route, logits_of
+from test_gpu_layer import BF16, F32, check_route, gen, logits_of
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +44,48 @@ def test_saturated_scores_of_several_groups(T, dtype, start):
         l = l.to(dtype)
         check_route(l, k, "sigmoid", groups=8, top_groups=2, group_best=2)
         check_route(l, k, "sigmoid", renormalize=False, groups=4, top_groups=1, group_best=1)
+
+
+def decided(l, kind, bias, groups, top):
+    """Rows whose group ranks, sums of two, 64 bits tell apart at the edge of the groups that stay.  A score there is off
+    by 4 half steps of 1, a bias added to it by half a step of the sum, twice, and their sum by half a step of at most
+    both sizes: two ranks differ for certain from 16 half steps of (1 + the two sizes) on."""
+    c = (ref.scores(kind, l.cpu()) + bias.cpu().double()).view(l.shape[0], groups, -1)
+    two = c.topk(2, dim=2).values
+    rank, order = two.sum(2).sort(1, descending=True)
+    size = torch.gather(1.0 + two.abs().sum(2), 1, order)
+    return rank[:, top - 1] - rank[:, top] > 16 * 2.0 ** -53 * (size[:, top - 1] + size[:, top])
+
+
+@pytest.mark.parametrize("T", [500, MANY])
+@pytest.mark.parametrize("size", [10.0, 64.0, 1024.0])
+def test_group_ranks_whose_biases_cancel(T, size):
+    """A group's two best scores with biases of opposite sign: their sum is close to another group's, and each of
+    them is rounded at its own size."""
+    E, groups = 128, 8
+    l = logits_of(T, E, 1)
+    apart = torch.randn(T, generator=gen(2), device=DEV).sign() * 10.0 ** (-7.5 + 4 * torch.rand(T, generator=gen(3), device=DEV))
+    l[:, 16] = l[:, 0] + apart
+    l[:, 17] = l[:, 1]
+    bias = torch.full((E,), -4.0 * size, device=DEV)
+    bias[0], bias[1], bias[16], bias[17] = size, -size, 0.0, 0.0
+    for kind in ("sigmoid", "softmax"):
+        for b, top in ((bias, 1), (bias.flip(0).contiguous(), 7)):
+            sure = decided(l, kind, b, groups, top)
+            assert int(sure.sum()) >= 0.8 * T  # (float32 loses what is below 10^-6.9: 0.6 of the 4 decades)
+            check_route(l[sure.to(DEV)], 2, kind, bias=b, groups=groups, top_groups=top, group_best=2)
+
+
+def test_group_ranks_at_the_ends():
+    """Biases of infinite size and sums past float32's range."""
+    T, E = 200, 64
+    l = logits_of(T, E, 1)
+    inf = math.inf
+    for a, b in ((-inf, 0.0), (inf, 0.0), (inf, -inf), (3e38, 3e38), (-3e38, 3e38), (-3e38, -3e38), (inf, inf)):
+        bias = torch.zeros(E, device=DEV)
+        bias[3], bias[4], bias[20] = a, b, a
+        for top in (1, 2, 3):
+            check_route(l, 4, "sigmoid", bias=bias, groups=8, top_groups=top, group_best=2)
+    bias = torch.full((E,), -inf, device=DEV)  # (experts left out by their bias, whole groups of them)
+    bias[8:20] = 0.01
+    check_route(l, 4, "sigmoid", bias=bias, groups=8, top_groups=2, group_best=2)
