@@ -438,8 +438,9 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(RouteArgs a,
     const int up = sub + 1 < L ? lane + 1 : lane;
     const float cn = __shfl(cj, up, kWave), ln = __shfl(lj, up, kWave), bn = __shfl(bj, up, kWave);
     const int en = __shfl(mine, up, kWave);
-    // a key's cell is 2 NV steps of float32, the sums' roundings two
-    const float margin = fmaxf(fabsf(cj), fabsf(cn)) * (2.0f * NV + 2.0f) * 0x1p-23f + score_error;
+    // a key's cell is 2 NV steps of float32 (below its least normal number of
+    // 2^-149 each), the sums' roundings two
+    const float margin = fmaxf(fmaxf(fabsf(cj), fabsf(cn)), 0x1p-126f) * (2.0f * NV + 2.0f) * 0x1p-23f + score_error;
     const bool clear = en < 0 || (sub < a.k - 1 && lj == ln && bj == bn) || (cn == -INFINITY && cj > cn) || cj - cn > margin;
     return token_bits<L>(ballot(clear), lane);
   };

@@ -8,7 +8,7 @@ import torch
 
 import layer_ref as ref
 from gpu_helpers import DEV
-from test_gpu_layer import BF16, F32, check_route, gen, logits_of
+from test_gpu_layer import BF16, F32, call_route, check_route, gen, logits_of
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +89,23 @@ def test_group_ranks_at_the_ends():
     bias = torch.full((E,), -inf, device=DEV)  # (experts left out by their bias, whole groups of them)
     bias[8:20] = 0.01
     check_route(l, 4, "sigmoid", bias=bias, groups=8, top_groups=2, group_best=2)
+
+
+def subnormal(steps):
+    """Float32 values of so many steps of 2^-149."""
+    size = steps.abs().to(torch.int32)
+    return torch.where(steps < 0, size | torch.iinfo(torch.int32).min, size).view(torch.float32).to(DEV)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T, E, k", [(1, 4, 1), (300, 64, 4), (300, 256, 8), (MANY, 256, 8), (MANY, 512, 8)])
+def test_subnormal_logits(T, E, k, kind):
+    """Logits of a few steps of 2^-149: a key's cell there is as wide as the values themselves."""
+    l = subnormal(torch.tensor([3, 1, 5, 0])).repeat(T, 1)
+    idx, _ = call_route(l, 1, kind)
+    assert bool((idx == 2).all())
+    g = torch.Generator().manual_seed(E)
+    for most in (2, 8, 1 << 10, 1 << 22):
+        check_route(subnormal(torch.randint(-most, most + 1, (T, E), generator=g)), k, kind)
+        few = torch.where(torch.rand(T, E, generator=g) < 0.02, torch.randint(1, most + 1, (T, E), generator=g), 0)
+        check_route(subnormal(few), k, kind)
