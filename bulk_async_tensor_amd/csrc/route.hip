@@ -558,7 +558,8 @@ __device__ __forceinline__ void route_back(const RouteBackwardArgs& a, int64_t t
   const float D = a.renorm || !a.sigmoid ? wave_sum(p * dw) : 0.0f;
   // the slot's own part (dense: without the part that every expert has)
   float g = dense ? p * dw : p * (dw - D);
-  if (a.sigmoid) g *= 1.0f - sig;
+  // (1 - s in a form that keeps its digits where s is nearly 1)
+  if (a.sigmoid) g *= 1.0f / (1.0f + expf(l));
   if (!here) g = 0.0f;
   for (int base = 0; base < E; base += kWave) {
     const int i = base + lane;

@@ -1,10 +1,12 @@
-"""ep_route where scores or group ranks are closer than float32 holds, against 64
-bits (layer_ref.py)."""
+"""ep_route where scores or group ranks are closer than float32 holds, and
+ep_route_backward where a sigmoid is nearly one, against 64 bits (layer_ref.py)."""
 
 import math
 
 import pytest
 import torch
+
+import bulk_async_tensor_amd as ep
 
 import layer_ref as ref
 from gpu_helpers import DEV
@@ -109,3 +111,30 @@ def test_subnormal_logits(T, E, k, kind):
         check_route(subnormal(torch.randint(-most, most + 1, (T, E), generator=g)), k, kind)
         few = torch.where(torch.rand(T, E, generator=g) < 0.02, torch.randint(1, most + 1, (T, E), generator=g), 0)
         check_route(subnormal(few), k, kind)
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_gradient_of_a_sigmoid_near_one(out, renorm):
+    """dl = scale p (1 - s) (dw - D) relative to its own size.  In half steps of float32: exp costs 2, the sum and the
+    quotient after it 2, so s and 1 - s are 4 off; p, divided by a sum over k = 4, 12; D, a sum of p dw, 16; the
+    difference is 1 + 16 off relative to |dw| + |D|, and four products add 4: 12 + 4 + 17 + 4 = 37."""
+    T, E, k = 400, 32, 4
+    l = torch.rand(T, E, generator=gen(1), device=DEV) * 75.0 + 5.0
+    l[: T // 2] = torch.rand(T // 2, 1, generator=gen(2), device=DEV) * 25.0 + 5.0 + l[: T // 2] * 0.01
+    l[-20:] = -l[-20:]
+    idx, _ = call_route(l, k, "sigmoid")
+    dw = torch.randn(T, k, generator=gen(3), device=DEV)
+    dl = torch.full((T, E), 7.0, dtype=out, device=DEV)
+    ep.ep_route_backward(l, idx, dw, dl, score="sigmoid", renormalize=renorm, scale=2.5)
+    l, at, dw = l.cpu().double(), idx.cpu().long(), dw.cpu().double()
+    lj = torch.gather(l, 1, at)
+    s, rest = torch.sigmoid(lj), 1.0 / (1.0 + torch.exp(lj))
+    p = s / s.sum(1, keepdim=True) if renorm else s
+    D = (p * dw).sum(1, keepdim=True) if renorm else torch.zeros(T, 1, dtype=torch.float64)
+    want = torch.zeros(T, E, dtype=torch.float64).scatter_(1, at, 2.5 * p * rest * (dw - D))
+    size = torch.zeros(T, E, dtype=torch.float64).scatter_(1, at, 2.5 * p * rest * (dw.abs() + D.abs()))
+    err = (dl.cpu().double() - want).abs()
+    tol = 37 * ref.U32 * size
+    tol = tol + ref.UNIT[out] * (want.abs() + tol) + 2.0 ** -133
+    assert bool((err <= tol).all()), float((err / tol.clamp_min(1e-300)).max())
