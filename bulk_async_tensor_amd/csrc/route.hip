@@ -124,13 +124,14 @@ __device__ __forceinline__ double sigmoid64(double l) {
   return (l < 0.0 ? e : 1.0) / (1.0 + e);
 }
 
-// One token by one wave, scores in float64.  s_c: E doubles of LDS, the lane's
-// experts e = lane, lane + 64, ...: held there and not in registers, which the
-// path that nearly every token takes would lack.
-__device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t t, int lane, double* s_c) {
+// One token by one wave, scores in float64.  s_bits: 8 E bytes of LDS, the
+// lane's experts e = lane, lane + 64, ...: held there and not in registers,
+// which the path that nearly every token takes would lack.  First a score's
+// bits, then the key that orders as it does: one type, so that the compiler
+// keeps the stores of one before those of the other.
+__device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t t, int lane, int64_t* s_bits) {
   const int E = a.E;
   const int64_t row = t * E;
-  int64_t* const s_key = reinterpret_cast<int64_t*>(s_c);
   double top = -INFINITY, total = 0.0;
   if (!a.sigmoid) {
 #pragma unroll 4
@@ -146,12 +147,13 @@ __device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t t, int l
   for (int e = lane; e < E; e += kWave) {
     const double l = (double)logit_at(a.logits, a.bf16, row + e);
     const double x = a.sigmoid ? sigmoid64(l) : none ? 0.0 : exp(l - top);
-    s_c[e] = x;
+    s_bits[e] = __double_as_longlong(x);
     total += x;
   }
   total = a.sigmoid || none ? 1.0 : wave_sum(total);
 #pragma unroll 4
-  for (int e = lane; e < E; e += kWave) s_c[e] = s_c[e] / total + (a.bias ? (double)a.bias[e] : 0.0);
+  for (int e = lane; e < E; e += kWave)
+    s_bits[e] = __double_as_longlong(__longlong_as_double(s_bits[e]) / total + (a.bias ? (double)a.bias[e] : 0.0));
   uint64_t kept = ~0ull;
   const int per = E / a.groups;
   if (a.groups > 1) {
@@ -161,7 +163,7 @@ __device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t t, int l
       int64_t k1 = kGone, k2 = kGone;
       double v1 = 0.0, v2 = 0.0;
       for (int i = 0; i < per; ++i) {
-        const double v = s_c[lane * per + i];
+        const double v = __longlong_as_double(s_bits[lane * per + i]);
         const int64_t k = order_of(v);
         if (k > k1) {
           k2 = k1, v2 = v1;
@@ -184,23 +186,23 @@ __device__ __forceinline__ void route_exact(const RouteArgs& a, int64_t t, int l
   }
 #pragma unroll 4
   for (int e = lane; e < E; e += kWave)
-    s_key[e] = kept >> (a.groups > 1 ? e / per : 0) & 1
-                   ? order_of(a.bias ? s_c[e] : (double)logit_at(a.logits, a.bf16, row + e))
-                   : kGone;
+    s_bits[e] = kept >> (a.groups > 1 ? e / per : 0) & 1
+                    ? order_of(a.bias ? __longlong_as_double(s_bits[e]) : (double)logit_at(a.logits, a.bf16, row + e))
+                    : kGone;
   int mine = 0;  // lane j: the expert of slot j
   for (int j = 0; j < a.k; ++j) {
     int64_t best = kGone;
     int at = INT32_MAX;
 #pragma unroll 4
     for (int e = lane; e < E; e += kWave) {
-      const int64_t k = s_key[e];
+      const int64_t k = s_bits[e];
       if (k > best) {
         best = k;
         at = e;
       }
     }
     wave_best(best, at);
-    if (lane == (at & (kWave - 1))) s_key[at] = kGone;
+    if (lane == (at & (kWave - 1))) s_bits[at] = kGone;
     if (lane == j) mine = at;
   }
   // ---- the weights
@@ -498,7 +500,7 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(RouteArgs a,
     const int at = __builtin_ctzll(left);
     left &= left - 1;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    route_exact(a, t0 + at / L, lane, reinterpret_cast<double*>(s_all[wave]));
+    route_exact(a, t0 + at / L, lane, reinterpret_cast<int64_t*>(s_all[wave]));
   }
 }
 
