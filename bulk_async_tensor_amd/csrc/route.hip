@@ -372,9 +372,9 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(RouteArgs a,
       // What the rank may be off by, in the place of the group's first score,
       // which is not read again: the scores' errors (half of score_error each),
       // half a step for a bias added to each at its own size, which may be far
-      // above the sum's, half a step for the sum, and as much again for the
-      // sums with this bound below.
-      p[0] = two ? score_error + (fabsf(v1) + fabsf(v2)) * 0x1p-22f : 0.5f * score_error + fabsf(v1) * 0x1p-23f;
+      // above the sum's, half a step for the sum and half a step for the sums
+      // with this bound below (3 of 2^-24, 3.125 with what this line rounds).
+      p[0] = two ? score_error + (fabsf(v1) + fabsf(v2)) * 0x1.9p-23f : 0.5f * score_error + fabsf(v1) * 0x1.1p-23f;
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     uint64_t kept = 0;
