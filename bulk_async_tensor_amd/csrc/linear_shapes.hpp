@@ -10,7 +10,7 @@ constexpr int kLinearDeep = 64;            // places along the sum in a step
 constexpr int kLinearCus = 256;            // compute units that a call's work is cut for
 constexpr int kLinearMostItems = 1 << 30;  // items of a call
 constexpr int kLinearMostSplits = 64;
-constexpr int64_t kLinearMostPartial = (int64_t)64 << 20;  // bytes of results of cut sums
+constexpr int64_t kLinearMostPartial = (int64_t)64 << 20;  // bytes that cut sums store
 
 // A tile's columns, by its rows.
 constexpr int linear_cols(int rows) { return rows == 64 ? 128 : 256; }
@@ -56,7 +56,8 @@ struct LinearWork {
   int64_t tiles[3];   // tiles there may be expected to be with 64, 128 and 256 rows,
   int64_t most[3];    // and at most
   int64_t steps;      // of a tile's sum
-  int64_t results;    // float32 values of a run's results
+  int64_t results;    // float32 values of a run's results,
+  int64_t stored;     // and with the bias's sums, which wgrad keeps beside them
   bool wgrad;
 };
 
@@ -83,7 +84,7 @@ inline LinearShape linear_best(const LinearWork& w) {
     // of the numbers of runs that leave the longest the same steps the smallest
     // costs least, and a run has `least` steps however few it is given
     for (uint32_t s = 1; s <= kLinearMostSplits;) {
-      if (s > 1 && s * w.results * 4 > kLinearMostPartial) break;
+      if (s > 1 && s * w.stored * 4 > kLinearMostPartial) break;
       const uint32_t steps = (all + s - 1) / s;
       const int64_t c = linear_cost_ns(w, h, s, steps > least ? steps : least);
       if (cost < 0 || c < cost) {
@@ -110,7 +111,7 @@ inline LinearShape linear_shape(int64_t rows, int E, int cols, int deep, int64_t
     w.most[h] = units * (E == 1 ? (rows + bm - 1) / bm : rows / bm + held);
   }
   w.steps = (deep + kLinearDeep - 1) / kLinearDeep;
-  w.results = results;
+  w.results = w.stored = results;
   return linear_best(w);
 }
 
@@ -123,6 +124,7 @@ inline LinearShape wgrad_shape(int64_t rows, int E, int N, int K) {
   }
   w.steps = (rows / E + kLinearDeep - 1) / kLinearDeep;
   w.results = (int64_t)E * N * K;
+  w.stored = (int64_t)E * N * (K + 1LL);
   w.wgrad = true;
   return linear_best(w);
 }
