@@ -39,8 +39,11 @@ __device__ __forceinline__ Segment segment_of(const int32_t* __restrict__ offset
 constexpr int kTilesCap = 1 << 29;
 
 // first[e] = tiles before expert e, first[E] = all of them.  One wave.  (64
-// experts' tiles fit 30 bits: BM is 128 or more where there are more than 80
-// rows for each expert, 81920 with EP_MAX_EXPERTS of them.)
+// experts' tiles and kTilesCap before them fit 31 bits, though each may hold
+// every row: BM is 128 or more wherever there are more than 2^22 rows.  The
+// 8-bit products take less for up to 80 rows an expert, 81920 with
+// EP_MAX_EXPERTS of them, the bf16 products where the CUs would otherwise make
+// a few rounds only, up to about 1.4 million.)
 template <int BM>
 __device__ __forceinline__ void first_tiles(const int32_t* __restrict__ offsets, int E, int rows, int lane,
                                             int32_t* first) {
