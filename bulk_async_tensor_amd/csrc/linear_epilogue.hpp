@@ -33,11 +33,13 @@ __device__ __forceinline__ float exp_of(float z) { return __builtin_amdgcn_exp2f
 // hardware's reciprocal, one step off, for the 10 instructions of a division.)
 __device__ __forceinline__ float sigmoid_of(float z) { return __builtin_amdgcn_rcpf(1.0f + exp_of(-z)); }
 
-// (1 + erf(z / sqrt 2)) / 2, to a few steps of float32 relative to its value
-// far below zero too.  With x = |z| / sqrt 2 and t = 1 / (1 + x / 3),
+// (1 + erf(z / sqrt 2)) / 2.  With x = |z| / sqrt 2 and t = 1 / (1 + x / 3),
 //   erfc(x) = t exp(-x^2 + p(t)),
 // p of degree 9 fitted to log(erfc(x) exp(x^2) / t) over x in [0, 10], where it
-// is 1.5e-8 off.  22 instructions for the library function's 100.
+// is 1.5e-8 off.  22 instructions for the library function's 100.  Far below
+// zero the rounding of the argument shows, of which exp makes z^2 / 2 half
+// steps and more: relative to its value it is 4 steps of float32 off at -1, 9 at
+// -5, 33 at -10 and 63 at -13, a five-hundredth of a bf16 rounding.
 __device__ __forceinline__ float normal_cdf(float z) {
   const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.23570226f, 1.0f));
   float p = fmaf(-0.311686669f, t, 1.56484535f);

@@ -731,7 +731,9 @@ __device__ __forceinline__ void linear_wide(const LinearArgs& g, const LinearSha
   wait_vmcnt<0>();  // no load may write this workgroup's LDS after its end
 }
 
-// One workgroup fills a CU's LDS: a wave or two per SIMD, 256 registers each.
+// One workgroup a CU: of 128 and 256 rows it takes 156 and 140 KiB of LDS and
+// puts two waves on a SIMD, of 256 registers each; of 64 rows 84 KiB and one
+// wave, which may have 512 registers and uses 110 to 150.
 template <Product P, int ACT, int BM, int PER_SIMD = Wide<BM>::kWaves / 4>
 __global__ __launch_bounds__(Wide<BM>::kWaves * kWave) __attribute__((amdgpu_waves_per_eu(PER_SIMD, PER_SIMD))) void
 linear_wide_kernel(LinearArgs g, LinearShape shape) {

@@ -17,8 +17,8 @@
  *   ep_grouped_gemm_fp8   down product, bf16 expert outputs
  *   ep_combine            the gate-weighted sum back in token order
  *
- * and, training on bf16 rows (ep_dispatch; the experts' products and their
- * backward are the caller's), the way back:
+ * and, training on bf16 rows (ep_dispatch; the experts' products in bf16 and
+ * their backward are in ep_layer.h), the way back:
  *
  *   ep_combine_backward   dout -> gradient of the expert rows and the routing
  *                         weights

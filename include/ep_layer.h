@@ -70,12 +70,12 @@ enum { EP_ACT_NONE = 0, EP_ACT_SILU = 1, EP_ACT_GELU = 2, EP_ACT_SWIGLU = 3 };
  * and sums that float32 cannot tell apart are compared in float64.  The
  * weights are float32; a renormalised weight is formed without passing through
  * scores that underflow, so logits of -200 still share their weight.
- * A NaN counts as larger than any number (c is NaN with its logit or bias); its
- * weight is NaN, and so is every weight of a softmax over a row that holds a
- * NaN or +infinity.  A logit of -infinity has score 0 (a masked expert): it is
- * chosen last, with weight 0, and a row of nothing else gets weights 0 and the
- * lowest indices.  The chosen indices are distinct and in range whatever the
- * logits hold.
+ * A NaN counts as larger than any number (c is NaN with its logit or bias).  The
+ * weight of a NaN logit is NaN, and so are those divided by a sum with it and
+ * every weight of a softmax over a row that holds a NaN or +infinity.  A logit of -infinity has score 0 and weight 0 (a masked
+ * expert).  Without a bias it is chosen last, and a row of nothing else gets the
+ * lowest indices; with one it is compared by its bias alone.  The chosen indices
+ * are distinct and in range whatever the logits hold.
  *   logits     [T, E] of logits_type (EP_BF16 or EP_F32), aligned to its element
  *   bias       float32 [E] or NULL
  *   topk_idx   int32 [T, k],  topk_w float32 [T, k]: as ep_layout and
