@@ -29,9 +29,10 @@ struct LinearShape {
 // The shape is the one whose estimated time is least: the CUs make whole rounds
 // of items, a tile takes its steps and some time beside them, and a cut sum
 // costs a second kernel, 6 us, and its results their way to memory and back, 2.6
-// bytes a picosecond.  The times are set so that over 1480 random sizes (1 to
-// 8000 rows, 1 to 64 experts, sides of 64 to 8192) the rule's choice takes 1.3 %
-// longer than the best of those tried (heights, 1 to 16 runs) on average.
+// bytes a picosecond.  The times are set so that over 1474 random sizes (1 to
+// 8000 rows, 1 to 64 experts, sides of 64 to 8192) the rule's choice takes 1.2 %
+// longer than the best of those tried (heights, 1 to 16 runs) on average, and
+// 4 % of the sizes more than 10 % longer.
 // Measured, us, by rows / runs (the rule's choice first):
 //   128 rows, K 7168, N 256 (a router)      64/28 13.4   64/14 13.9   128/28 17.3
 //   512 rows of it                          64/16 16.0   64/4 19.7    128/8 24.0

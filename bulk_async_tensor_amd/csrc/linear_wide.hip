@@ -14,19 +14,20 @@
 // it (see the two barriers of a step below).  The stream goes on loading past
 // its end (the last tile again), so that the waits can count the loads.
 //
-// What bounds it.  49152 rows, 64 experts, K 7168, I 2048, with SwiGLU and the
-// values before it kept: 2.58 ms, 1.12 PFLOP/s, 70 % of what a bf16 library
-// product of 16384^3 reaches (1.59); the matrix cores are busy 60 % of the
-// cycles.  It is the chip's power: without its loads from memory, its LDS reads
-// or both the same products run at 2.0, 1.75 and 2.1 GHz instead of 1.7, and
-// experts of equal rows, whose operands are found in L2 more often (misses 27 %
-// of the requests instead of 42 %), take 2.39 ms.  The down product's gradient
-// 1.48 ms, 0.97 PFLOP/s (its tiles read and write 512 KiB beside the product, at
-// the same time on all CUs: 23000 cycles of a tile's 330000); its weights'
-// gradient 1.56 ms, 0.93 PFLOP/s (tiles of 12 steps, with 9000 cycles of 50000
-// spent on a tile's results and its first step).  A decode batch's down product
-// reads its weights at 6.4 TB/s: 64 rows with 128 columns 1165 us, 128 with 256
-// 1217.
+// What bounds it (kernel times; clock and counters with the profiler beside).
+// 49152 rows, 64 experts, K 7168, I 2048, with SwiGLU and the values before it
+// kept: 2.62 ms, 1.10 PFLOP/s, 69 % of what a bf16 library product of 16384^3
+// reaches (1.59).  The clock is down to 1.88 GHz under this load, and the matrix
+// cores are busy 56 % of its cycles: a step takes 2500 to 2900 for 2048 of
+// products, and a tile's results and first step 9000 to 13000 and 4000 more.
+// 35 % of the L2 requests miss and bring 8.3 GB; experts of equal rows, where
+// 27 % do and bring 5.4 GB, take 2.30 ms.  The down product's gradient 1.52 ms,
+// 0.95 PFLOP/s (its tiles read and write 512 KiB beside the product, at the same
+// time on all CUs: results and first step 22000 to 28000 cycles and 11000 to
+// 15000 more, of a tile's 340000); its weights' gradient 1.59 ms, 0.91 PFLOP/s
+// (steps of 3300 to 4400 cycles, both sides turned, and 9000 of a tile's 57000
+// on its results and its first step).  A decode batch's down product reads its
+// weights at 6.4 TB/s: 64 rows with 128 columns 1165 us, 128 with 256 1217.
 //
 // A side that lies along the sum in memory (its rows are the tile's rows) has
 // LDS rows of 128 bytes, 8 chunks of 16; row r keeps chunk c at place

@@ -20,12 +20,13 @@
 // and half a maximum a key); four exchanges give the token's largest value, a
 // ballot the first lane that holds it (of equal values the lowest expert).
 //
-// us, kernel alone: 128 tokens of 256 experts in 8 groups, k 8 6.5; 16384 of
-// them 17.7 (without groups 10.6), 17.8 MB or 1.0 TB/s: 12 are the scores,
+// us, kernel alone: 128 tokens of 256 experts in 8 groups, k 8 6.7; 16384 of
+// them 17.8 (without groups 10.6), 17.8 MB or 1.0 TB/s: 12 are the scores,
 // groups and nine rounds of choosing, the rest a token or two that float64
 // decides, one load and one exchange after another; 16384 tokens of 64 experts
-// in bf16, k 6, 5.5.  The gradient: 4096 tokens of 256 experts 7.6, 8191 of 60
-// 6.9, load latency.
+// in bf16, k 6, 5.6.  The gradient: 4096 tokens of 256 experts 7.6, 8191 of 60
+// 6.9: load latency, and for each 64 experts 2 k exchanges and a store of 2 or 4
+// bytes a lane.
 #include <math.h>
 
 #include "ep.h"
