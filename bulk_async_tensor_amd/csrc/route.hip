@@ -314,8 +314,10 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(RouteArgs a,
   // What the scores may be off by, twice.  Sigmoid, in half steps of 1: exp's
   // argument loses 1.22 |l|, exp itself 2, of which the sigmoid's slope leaves
   // 0.27 and 0.5, and the sum and the reciprocal add 3: 3.8, twice 2^-21.
-  // Softmax: the sum's roundings, NV and a few half steps, relative to scores of
-  // at most 1 / total, and 2^-24 by exp.
+  // Softmax: relative to scores of at most 1 / total, NV and a few half steps by
+  // the sum's roundings and by what exp's arguments lose, 2.2 of their own size
+  // (2^-22 covers the rest of it; rows of one large logit and many equal ones
+  // come to two thirds of this bound).
   const float score_error = !scores ? 0.0f : a.sigmoid ? 0x1p-21f : inv * (NV + 10) * 0x1p-23f + 0x1p-22f;
   uint32_t key[NV];
   float probe = 0.0f;  // NaN if any is
